@@ -66,8 +66,9 @@ typedef enum bevpool_status {
 typedef enum bevpool_dtype {
     BEVPOOL_F16 = 0,   /* depth and feat are IEEE binary16                         */
     BEVPOOL_E4M3 = 1,  /* depth and feat are OCP FP8 E4M3 codes, one scale each    */
-    BEVPOOL_NVFP4 = 2  /* feat NVFP4 (E2M1 + E4M3 block scales), depth E4M3:
+    BEVPOOL_NVFP4 = 2, /* feat NVFP4 (E2M1 + E4M3 block scales), depth E4M3:
                           bevpool_forward_nvfp4 only                             */
+    BEVPOOL_BF16 = 3   /* bfloat16: the token operators only                      */
 } bevpool_dtype;
 
 /* Human-readable name of a status code (static string, never NULL). */
@@ -400,6 +401,153 @@ BEVPOOL_API bevpool_status bevpool_probe_l2(int32_t mode, void *buf, size_t byte
 BEVPOOL_API bevpool_status bevpool_probe_gather(const void *feat, int32_t n_rows, int32_t row_bytes,
                                                 const int32_t *rows, int32_t n_points, int32_t ctas_per_sm,
                                                 uint32_t *d_sink, void *stream);
+
+/* ======================================================================
+ * Token operators: temporal attention over BEV cells.
+ *
+ * The pooled cells of a frame are tokens; the queries of new tokens attend
+ * over the keys and values of this and earlier frames, kept in a paged
+ * cache.  Three operators: norms of queries and keys with rotary positions
+ * (forward and backward), the append to the cache, and the attention.
+ *
+ * Conventions, beside those at the top of this file:
+ *   - q, k, v and outputs are [token][head][head_dim] with strides in
+ *     elements for token and head (multiples of 8, so a slice of a fused
+ *     projection's output is taken as it is) and unit stride inside a head;
+ *     pointers are 16-byte aligned.  Output rows must not overlap.
+ *   - dtype is BEVPOOL_F16 or BEVPOOL_BF16.  Sums, norms and softmax
+ *     statistics are FP32; each output is rounded once, except that the
+ *     attention rounds its weights to 16 bits before their product with the
+ *     values.
+ *   - Rotary positions: pair p of a head (rotary_dim / 2 pairs) turns by
+ *     positions[t][axis(p)] * inv_freq[p].  sections[a] pairs belong to axis
+ *     a, in order, so several axes (time, y, x) share a head.  The angle is
+ *     reduced exactly for every int32 position.  Pair p is elements
+ *     (p, p + rotary_dim/2), or (2p, 2p + 1) with interleaved != 0; elements
+ *     from rotary_dim on are left unturned.
+ *   - Norm of a head: x / sqrt(mean(x^2) + eps) * weight.  A NULL weight
+ *     leaves that tensor without a norm (it is only turned).
+ *   - n_tokens = 0 is valid with any pointers, and enqueues nothing but the
+ *     zeroing that is named below.
+ * ====================================================================== */
+
+/*
+ * Norms of queries and keys for each head and their rotary positions, in one
+ * launch.  q_out / k_out may be q / k themselves (same strides).
+ *   head_dim    a multiple of 8 in [32, 256];
+ *   rotary_dim  a multiple of 16 in [16, head_dim];
+ *   q_weight,
+ *   k_weight    device float[head_dim], or NULL (no norm);
+ *   positions   device int32 [n_tokens][n_axes];
+ *   n_axes      1..4;  sections: host int32[n_axes], summing to rotary_dim/2;
+ *   inv_freq    device float[rotary_dim/2], finite.
+ */
+BEVPOOL_API bevpool_status bevpool_qk_norm_rope(
+    bevpool_dtype dtype, const void *q, int64_t q_token_stride, int64_t q_head_stride, const void *k,
+    int64_t k_token_stride, int64_t k_head_stride, int32_t n_tokens, int32_t n_q_heads, int32_t n_k_heads,
+    int32_t head_dim, const float *q_weight, const float *k_weight, float eps, const int32_t *positions,
+    int32_t n_axes, const int32_t *sections, int32_t rotary_dim, const float *inv_freq, int32_t interleaved,
+    void *q_out, int64_t q_out_token_stride, int64_t q_out_head_stride, void *k_out, int64_t k_out_token_stride,
+    int64_t k_out_head_stride, void *stream);
+
+/* Device workspace (bytes, 256-byte aligned) of bevpool_qk_norm_rope_backward
+ * on the current device; 0 for invalid sizes. */
+BEVPOOL_API size_t bevpool_qk_norm_rope_backward_workspace_size(int32_t n_tokens, int32_t n_q_heads,
+                                                                int32_t n_k_heads, int32_t head_dim);
+
+/*
+ * Gradients of bevpool_qk_norm_rope for q, k and the weights, from the
+ * gradients of its outputs and its inputs (the norm is recomputed).
+ *   dq_out, dk_out      gradients of the outputs, dtype, with strides;
+ *   dq, dk              dtype, with strides (may be dq_out / dk_out);
+ *   dq_weight, dk_weight  device float[head_dim]: written, not added to;
+ *                       NULL exactly where the weight is NULL.
+ * Sums over tokens and heads run in a fixed order (no atomics): results are
+ * deterministic.  n_tokens = 0 zeroes the weights' gradients.
+ */
+BEVPOOL_API bevpool_status bevpool_qk_norm_rope_backward(
+    bevpool_dtype dtype, const void *dq_out, int64_t dq_out_token_stride, int64_t dq_out_head_stride,
+    const void *dk_out, int64_t dk_out_token_stride, int64_t dk_out_head_stride, const void *q,
+    int64_t q_token_stride, int64_t q_head_stride, const void *k, int64_t k_token_stride, int64_t k_head_stride,
+    int32_t n_tokens, int32_t n_q_heads, int32_t n_k_heads, int32_t head_dim, const float *q_weight,
+    const float *k_weight, float eps, const int32_t *positions, int32_t n_axes, const int32_t *sections,
+    int32_t rotary_dim, const float *inv_freq, int32_t interleaved, void *dq, int64_t dq_token_stride,
+    int64_t dq_head_stride, void *dk, int64_t dk_token_stride, int64_t dk_head_stride, float *dq_weight,
+    float *dk_weight, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Append the keys and values of new tokens to a paged cache, with the keys'
+ * norm and rotation on the way; optionally the same for the queries of the
+ * tokens (q NULL: none), all in one launch.
+ *
+ * Request b holds kv_len[b] keys, its new tokens included; its new tokens are
+ * rows cu_q[b] .. cu_q[b+1]-1.  Token i of them (from 0) goes to place
+ * kv_len[b] - q_len + i: slot place % page_size of page
+ * block_table[b][place / page_size].  A place below 0 or past the table, a
+ * page outside [0, n_pages) and tokens from cu_q[n_seqs] on write nothing to
+ * the cache (their q rows are still written).
+ *   cache_dtype  dtype, or BEVPOOL_E4M3: codes of value / k_scale (v_scale),
+ *                rounded to nearest even, saturating at +-448 (NaN stays NaN);
+ *   k_cache, v_cache  device [n_pages] pages; slot s, head h of page p starts
+ *                at p*page_stride + s*slot_stride + h*head_stride elements
+ *                (strides in elements, multiples of 16 bytes);
+ *   page_size    a power of two in [16, 256];
+ *   block_table  device int32 [n_seqs][table_pages];
+ *   kv_len       device int32 [n_seqs];  cu_q: device int32 [n_seqs + 1],
+ *                ascending from 0;
+ *   k_scale, v_scale  finite and > 0; used with BEVPOOL_E4M3 only.
+ * The other arguments are those of bevpool_qk_norm_rope.
+ */
+BEVPOOL_API bevpool_status bevpool_kv_append(
+    bevpool_dtype dtype, bevpool_dtype cache_dtype, const void *k, int64_t k_token_stride, int64_t k_head_stride,
+    const void *v, int64_t v_token_stride, int64_t v_head_stride, const void *q, int64_t q_token_stride,
+    int64_t q_head_stride, int32_t n_tokens, int32_t n_q_heads, int32_t n_k_heads, int32_t head_dim,
+    const float *q_weight, const float *k_weight, float eps, const int32_t *positions, int32_t n_axes,
+    const int32_t *sections, int32_t rotary_dim, const float *inv_freq, int32_t interleaved, void *q_out,
+    int64_t q_out_token_stride, int64_t q_out_head_stride, void *k_cache, void *v_cache, int64_t page_stride,
+    int64_t slot_stride, int64_t head_stride, int32_t n_pages, int32_t page_size, const int32_t *block_table,
+    int32_t table_pages, const int32_t *kv_len, const int32_t *cu_q, int32_t n_seqs, float k_scale, float v_scale,
+    void *stream);
+
+/* Device workspace (bytes, 256-byte aligned) of bevpool_paged_attention with
+ * these sizes on the current device; 0 where none is needed or a size is
+ * invalid. */
+BEVPOOL_API size_t bevpool_paged_attention_workspace_size(int32_t n_seqs, int32_t n_tokens, int32_t n_q_heads,
+                                                          int32_t n_k_heads, int32_t head_dim, int32_t max_q_len,
+                                                          int32_t max_kv_len);
+
+/*
+ * Attention of new tokens over the paged cache:
+ *     s_j = scale * q . k_j,   lse = log sum_j exp(s_j),
+ *     out = sum_j exp(s_j - lse) * v_j
+ * over the keys j a token sees.  Query head h reads key head
+ * h / (n_q_heads / n_k_heads).  Token i of request b stands at place
+ * pos = kv_len[b] - q_len + i and sees the keys j with 0 <= j < kv_len[b], on
+ * a page inside [0, n_pages), with j <= pos if causal, and j > pos - window
+ * if window > 0 (causal only).  Keys it does not see never reach its result,
+ * whatever bits their slots hold.  A token that sees none gets out = 0 and
+ * lse = -inf.
+ *   head_dim     64 or 128;  n_q_heads a multiple of n_k_heads;
+ *   cache_dtype  dtype, or BEVPOOL_E4M3 codes: key = code * k_scale, value =
+ *                code * v_scale;
+ *   scale        finite and > 0;
+ *   max_q_len,
+ *   max_kv_len   host bounds of the requests' new tokens and keys.  Tokens of
+ *                a request past max_q_len are not computed; keys past
+ *                max_kv_len (or past the table) are not seen;
+ *   out          dtype, with strides; lse: device float [n_tokens][n_q_heads]
+ *                or NULL.
+ * The cache arguments are those of bevpool_kv_append.  Results are
+ * deterministic.
+ */
+BEVPOOL_API bevpool_status bevpool_paged_attention(
+    bevpool_dtype dtype, bevpool_dtype cache_dtype, const void *q, int64_t q_token_stride, int64_t q_head_stride,
+    const void *k_cache, const void *v_cache, int64_t page_stride, int64_t slot_stride, int64_t head_stride,
+    int32_t n_pages, int32_t page_size, const int32_t *block_table, int32_t table_pages, const int32_t *kv_len,
+    const int32_t *cu_q, int32_t n_seqs, int32_t n_tokens, int32_t n_q_heads, int32_t n_k_heads, int32_t head_dim,
+    int32_t max_q_len, int32_t max_kv_len, float scale, int32_t causal, int32_t window, float k_scale,
+    float v_scale, void *out, int64_t out_token_stride, int64_t out_head_stride, float *lse, void *workspace,
+    size_t workspace_bytes, void *stream);
 
 #ifdef __cplusplus
 }
