@@ -18,12 +18,25 @@ struct AttnArgs {
     float v_scale;
     int32_t causal, window;
     float *lse;
-    void *workspace;
+    float *part_o;                    // [n_seqs][Hk][n_chunks][rows][D], of n_chunks > 1
+    float *part_ml;                   // [n_seqs][Hk][n_chunks][rows][2]: maximum (base 2), sum
     cudaStream_t stream;
 };
+
+// How one call is laid out, from its sizes alone.
+struct AttnPlan {
+    int32_t few;              // 1: at most 16 query rows a request and key head
+    int32_t rows;             // query rows a request and key head: max_q_len * G
+    int32_t chunk;            // keys of one CTA
+    int32_t n_chunks;         // CTAs along the keys; above 1 their results are joined by a second kernel
+};
+AttnPlan attention_plan(int32_t n_seqs, int32_t Hq, int32_t Hk, int32_t max_q_len, int32_t max_kv_len, int32_t window);
+cudaError_t launch_attend_few(const AttnArgs &a, const AttnPlan &pl);      // attend_few.cu
+cudaError_t launch_attend_join(const AttnArgs &a, const AttnPlan &pl);     // attend_join.cu
+
 size_t attention_workspace_bytes(int32_t n_seqs, int32_t T, int32_t Hq, int32_t Hk, int32_t D, int32_t max_q_len,
                                  int32_t max_kv_len);
-cudaError_t launch_paged_attention(const AttnArgs &a);
+cudaError_t launch_paged_attention(const AttnArgs &a, void *workspace);
 
 // ---------------------------------------------------------------- device
 
@@ -52,6 +65,26 @@ __device__ __forceinline__ void seen_keys(const AttnArgs &a, const Request &r, i
     const int32_t pos = r.pos0 + i;
     *hi = a.causal ? min(max(pos + 1, 0), r.kv_len) : r.kv_len;
     *lo = a.window > 0 ? static_cast<int32_t>(max(static_cast<int64_t>(pos) - a.window + 1, static_cast<int64_t>(0))) : 0;
+}
+
+// Where the keys of a request's chunks start, and how many chunks it has (one
+// at least: it writes the rows that see nothing).
+constexpr int32_t kChunkAlign = 64;
+__device__ __forceinline__ int32_t chunks_of(const AttnArgs &a, const Request &r, int32_t chunk, int32_t n_chunks,
+                                             int32_t *base) {
+    int32_t lo, hi, x;
+    seen_keys(a, r, 0, &lo, &x);
+    seen_keys(a, r, max(r.q_rows - 1, 0), &x, &hi);
+    *base = min(lo, hi) / kChunkAlign * kChunkAlign;
+    const int64_t n = (static_cast<int64_t>(hi) - *base + chunk - 1) / chunk;
+    return static_cast<int32_t>(min(max(n, static_cast<int64_t>(1)), static_cast<int64_t>(n_chunks)));
+}
+
+// 2^x, 2^-inf = 0; results below 2^-126 are zero.
+__device__ __forceinline__ float pow2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 
 // E elements of a cache row as FP32.
@@ -110,6 +143,55 @@ __device__ void attend_row(const AttnArgs &a, int b, int hk, const float *q, int
             for (int i = 0; i < E; ++i) acc[i] = fmaf(acc[i], r, p * v[i]);
         }
     }
+}
+
+// The keys [c0, c1) of one row again, by attend_row: *m, *l, acc (lane l:
+// elements l*E ..).
+template <typename T, bool E4M3, int D>
+__device__ __noinline__ void redo_row(const AttnArgs &a, const Request &r, int b, int hk, int i, int h, int32_t c0,
+                                      int32_t c1, float *m, float *l, float *acc) {
+    constexpr int E = D / 32;
+    const int lane = threadIdx.x & 31;
+    const T *qp = static_cast<const T *>(a.q.p) + static_cast<int64_t>(r.q0 + i) * a.q.token_stride + h * a.q.head_stride +
+                  lane * E;
+    float q[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        q[e] = static_cast<float>(qp[e]);
+        acc[e] = 0.0f;
+    }
+    *m = -INFINITY;
+    *l = 0.0f;
+    int32_t lo, hi;
+    seen_keys(a, r, i, &lo, &hi);
+    attend_row<T, E4M3, D>(a, b, hk, q, max(lo, c0), min(hi, c1), m, l, acc);
+}
+
+__device__ __forceinline__ int64_t part_row(const AttnArgs &a, const AttnPlan &pl, int b, int hk, int chunk, int row) {
+    return ((static_cast<int64_t>(b) * a.Hk + hk) * pl.n_chunks + chunk) * pl.rows + row;
+}
+
+// The end of a row, held by a warp (lane l: elements l*E ..): to out and lse
+// where the request has one chunk, else to the chunk's partial results.
+template <typename T, int E>
+__device__ __forceinline__ void store_row(const AttnArgs &a, const AttnPlan &pl, const Request &r, int b, int hk, int i,
+                                          int h, int row, int chunk, int n_used, float m, float l, const float *acc) {
+    const int lane = threadIdx.x & 31;
+    if (n_used > 1) {
+        const int64_t at = part_row(a, pl, b, hk, chunk, row);
+        float *o = a.part_o + at * (32 * E) + lane * E;
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] = acc[e];
+        if (lane == 0) *reinterpret_cast<float2 *>(a.part_ml + at * 2) = make_float2(m, l);
+        return;
+    }
+    const int64_t t = r.q0 + i;
+    const bool some = !(l == 0.0f);
+    const float inv = some ? a.v_scale / l : 0.0f;
+    T *op = static_cast<T *>(a.out.p) + t * a.out.token_stride + h * a.out.head_stride + lane * E;
+#pragma unroll
+    for (int e = 0; e < E; e += 2) *reinterpret_cast<uint32_t *>(op + e) = pack2<T>(acc[e] * inv, acc[e + 1] * inv);
+    if (a.lse && lane == 0) a.lse[t * a.Hq + h] = some ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
 }
 
 }  // namespace bevpool

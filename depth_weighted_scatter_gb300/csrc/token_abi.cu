@@ -303,9 +303,8 @@ bevpool_status bevpool_paged_attention(
     a.causal = causal != 0;
     a.window = window;
     a.lse = lse;
-    a.workspace = workspace;
     a.stream = static_cast<cudaStream_t>(stream);
-    return cuda_status(launch_paged_attention(a));
+    return cuda_status(launch_paged_attention(a, workspace));
 }
 
 }  // extern "C"
