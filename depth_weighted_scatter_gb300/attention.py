@@ -44,11 +44,13 @@ _lib.bevpool_qk_norm_rope_backward.restype = ctypes.c_int
 _lib.bevpool_kv_append.argtypes = ([_dt, _dt] + _rows * 3 + [_i32] * 4 + [_vp, _vp, _f32] + _rotary + _rows
                                    + [_vp, _vp] + _pages + [_f32, _f32, _vp])
 _lib.bevpool_kv_append.restype = ctypes.c_int
-_lib.bevpool_paged_attention_workspace_size.argtypes = [_i32] * 7
+_lib.bevpool_paged_attention_workspace_size.argtypes = [_i32] * 8
 _lib.bevpool_paged_attention_workspace_size.restype = _sz
 _lib.bevpool_paged_attention.argtypes = ([_dt, _dt] + _rows + [_vp, _vp] + _pages + [_i32] * 6
                                          + [_f32, _i32, _i32, _f32, _f32] + _rows + [_vp, _vp, _sz, _vp])
 _lib.bevpool_paged_attention.restype = ctypes.c_int
+_lib.bevpool_attention_timeouts.argtypes = [_vp]
+_lib.bevpool_attention_timeouts.restype = ctypes.c_int
 
 
 # ---------------------------------------------------------------- raw C entry points (arguments as in the header)
@@ -70,13 +72,22 @@ def bevpool_kv_append(*args) -> int:
 
 
 def bevpool_paged_attention_workspace_size(n_seqs: int, n_tokens: int, n_q_heads: int, n_k_heads: int, head_dim: int,
-                                           max_q_len: int, max_kv_len: int) -> int:
+                                           max_q_len: int, max_kv_len: int, window: int) -> int:
     return _lib.bevpool_paged_attention_workspace_size(n_seqs, n_tokens, n_q_heads, n_k_heads, head_dim, max_q_len,
-                                                       max_kv_len)
+                                                       max_kv_len, window)
 
 
 def bevpool_paged_attention(*args) -> int:
     return _lib.bevpool_paged_attention(*args)
+
+
+def bevpool_attention_timeouts() -> int:
+    """Bounded waits of the attention kernels that ran out so far (0 unless the device misbehaves); synchronises."""
+    n = _i64(0)
+    st = _lib.bevpool_attention_timeouts(ctypes.byref(n))
+    if st != BEVPOOL_OK:
+        raise BevpoolError(st, "bevpool_attention_timeouts")
+    return n.value
 
 
 # ---------------------------------------------------------------- tensor helpers
@@ -280,7 +291,7 @@ def paged_attention(q, k_cache, v_cache, block_table, kv_len, cu_q, *, max_q_len
     out = _out("out", out, q, Hq)
     lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device) if return_lse else None
     if workspace is None:
-        n = bevpool_paged_attention_workspace_size(pages[-1], T, Hq, Hk, D, max_q_len, max_kv_len)
+        n = bevpool_paged_attention_workspace_size(pages[-1], T, Hq, Hk, D, max_q_len, max_kv_len, window)
         workspace = torch.empty(n, dtype=torch.uint8, device=q.device) if n else None
     st = bevpool_paged_attention(
         _DTYPES[q.dtype], cache_dtype, *qa, *ptrs, *pages, T, Hq, Hk, D, max_q_len, max_kv_len,

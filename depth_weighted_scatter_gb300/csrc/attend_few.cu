@@ -13,8 +13,7 @@
 // E4M3 codes stay codes in shared memory and are widened in registers.  For
 // K a thread's four consecutive codes serve as its four places along the
 // product's inner axis (Q is loaded in the same order); for V a transposed
-// load of 2-byte units yields two columns at once.  P and V are then fp16
-// whatever the heads' type: fp16 holds every code.
+// load of 2-byte units yields two columns at once.
 #include "paged_attention.cuh"
 
 namespace bevpool {
@@ -60,18 +59,6 @@ __device__ __forceinline__ void mma(float *c, const uint32_t *a, uint32_t b0, ui
                      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Two E4M3 codes (low 16 bits) as two 16-bit values.
-template <typename T>
-__device__ __forceinline__ uint32_t widen2(uint32_t codes) {
-    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(codes), __NV_E4M3);
-    if constexpr (std::is_same<T, __half>::value) {
-        return *reinterpret_cast<const uint32_t *>(&h);
-    } else {
-        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
-        return pack2<T>(f.x, f.y);
-    }
-}
-
 template <bool E4M3, int D>
 struct FewShape {
     static constexpr int EB = E4M3 ? 1 : 2;
@@ -92,7 +79,6 @@ template <typename T, bool E4M3, int D>
 __global__ void __launch_bounds__(kFewWarps * 32, 2)
 k_attend_few(AttnArgs a, AttnPlan pl) {
     using S = FewShape<E4M3, D>;
-    using P = typename std::conditional<E4M3, __half, T>::type;            // type of P and V in their product
     constexpr int KS = D / 16, NT = D / 8, KG = S::KT / 16;                // k steps of S, columns tiles of O, 16-key groups
     extern __shared__ __align__(128) uint8_t smem[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, qd = lane & 3;
@@ -100,7 +86,7 @@ k_attend_few(AttnArgs a, AttnPlan pl) {
     const Request r = request_of(a, b);
     if (r.q_rows == 0) return;
     int32_t base;
-    const int n_used = chunks_of(a, r, pl.chunk, pl.n_chunks, &base);
+    const int n_used = chunks_of(a, r, pl.chunk, pl.n_chunks, pl.align, &base);
     if (static_cast<int>(blockIdx.x) >= n_used) return;
     const int rows = r.q_rows * a.G;
 
@@ -268,8 +254,8 @@ k_attend_few(AttnArgs a, AttnPlan pl) {
                 const float p2 = pow2(s[2 * x + n][2] - from[1]), p3 = pow2(s[2 * x + n][3] - from[1]);
                 l[0] += p0 + p1;
                 l[1] += p2 + p3;
-                pf[2 * n] = pack2<P>(p0, p1);
-                pf[2 * n + 1] = pack2<P>(p2, p3);
+                pf[2 * n] = pack2<T>(p0, p1);
+                pf[2 * n + 1] = pack2<T>(p2, p3);
             }
             const int row = 16 * x + (lane & 15), piece = lane >> 4;
 #pragma unroll
@@ -280,13 +266,13 @@ k_attend_few(AttnArgs a, AttnPlan pl) {
 #pragma unroll
                     for (int y = 0; y < 2; ++y) {
                         const uint32_t w0 = w[2 * y], w1 = w[2 * y + 1];
-                        mma<P>(o[2 * (c + y)], pf, widen2<P>(__byte_perm(w0, 0, 0x4420)), widen2<P>(__byte_perm(w1, 0, 0x4420)));
-                        mma<P>(o[2 * (c + y) + 1], pf, widen2<P>(__byte_perm(w0, 0, 0x4431)),
-                               widen2<P>(__byte_perm(w1, 0, 0x4431)));
+                        mma<T>(o[2 * (c + y)], pf, widen2<T>(__byte_perm(w0, 0, 0x4420)), widen2<T>(__byte_perm(w1, 0, 0x4420)));
+                        mma<T>(o[2 * (c + y) + 1], pf, widen2<T>(__byte_perm(w0, 0, 0x4431)),
+                               widen2<T>(__byte_perm(w1, 0, 0x4431)));
                     }
                 } else {
-                    mma<P>(o[c], pf, w[0], w[1]);
-                    mma<P>(o[c + 1], pf, w[2], w[3]);
+                    mma<T>(o[c], pf, w[0], w[1]);
+                    mma<T>(o[c + 1], pf, w[2], w[3]);
                 }
             }
         }

@@ -15,7 +15,7 @@ k_attend_join(AttnArgs a, AttnPlan pl) {
     const int lane = threadIdx.x & 31, hk = blockIdx.y, b = blockIdx.z;
     const Request r = request_of(a, b);
     int32_t base;
-    const int n = chunks_of(a, r, pl.chunk, pl.n_chunks, &base);
+    const int n = chunks_of(a, r, pl.chunk, pl.n_chunks, pl.align, &base);
     if (n == 1) return;
     const int rows = r.q_rows * a.G;
     grid_dep_wait();
@@ -31,7 +31,8 @@ k_attend_join(AttnArgs a, AttnPlan pl) {
         for (int c = 0; c < n; ++c) {
             const int64_t p = at + static_cast<int64_t>(c) * pl.rows;
             const float2 ml = *reinterpret_cast<const float2 *>(a.part_ml + p * 2);
-            const float f = exp2f(ml.x - from);
+            if (ml.y == 0.0f) continue;                    // nothing seen there, and no O written
+            const float f = pow2(ml.x - from);
             l = fmaf(ml.y, f, l);
             const float *o = a.part_o + p * D + lane * E;
 #pragma unroll

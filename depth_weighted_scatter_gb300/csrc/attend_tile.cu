@@ -1,0 +1,618 @@
+// attend_tile.cu -- attention of many query rows on the tcgen05 tensor cores.
+//
+// The rows of a request and key head are its new tokens times the query heads
+// of the group, so that a tile of 128 rows is full even for short chunks and
+// each key is read once for the whole group.  A CTA holds two row tiles and
+// walks the keys in blocks of 128:
+//   warps 0-3, 4-7   softmax of tile 0, 1 (one row a thread): S from tensor
+//                    memory, running maximum and sum, P (16 bits) back over S
+//   warp 8           issues the products: S = Q K^T (both from shared memory)
+//                    and O += P V (P from tensor memory), O in tensor memory
+//   warp 9           loads K and V: a TMA box for each page and 64 elements of
+//                    the head, into a ring of 128-byte-swizzled blocks
+//   warps 9-12       (E4M3 cache instead) load codes, widen them to 16 bits and
+//                    store them in the same layout
+// While one tile is in its softmax the tensor core works on the other.
+//
+// Bound by the tensor core at head_dim 128 (two products of 128 x 128 x 128 a
+// tile and block, 512 cycles each, against 512 cycles of exponentials), by
+// tensor core and exponentials alike at 64.
+//
+// O is only rescaled when a row's maximum has grown by more than 2^8 since the
+// scale in use was set: P then stays below 2^8 and FP32 sums lose nothing.
+// The completion of S(j+1) also says that O += P V of block j is done, as they
+// are issued in that order: the softmax may then touch O.
+//
+// A wait that runs out (it never should) ends the CTA: its rows become NaN and
+// bevpool_attention_timeouts counts it.
+#include <cuda.h>
+
+#include "paged_attention.cuh"
+#include "tcgen05.cuh"
+
+namespace bevpool {
+
+__device__ unsigned long long g_attention_timeouts;
+
+namespace {
+
+constexpr int kBlock = 128;                // keys of a block
+constexpr int kTileRows = 128;
+constexpr float kGrow = 8.0f;              // log2 of the growth that P may show
+
+template <bool E4M3, int D>
+struct TileShape {
+    static constexpr int LOADERS = E4M3 ? 4 : 1;                           // warps
+    static constexpr int THREADS = (9 + LOADERS) * 32;
+    static constexpr int HALVES = D / 64;                                  // 128-byte columns of a block
+    static constexpr int BLOCK_BYTES = kBlock * D * 2;
+    static constexpr int STAGES = D == 128 ? 4 : 6;                        // K and V blocks in turn
+    static constexpr int Q_BYTES = kTileRows * D * 2;
+    static constexpr int SMEM = 1024 + 2 * Q_BYTES + STAGES * BLOCK_BYTES; // 1024: alignment
+};
+
+struct TileBars {                          // shared memory
+    uint64_t full[6], empty[6];            // ring
+    uint64_t q_full[2], s_full[2], p_full[2], o_full[2], drain;
+    uint32_t tmem, failed;
+};
+
+// What a row tile of this CTA sees: blocks [b0, b1) of the chunk.
+struct TileRange {
+    int32_t b0, b1;
+};
+
+__device__ __forceinline__ TileRange tile_range(const AttnArgs &a, const Request &r, int32_t row0, int32_t rows, int32_t c0,
+                                                int64_t c1) {
+    if (row0 >= rows) return {0, 0};
+    int32_t lo, hi, x;
+    seen_keys(a, r, row0 / a.G, &lo, &x);
+    seen_keys(a, r, (min(row0 + kTileRows, rows) - 1) / a.G, &x, &hi);
+    lo = max(lo, c0);
+    hi = static_cast<int32_t>(min(static_cast<int64_t>(hi), c1));
+    if (hi <= lo) return {0, 0};
+    return {lo / kBlock, (hi - 1) / kBlock + 1};
+}
+
+template <typename T, bool E4M3, int D>
+__global__ void __launch_bounds__(TileShape<E4M3, D>::THREADS, 1)
+k_attend_tile(AttnArgs a, AttnPlan pl, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
+    using S = TileShape<E4M3, D>;
+    extern __shared__ uint8_t raw_smem[];
+    __shared__ TileBars bars;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+
+    // x: row tiles (the longest first) by key heads; y: chunks; z: requests.
+    const int hk = blockIdx.x % a.Hk, b = blockIdx.z, chunk = blockIdx.y;
+    const Request r = request_of(a, b);
+    const int32_t rows = r.q_rows * a.G;
+    const int32_t row0 = static_cast<int32_t>(gridDim.x / a.Hk - 1 - blockIdx.x / a.Hk) * (2 * kTileRows);
+    if (row0 >= rows) return;
+    int32_t base;
+    const int n_used = chunks_of(a, r, pl.chunk, pl.n_chunks, pl.align, &base);
+    if (chunk >= n_used) return;
+    const int32_t c0 = base + chunk * pl.chunk;
+    const int64_t c1 = static_cast<int64_t>(c0) + pl.chunk;
+    const TileRange t0 = tile_range(a, r, row0, rows, c0, c1), t1 = tile_range(a, r, row0 + kTileRows, rows, c0, c1);
+    const int32_t j0 = t0.b1 == 0 ? t1.b0 : t1.b1 == 0 ? t0.b0 : min(t0.b0, t1.b0);
+    const int32_t j1 = max(t0.b1, t1.b1);
+    const int32_t *table = a.pg.block_table + static_cast<int64_t>(b) * a.pg.table_pages;
+
+    const uint32_t smem = (shared_addr(raw_smem) + 1023) & ~1023u;
+    const uint32_t q_smem = smem, ring = smem + 2 * S::Q_BYTES;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < S::STAGES; ++i) {
+            bar_init(shared_addr(&bars.full[i]), E4M3 ? S::LOADERS * 32 : 1);
+            bar_init(shared_addr(&bars.empty[i]), 1);
+        }
+        for (int t = 0; t < 2; ++t) {
+            bar_init(shared_addr(&bars.q_full[t]), kTileRows);
+            bar_init(shared_addr(&bars.s_full[t]), 1);
+            bar_init(shared_addr(&bars.p_full[t]), kTileRows);
+            bar_init(shared_addr(&bars.o_full[t]), 1);
+        }
+        bar_init(shared_addr(&bars.drain), 1);
+        bars.failed = 0;
+        bar_init_fence();
+    }
+    if (warp == 8) tmem_alloc<512>(shared_addr(&bars.tmem));
+    tmem_fence_before();
+    __syncthreads();
+    tmem_fence_after();
+    const uint32_t tmem = bars.tmem;
+    bool ok = true;
+
+    if (warp < 8) {
+        // ------------------------------------------------------------ softmax
+        const int t = warp >> 2, tid = threadIdx.x & 127;
+        const TileRange tr = t == 0 ? t0 : t1;
+        const int32_t tile0 = row0 + t * kTileRows;
+        if (tr.b1 > tr.b0) {
+            constexpr int CPR = D / 8;                                     // 16-byte pieces of a row
+            for (int x = tid; x < kTileRows * CPR; x += kTileRows) {
+                const int row = x / CPR, c = x % CPR;
+                const int32_t gr = tile0 + row;
+                uint4 w = make_uint4(0, 0, 0, 0);
+                if (gr < rows)
+                    w = *reinterpret_cast<const uint4 *>(static_cast<const T *>(a.q.p) +
+                                                         static_cast<int64_t>(r.q0 + gr / a.G) * a.q.token_stride +
+                                                         (hk * a.G + gr % a.G) * a.q.head_stride + c * 8);
+                const uint32_t d = q_smem + t * S::Q_BYTES + (c >> 3) * (kTileRows * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4);
+                asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(d), "r"(w.x), "r"(w.y), "r"(w.z), "r"(w.w) : "memory");
+            }
+            fence_shared_async();
+            bar_arrive(shared_addr(&bars.q_full[t]));
+        }
+        const int32_t row = tile0 + tid;
+        const bool used = row < rows;
+        int32_t lo = 0, hi = INT32_MAX;                                    // a place past the last row sees all, and is not kept
+        if (used) seen_keys(a, r, row / a.G, &lo, &hi);
+        const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        const uint32_t s_mem = tmem + lanes + t * kBlock, o_mem = tmem + lanes + 2 * kBlock + t * D;
+        float m = -INFINITY;                                               // the scale in use (base 2)
+        uint64_t sum = pair(0.0f, 0.0f);
+        // Groups of 16 keys that lie on no page, one bit each; read a block ahead.
+        auto holes_of = [&](int32_t j) {
+            bool hole = false;
+            if (lane < kBlock / 16) {
+                const int32_t k = j * kBlock + lane * 16;
+                if (k < r.kv_len) {
+                    const int32_t p = table[k >> a.pg.page_shift];
+                    hole = p < 0 || p >= a.pg.n_pages;
+                }
+            }
+            return hole;
+        };
+        bool hole = tr.b1 > tr.b0 ? holes_of(tr.b0) : false;
+        uint32_t phase = 0;
+        for (int32_t j = tr.b0; j < tr.b1; ++j, phase ^= 1) {
+            const uint32_t holes = __ballot_sync(0xffffffffu, hole);
+            if (j + 1 < tr.b1) hole = holes_of(j + 1);
+            ok = bar_wait(shared_addr(&bars.s_full[t]), phase);
+            if (!__all_sync(0xffffffffu, ok)) {
+                ok = false;
+                break;
+            }
+            tmem_fence_after();
+            uint32_t s[kBlock];
+#pragma unroll
+            for (int c = 0; c < kBlock; c += 32) tmem_ld32(s_mem + c, s + c);
+            tmem_wait_ld();
+            const int32_t k0 = j * kBlock;
+            if (!__all_sync(0xffffffffu, holes == 0 && lo <= k0 && hi - kBlock >= k0)) {
+                const int32_t from = lo - k0, to = hi - k0;
+#pragma unroll
+                for (int c = 0; c < kBlock; ++c)
+                    if (c < from || c >= to || ((holes >> (c / 16)) & 1)) s[c] = 0xff800000u;      // -inf
+            }
+            float mx[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) mx[x] = __uint_as_float(s[x]);
+#pragma unroll
+            for (int c = 4; c < kBlock; c += 8) {
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    mx[x] = fmaxf(mx[x], __uint_as_float(s[c + x]));
+                    if (c + 4 < kBlock) mx[x] = fmaxf(mx[x], __uint_as_float(s[c + 4 + x]));
+                }
+            }
+            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
+            const bool grown = top > m + kGrow || (m == -INFINITY && top > m);
+            if (__any_sync(0xffffffffu, grown)) {
+                const float mn = grown ? top : m;
+                const float f = grown ? pow2(m - mn) : 1.0f;               // m = -inf: 0
+                m = mn;
+                if (j > tr.b0) {
+                    const uint64_t f2 = pair(f, f);
+                    sum = mul2(sum, f2);
+#pragma unroll
+                    for (int c = 0; c < D; c += 32) {
+                        uint32_t o[32];
+                        tmem_ld32(o_mem + c, o);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
+                        tmem_st32(o_mem + c, o);
+                    }
+                }
+            }
+            const float base2 = m == -INFINITY ? 0.0f : -m;
+            const uint64_t scale2 = pair(a.scale_log2, a.scale_log2), from2 = pair(base2, base2);
+            uint64_t part = pair(0.0f, 0.0f);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint32_t p[32];
+#pragma unroll
+                for (int c = 0; c < 32; ++c) {
+                    const int at = h * 64 + 2 * c;
+                    const uint64_t e = fma2(pair(__uint_as_float(s[at]), __uint_as_float(s[at + 1])), scale2, from2);
+                    float x, y;
+                    unpair(e, &x, &y);
+                    x = pow2(x);
+                    y = pow2(y);
+                    if (c & 1)
+                        part = add2(part, pair(x, y));
+                    else
+                        sum = add2(sum, pair(x, y));
+                    p[c] = pack2<T>(x, y);
+                }
+                tmem_st32(s_mem + h * 32, p);
+            }
+            sum = add2(sum, part);
+            tmem_wait_st();
+            tmem_fence_before();
+            bar_arrive(shared_addr(&bars.p_full[t]));
+        }
+        float l, l1;
+        unpair(sum, &l, &l1);
+        l += l1;
+        if (ok && tr.b1 > tr.b0) ok = bar_wait(shared_addr(&bars.o_full[t]), 0);
+        if (!__all_sync(0xffffffffu, ok)) {
+            ok = false;
+        } else {
+            tmem_fence_after();
+            // O to its row: two 16-byte stores for each 32-byte sector of a row.
+            const bool some = !(l == 0.0f);
+            const int64_t token = r.q0 + (used ? row / a.G : 0);
+            const int32_t h = hk * a.G + (used ? row % a.G : 0);
+            const float inv = some ? a.v_scale / l : 0.0f;
+            T *op = static_cast<T *>(a.out.p) + token * a.out.token_stride + h * a.out.head_stride;
+            const int64_t part = n_used > 1 && used ? part_row(a, pl, b, hk, chunk, row) : 0;
+            bool fine = l - l == 0.0f;
+            if (tr.b1 > tr.b0) {
+#pragma unroll
+                for (int c = 0; c < D; c += 32) {
+                    uint32_t o[32];
+                    tmem_ld32(o_mem + c, o);
+                    tmem_wait_ld();
+                    float f[32];
+#pragma unroll
+                    for (int x = 0; x < 32; ++x) {
+                        f[x] = __uint_as_float(o[x]);
+                        fine = fine && f[x] - f[x] == 0.0f;
+                    }
+                    if (used && n_used > 1) {
+#pragma unroll
+                        for (int x = 0; x < 32; x += 4)
+                            *reinterpret_cast<float4 *>(a.part_o + part * D + c + x) =
+                                make_float4(f[x], f[x + 1], f[x + 2], f[x + 3]);
+                    } else if (used) {
+#pragma unroll
+                        for (int x = 0; x < 32; ++x) f[x] = some ? f[x] * inv : 0.0f;
+#pragma unroll
+                        for (int x = 0; x < 32; x += 8) *reinterpret_cast<uint4 *>(op + c + x) = pack8<T>(f + x);
+                    }
+                    __syncwarp();
+                }
+            } else if (used && n_used == 1) {
+#pragma unroll
+                for (int c = 0; c < D; c += 8) *reinterpret_cast<uint4 *>(op + c) = make_uint4(0, 0, 0, 0);
+            }
+            if (used) {
+                if (n_used > 1)
+                    *reinterpret_cast<float2 *>(a.part_ml + part * 2) = make_float2(m, l);
+                else if (a.lse)
+                    a.lse[token * a.Hq + h] = some ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+            }
+            // An infinity or NaN may come from a key in the block that the row
+            // does not see (its weight 0 times the value): such rows are taken
+            // again element by element.
+            uint32_t again = __ballot_sync(0xffffffffu, used && !fine);
+            __syncwarp();
+            while (again) {
+                const int x = __ffs(again) - 1;
+                again &= again - 1;
+                const int32_t rr = tile0 + (warp & 3) * 32 + x;
+                float acc[D / 32], m1, s1;
+                redo_row<T, E4M3, D>(a, r, b, hk, rr / a.G, hk * a.G + rr % a.G, c0,
+                                     static_cast<int32_t>(min(c1, static_cast<int64_t>(r.kv_len))), &m1, &s1, acc);
+                store_row<T, D / 32>(a, pl, r, b, hk, rr / a.G, hk * a.G + rr % a.G, rr, chunk, n_used, m1, s1, acc);
+            }
+        }
+    } else if (warp == 8) {
+        // ------------------------------------------------------------ products
+        constexpr int format = std::is_same<T, __half>::value ? 0 : 1;
+        constexpr uint32_t s_desc = mma_desc(format, kBlock, false), o_desc = mma_desc(format, D, true);
+        auto in = [&](int t, int32_t j) { return t == 0 ? j >= t0.b0 && j < t0.b1 : j >= t1.b0 && j < t1.b1; };
+        auto scores = [&](int t, uint32_t k_smem) {
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+                const uint32_t off = (k >> 2) * (kBlock * 128) + (k & 3) * 32;
+                mma_ss(tmem + t * kBlock, operand_desc(q_smem + t * S::Q_BYTES + off, 16, 1024),
+                       operand_desc(k_smem + off, 16, 1024), s_desc, k > 0);
+            }
+            mma_commit(shared_addr(&bars.s_full[t]));
+        };
+        uint32_t at = 0, lap = 0;                                          // place in the ring and its phase
+        auto next = [&]() {
+            if (++at == S::STAGES) {
+                at = 0;
+                lap ^= 1;
+            }
+        };
+        uint32_t p_phase[2] = {0, 0};
+        if (j1 > j0) {
+            for (int t = 0; t < 2 && ok; ++t)
+                if ((t == 0 ? t0.b1 : t1.b1) > 0) ok = bar_wait(shared_addr(&bars.q_full[t]), 0);
+            ok = ok && bar_wait(shared_addr(&bars.full[at]), lap);
+            if (__all_sync(0xffffffffu, ok) && lane == 0) {
+                for (int t = 0; t < 2; ++t)
+                    if (in(t, j0)) scores(t, ring + at * S::BLOCK_BYTES);
+                mma_commit(shared_addr(&bars.empty[at]));
+            }
+            next();
+        }
+        for (int32_t j = j0; j < j1; ++j) {
+            ok = ok && bar_wait(shared_addr(&bars.full[at]), lap);
+            if (!__all_sync(0xffffffffu, ok)) {
+                ok = false;
+                break;
+            }
+            const uint32_t v_at = at, v_smem = ring + at * S::BLOCK_BYTES;
+            next();
+            // Values past the request's last key are whatever the page holds:
+            // zeros in their place (the weights there are 0, but 0 * NaN is not).
+            if (!E4M3 && (j + 1) * static_cast<int64_t>(kBlock) > r.kv_len) {
+                const int dead = r.kv_len - j * kBlock;                    // first row to clear
+                for (int x = dead * 8 + lane; x < kBlock * 8; x += 32)
+#pragma unroll
+                    for (int h = 0; h < S::HALVES; ++h)
+                        asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(v_smem + h * (kBlock * 128) + x * 16), "r"(0)
+                                     : "memory");
+                fence_shared_async();
+                __syncwarp();
+            }
+            if (j + 1 < j1) {
+                ok = bar_wait(shared_addr(&bars.full[at]), lap);
+                if (!__all_sync(0xffffffffu, ok)) {
+                    ok = false;
+                    break;
+                }
+            }
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                const bool now = in(t, j), then = in(t, j + 1) && j + 1 < j1;
+                if (now) {
+                    ok = ok && bar_wait(shared_addr(&bars.p_full[t]), p_phase[t]);
+                    p_phase[t] ^= 1;
+                }
+                if (!__all_sync(0xffffffffu, ok)) {
+                    ok = false;
+                    break;
+                }
+                tmem_fence_after();
+                if (lane == 0) {
+                    if (now) {
+                        const bool first = j == (t == 0 ? t0.b0 : t1.b0);
+#pragma unroll
+                        for (int k = 0; k < kBlock / 16; ++k)
+                            mma_ts(tmem + 2 * kBlock + t * D, tmem + t * kBlock + k * 8,
+                                   operand_desc(v_smem + k * 2048, kBlock * 128, 1024), o_desc, !(first && k == 0));
+                    }
+                    if (then)
+                        scores(t, ring + at * S::BLOCK_BYTES);
+                    else if (now)
+                        mma_commit(shared_addr(&bars.o_full[t]));
+                }
+            }
+            if (!ok) break;
+            if (lane == 0) {
+                mma_commit(shared_addr(&bars.empty[v_at]));
+                if (j + 1 < j1) mma_commit(shared_addr(&bars.empty[at]));
+            }
+            if (j + 1 < j1) next();
+        }
+        // All products done before the CTA ends.
+        if (lane == 0) mma_commit(shared_addr(&bars.drain));
+        __syncwarp();
+        ok = bar_wait(shared_addr(&bars.drain), 0) && ok;
+    } else if constexpr (!E4M3) {
+        // ------------------------------------------------------------ TMA
+        const int per = a.pg.page_size < kBlock ? kBlock / a.pg.page_size : 1;         // pages of a block
+        const int high = kBlock / per;                                                 // rows of a box
+        const int boxes = per * S::HALVES;
+        const int page_i = lane / S::HALVES, half = lane % S::HALVES;
+        uint32_t at = 0, lap = 0;
+        // Page of this lane's box in block j; n_pages (past the pool: the box
+        // fills with zeros) where there is none.
+        auto page_of = [&](int32_t j) {
+            const int32_t k = j * kBlock + page_i * high;
+            int32_t p = a.pg.n_pages;
+            if (lane < boxes && j < j1 && k < r.kv_len) {
+                const int32_t x = table[k >> a.pg.page_shift];
+                if (x >= 0 && x < a.pg.n_pages) p = x;
+            }
+            return p;
+        };
+        int32_t page = page_of(j0);
+        int issued = 0;
+        for (int32_t j = j0; j < j1 && ok; ++j) {
+            const int32_t now = page;
+            page = page_of(j + 1);
+            const int32_t slot = (j * kBlock + page_i * high) & (a.pg.page_size - 1);
+#pragma unroll
+            for (int kv = 0; kv < 2; ++kv) {
+                ok = bar_wait(shared_addr(&bars.empty[at]), lap ^ 1);
+                if (!__all_sync(0xffffffffu, ok)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t full = shared_addr(&bars.full[at]);
+                if (lane == 0) bar_expect(full, S::BLOCK_BYTES);
+                __syncwarp();
+                if (lane < boxes)
+                    tma_load_4d(ring + at * S::BLOCK_BYTES + half * (kBlock * 128) + page_i * high * 128, kv ? &v_map : &k_map,
+                                full, half * 64, slot, hk, now);
+                ++issued;
+                if (++at == S::STAGES) {
+                    at = 0;
+                    lap ^= 1;
+                }
+            }
+        }
+        // All copies landed before the CTA ends.
+        for (int i = 0; i < S::STAGES && i < issued; ++i) {
+            if (at == 0) lap ^= 1;
+            at = at == 0 ? S::STAGES - 1 : at - 1;
+            ok = bar_wait(shared_addr(&bars.full[at]), lap) && ok;
+        }
+    } else {
+        // ------------------------------------------------------------ E4M3 codes
+        constexpr int CPR = D / 16;                                        // 16-byte pieces of a row of codes
+        constexpr int RPI = S::LOADERS * 32 / CPR;                         // rows in one step of all loader warps
+        constexpr int N = kBlock / RPI;
+        const int tid = threadIdx.x - 9 * 32, c = tid % CPR, row_i = tid / CPR;
+        uint32_t at = 0, lap = 0;
+        uint4 w[N];
+        auto load = [&](int32_t j, int kv) {
+            const uint8_t *cache = static_cast<const uint8_t *>(kv ? a.v_cache : a.k_cache);
+            int32_t p[N];
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const int32_t k = j * kBlock + i * RPI + row_i;
+                p[i] = j < j1 && k < r.kv_len ? table[k >> a.pg.page_shift] : -1;
+            }
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const int32_t k = j * kBlock + i * RPI + row_i;
+                w[i] = make_uint4(0, 0, 0, 0);
+                if (p[i] >= 0 && p[i] < a.pg.n_pages)
+                    w[i] = *reinterpret_cast<const uint4 *>(cache + p[i] * a.pg.page_stride +
+                                                            (k & (a.pg.page_size - 1)) * a.pg.slot_stride +
+                                                            hk * a.pg.head_stride + c * 16);
+            }
+        };
+        auto store = [&](int kv) {
+            const uint32_t dst = ring + at * S::BLOCK_BYTES + (c >> 2) * (kBlock * 128);
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const int row = i * RPI + row_i;
+                const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+                uint32_t x[8];
+#pragma unroll
+                for (int y = 0; y < 8; ++y) {
+                    const uint32_t codes = (u[y >> 1] >> (16 * (y & 1))) & 0xffffu;
+                    x[y] = widen2<T>(codes);
+                }
+#pragma unroll
+                for (int y = 0; y < 2; ++y)
+                    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(
+                                     dst + row * 128 + ((((c & 3) * 2 + y) ^ (row & 7)) << 4)),
+                                 "r"(x[4 * y]), "r"(x[4 * y + 1]), "r"(x[4 * y + 2]), "r"(x[4 * y + 3])
+                                 : "memory");
+            }
+        };
+        if (j1 > j0) load(j0, 0);
+        for (int32_t j = j0; j < j1 && ok; ++j) {
+#pragma unroll
+            for (int kv = 0; kv < 2; ++kv) {
+                ok = bar_wait(shared_addr(&bars.empty[at]), lap ^ 1);
+                if (!__all_sync(0xffffffffu, ok)) {
+                    ok = false;
+                    break;
+                }
+                store(kv);
+                load(kv ? j + 1 : j, kv ^ 1);
+                fence_shared_async();
+                bar_arrive(shared_addr(&bars.full[at]));
+                if (++at == S::STAGES) {
+                    at = 0;
+                    lap ^= 1;
+                }
+            }
+        }
+    }
+    if (!ok && lane == 0) bars.failed = 1;
+    tmem_fence_before();
+    __syncthreads();
+    tmem_fence_after();
+    if (warp == 8) tmem_free<512>(tmem);
+    if (bars.failed) {                                                     // a wait ran out: rows of NaN, and counted
+        if (threadIdx.x == 0) atomicAdd(&g_attention_timeouts, 1ull);
+        const int32_t row = row0 + static_cast<int32_t>(threadIdx.x);
+        if (warp < 8 && row < rows) {
+            const int64_t token = r.q0 + row / a.G;
+            const int32_t h = hk * a.G + row % a.G;
+            T *op = static_cast<T *>(a.out.p) + token * a.out.token_stride + h * a.out.head_stride;
+            if (n_used > 1) {
+                const int64_t part = part_row(a, pl, b, hk, chunk, row);
+                *reinterpret_cast<float2 *>(a.part_ml + part * 2) = make_float2(NAN, NAN);
+            } else {
+                for (int c = 0; c < D; ++c) op[c] = static_cast<T>(NAN);
+                if (a.lse) a.lse[token * a.Hq + h] = NAN;
+            }
+        }
+    }
+    grid_dep_allow();
+}
+
+// The driver's tensor-map encoder, found through the runtime.
+using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
+                                 const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiled encode_tiled() {
+    static const EncodeTiled fn = [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+            found != cudaDriverEntryPointSuccess)
+            p = nullptr;
+        return reinterpret_cast<EncodeTiled>(p);
+    }();
+    return fn;
+}
+
+// A 16-bit cache as a 4-D tensor (element, slot, head, page), in boxes of 64
+// elements by the slots of a page that a block takes.
+bool cache_map(const AttnArgs &a, const void *cache, CUtensorMap *map) {
+    const EncodeTiled encode = encode_tiled();
+    if (!encode) return false;
+    const cuuint64_t dims[4] = {static_cast<cuuint64_t>(a.D), static_cast<cuuint64_t>(a.pg.page_size),
+                                static_cast<cuuint64_t>(a.Hk), static_cast<cuuint64_t>(a.pg.n_pages)};
+    // the stride of an axis of one entry is never used
+    const auto stride = [&](int64_t s, int64_t n) { return static_cast<cuuint64_t>(n > 1 ? s : a.D) * 2; };
+    const cuuint64_t strides[3] = {stride(a.pg.slot_stride, a.pg.page_size), stride(a.pg.head_stride, a.Hk),
+                                   stride(a.pg.page_stride, a.pg.n_pages)};
+    const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(a.pg.page_size < kBlock ? a.pg.page_size : kBlock), 1, 1};
+    const cuuint32_t ones[4] = {1, 1, 1, 1};
+    return encode(map, a.dtype == BEVPOOL_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+                  const_cast<void *>(cache), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace
+
+cudaError_t attention_timeouts(int64_t *count) {
+    unsigned long long n = 0;
+    const cudaError_t e = cudaMemcpyFromSymbol(&n, g_attention_timeouts, sizeof(n));
+    if (e == cudaSuccess) *count = static_cast<int64_t>(n);
+    return e;
+}
+
+cudaError_t launch_attend_tile(const AttnArgs &a, const AttnPlan &pl) {
+    CUtensorMap k_map = {}, v_map = {};
+    if (!a.cache_e4m3 && (!cache_map(a, a.k_cache, &k_map) || !cache_map(a, a.v_cache, &v_map))) return cudaErrorInvalidValue;
+    auto run = [&](auto t, auto e4m3, auto d) {
+        constexpr bool E = decltype(e4m3)::value;
+        constexpr int D = decltype(d)::value;
+        using S = TileShape<E, D>;
+        auto *kernel = k_attend_tile<decltype(t), E, D>;
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
+        if (e != cudaSuccess) return e;
+        kernel<<<dim3(static_cast<unsigned>(div_up(pl.rows, 2 * kTileRows) * a.Hk), static_cast<unsigned>(pl.n_chunks),
+                      static_cast<unsigned>(a.pg.n_seqs)),
+                 S::THREADS, S::SMEM, a.stream>>>(a, pl, k_map, v_map);
+        count_launch();
+        return cudaGetLastError();
+    };
+    auto by_d = [&](auto t, auto e4m3) {
+        return a.D == 64 ? run(t, e4m3, std::integral_constant<int, 64>{})
+                         : run(t, e4m3, std::integral_constant<int, 128>{});
+    };
+    auto by_e = [&](auto t) { return a.cache_e4m3 ? by_d(t, std::true_type{}) : by_d(t, std::false_type{}); };
+    return a.dtype == BEVPOOL_F16 ? by_e(__half{}) : by_e(__nv_bfloat16{});
+}
+
+}  // namespace bevpool

@@ -23,19 +23,25 @@ struct AttnArgs {
     cudaStream_t stream;
 };
 
+struct AttnSizes {
+    int32_t n_seqs, T, Hq, Hk, D, max_q_len, max_kv_len, window;
+};
+
 // How one call is laid out, from its sizes alone.
 struct AttnPlan {
     int32_t few;              // 1: at most 16 query rows a request and key head
-    int32_t rows;             // query rows a request and key head: max_q_len * G
+    int32_t align;            // the first chunk starts at a multiple of this many keys, and has a multiple of it
+    int32_t rows;             // query rows a request and key head, at most
     int32_t chunk;            // keys of one CTA
     int32_t n_chunks;         // CTAs along the keys; above 1 their results are joined by a second kernel
 };
-AttnPlan attention_plan(int32_t n_seqs, int32_t Hq, int32_t Hk, int32_t max_q_len, int32_t max_kv_len, int32_t window);
+AttnPlan attention_plan(const AttnSizes &z);
 cudaError_t launch_attend_few(const AttnArgs &a, const AttnPlan &pl);      // attend_few.cu
+cudaError_t launch_attend_tile(const AttnArgs &a, const AttnPlan &pl);     // attend_tile.cu
+cudaError_t attention_timeouts(int64_t *count);
 cudaError_t launch_attend_join(const AttnArgs &a, const AttnPlan &pl);     // attend_join.cu
 
-size_t attention_workspace_bytes(int32_t n_seqs, int32_t T, int32_t Hq, int32_t Hk, int32_t D, int32_t max_q_len,
-                                 int32_t max_kv_len);
+size_t attention_workspace_bytes(const AttnSizes &z);
 cudaError_t launch_paged_attention(const AttnArgs &a, void *workspace);
 
 // ---------------------------------------------------------------- device
@@ -69,13 +75,12 @@ __device__ __forceinline__ void seen_keys(const AttnArgs &a, const Request &r, i
 
 // Where the keys of a request's chunks start, and how many chunks it has (one
 // at least: it writes the rows that see nothing).
-constexpr int32_t kChunkAlign = 64;
 __device__ __forceinline__ int32_t chunks_of(const AttnArgs &a, const Request &r, int32_t chunk, int32_t n_chunks,
-                                             int32_t *base) {
+                                             int32_t align, int32_t *base) {
     int32_t lo, hi, x;
     seen_keys(a, r, 0, &lo, &x);
     seen_keys(a, r, max(r.q_rows - 1, 0), &x, &hi);
-    *base = min(lo, hi) / kChunkAlign * kChunkAlign;
+    *base = min(lo, hi) / align * align;
     const int64_t n = (static_cast<int64_t>(hi) - *base + chunk - 1) / chunk;
     return static_cast<int32_t>(min(max(n, static_cast<int64_t>(1)), static_cast<int64_t>(n_chunks)));
 }
@@ -85,6 +90,18 @@ __device__ __forceinline__ float pow2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+// Two E4M3 codes (low 16 bits) as two 16-bit values.
+template <typename T>
+__device__ __forceinline__ uint32_t widen2(uint32_t codes) {
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(codes), __NV_E4M3);
+    if constexpr (std::is_same<T, __half>::value) {
+        return *reinterpret_cast<const uint32_t *>(&h);
+    } else {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
+        return pack2<T>(f.x, f.y);
+    }
 }
 
 // E elements of a cache row as FP32.

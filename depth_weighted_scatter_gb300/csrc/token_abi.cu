@@ -63,13 +63,15 @@ bool scale_ok(float s) { return std::isfinite(s) && s > 0.0f && std::isfinite(1.
 // The cache arguments, into *g.  eb: bytes of an element.
 bevpool_status cache_ok(const void *k_cache, const void *v_cache, int64_t page_stride, int64_t slot_stride,
                         int64_t head_stride, int32_t n_pages, int32_t page_size, const int32_t *block_table,
-                        int32_t table_pages, const int32_t *kv_len, const int32_t *cu_q, int32_t n_seqs, int eb,
-                        PagedArgs *g) {
+                        int32_t table_pages, const int32_t *kv_len, const int32_t *cu_q, int32_t n_seqs, int32_t Hk,
+                        int32_t D, int eb, PagedArgs *g) {
     if (page_size < 1 || n_pages < 1 || table_pages < 1 || n_seqs < 0) return BEVPOOL_ERR_INVALID_ARG;
     if (page_size < 16 || page_size > 256 || (page_size & (page_size - 1)) != 0) return BEVPOOL_ERR_UNSUPPORTED;
     const int64_t unit = 16 / eb;
     for (const int64_t s : {page_stride, slot_stride, head_stride})
         if (s < 0 || s >= kMaxStride / 2 || s % unit != 0) return BEVPOOL_ERR_INVALID_ARG;
+    // rows must not overlap; the stride of an axis of one entry is never used
+    if (slot_stride < D || (n_pages > 1 && page_stride < D) || (Hk > 1 && head_stride < D)) return BEVPOOL_ERR_INVALID_ARG;
     if (!k_cache || !v_cache || !aligned(k_cache, 16) || !aligned(v_cache, 16)) return BEVPOOL_ERR_INVALID_ARG;
     const int32_t *idx[] = {block_table, kv_len, cu_q};
     for (const int32_t *p : idx)
@@ -207,7 +209,7 @@ bevpool_status bevpool_kv_append(
     if (n_tokens == 0) return BEVPOOL_OK;
     AppendArgs g = {};
     st = cache_ok(k_cache, v_cache, page_stride, slot_stride, head_stride, n_pages, page_size, block_table, table_pages,
-                  kv_len, cu_q, n_seqs, e4m3 ? 1 : 2, &g.pg);
+                  kv_len, cu_q, n_seqs, n_k_heads, head_dim, e4m3 ? 1 : 2, &g.pg);
     if (st != BEVPOOL_OK) return st;
     if (!rows_ok(k, k_token_stride, k_head_stride) || !rows_ok(v, v_token_stride, v_head_stride) ||
         !weight_ok(q_weight) || !weight_ok(k_weight) || !eps_ok(eps) ||
@@ -254,10 +256,12 @@ bevpool_status attention_sizes_ok(int32_t n_seqs, int32_t T, int32_t Hq, int32_t
 }  // namespace
 
 size_t bevpool_paged_attention_workspace_size(int32_t n_seqs, int32_t n_tokens, int32_t n_q_heads, int32_t n_k_heads,
-                                              int32_t head_dim, int32_t max_q_len, int32_t max_kv_len) {
-    if (attention_sizes_ok(n_seqs, n_tokens, n_q_heads, n_k_heads, head_dim, max_q_len, max_kv_len) != BEVPOOL_OK) return 0;
+                                              int32_t head_dim, int32_t max_q_len, int32_t max_kv_len, int32_t window) {
+    if (attention_sizes_ok(n_seqs, n_tokens, n_q_heads, n_k_heads, head_dim, max_q_len, max_kv_len) != BEVPOOL_OK ||
+        window < 0)
+        return 0;
     if (n_seqs == 0 || n_tokens == 0 || max_q_len == 0) return 0;
-    return attention_workspace_bytes(n_seqs, n_tokens, n_q_heads, n_k_heads, head_dim, max_q_len, max_kv_len);
+    return attention_workspace_bytes({n_seqs, n_tokens, n_q_heads, n_k_heads, head_dim, max_q_len, max_kv_len, window});
 }
 
 bevpool_status bevpool_paged_attention(
@@ -275,7 +279,7 @@ bevpool_status bevpool_paged_attention(
     if (n_tokens == 0 || n_seqs == 0 || max_q_len == 0) return BEVPOOL_OK;
     AttnArgs a = {};
     st = cache_ok(k_cache, v_cache, page_stride, slot_stride, head_stride, n_pages, page_size, block_table, table_pages,
-                  kv_len, cu_q, n_seqs, e4m3 ? 1 : 2, &a.pg);
+                  kv_len, cu_q, n_seqs, n_k_heads, head_dim, e4m3 ? 1 : 2, &a.pg);
     if (st != BEVPOOL_OK) return st;
     if (!rows_ok(q, q_token_stride, q_head_stride) || !rows_ok(out, out_token_stride, out_head_stride) || !aligned(lse, 4))
         return BEVPOOL_ERR_INVALID_ARG;
@@ -283,7 +287,8 @@ bevpool_status bevpool_paged_attention(
     if (!(scale > 0.0f) || !scale_ok(k_scale) || !scale_ok(v_scale) || !std::isfinite(scale * k_scale * 1.4427f))
         return BEVPOOL_ERR_INVALID_ARG;
     if (window < 0 || (window > 0 && !causal)) return BEVPOOL_ERR_INVALID_ARG;
-    const size_t need = attention_workspace_bytes(n_seqs, n_tokens, n_q_heads, n_k_heads, head_dim, max_q_len, max_kv_len);
+    const size_t need =
+        attention_workspace_bytes({n_seqs, n_tokens, n_q_heads, n_k_heads, head_dim, max_q_len, max_kv_len, window});
     if (need > 0 && (!workspace || !aligned(workspace, 256) || workspace_bytes < need)) return BEVPOOL_ERR_WORKSPACE;
     a.dtype = dtype;
     a.cache_e4m3 = e4m3;
@@ -305,6 +310,11 @@ bevpool_status bevpool_paged_attention(
     a.lse = lse;
     a.stream = static_cast<cudaStream_t>(stream);
     return cuda_status(launch_paged_attention(a, workspace));
+}
+
+bevpool_status bevpool_attention_timeouts(int64_t *h_count) {
+    if (!h_count) return BEVPOOL_ERR_INVALID_ARG;
+    return cuda_status(attention_timeouts(h_count));
 }
 
 }  // extern "C"

@@ -514,7 +514,7 @@ BEVPOOL_API bevpool_status bevpool_kv_append(
  * invalid. */
 BEVPOOL_API size_t bevpool_paged_attention_workspace_size(int32_t n_seqs, int32_t n_tokens, int32_t n_q_heads,
                                                           int32_t n_k_heads, int32_t head_dim, int32_t max_q_len,
-                                                          int32_t max_kv_len);
+                                                          int32_t max_kv_len, int32_t window);
 
 /*
  * Attention of new tokens over the paged cache:
@@ -536,7 +536,7 @@ BEVPOOL_API size_t bevpool_paged_attention_workspace_size(int32_t n_seqs, int32_
  *                a request past max_q_len are not computed; keys past
  *                max_kv_len (or past the table) are not seen;
  *   out          dtype, with strides; lse: device float [n_tokens][n_q_heads]
- *                or NULL.
+ *                or NULL.  out must not overlap q.
  * The cache arguments are those of bevpool_kv_append.  Results are
  * deterministic.
  */
@@ -548,6 +548,12 @@ BEVPOOL_API bevpool_status bevpool_paged_attention(
     int32_t max_q_len, int32_t max_kv_len, float scale, int32_t causal, int32_t window, float k_scale,
     float v_scale, void *out, int64_t out_token_stride, int64_t out_head_stride, float *lse, void *workspace,
     size_t workspace_bytes, void *stream);
+
+/* Waits inside the attention kernels that ran out since the library was loaded
+ * (0 unless the device misbehaves: every wait is bounded, and a CTA whose wait
+ * runs out writes NaN to its rows).  h_count: host; the call synchronises with
+ * the device. */
+BEVPOOL_API bevpool_status bevpool_attention_timeouts(int64_t *h_count);
 
 #ifdef __cplusplus
 }
