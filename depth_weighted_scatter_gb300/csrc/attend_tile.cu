@@ -10,7 +10,7 @@
 //                    and O += P V (P from tensor memory), O in tensor memory
 //   warp 9           loads K and V: a TMA box for each page and 64 elements of
 //                    the head, into a ring of 128-byte-swizzled blocks
-//   warps 9-12       (E4M3 cache instead) load codes, widen them to 16 bits and
+//   warps 12-15      (E4M3 cache instead) load codes, widen them to 16 bits and
 //                    store them in the same layout
 // While one tile is in its softmax the tensor core works on the other.
 //
@@ -42,8 +42,18 @@ constexpr float kGrow = 8.0f;              // log2 of the growth that P may show
 
 template <bool E4M3, int D>
 struct TileShape {
+    // Warpgroups: two of softmax, one of products and TMA, and with E4M3 codes
+    // one of loaders.  Registers a thread, by setmaxnreg; their sum is within
+    // what the launch gives (168 a thread of 384, 128 of 512).
     static constexpr int LOADERS = E4M3 ? 4 : 1;                           // warps
-    static constexpr int THREADS = (9 + LOADERS) * 32;
+    static constexpr int FIRST_LOADER = E4M3 ? 12 : 9;
+    static constexpr int THREADS = E4M3 ? 512 : 384;
+    static constexpr int LAUNCH_REGS = E4M3 ? 128 : 168;
+    static constexpr int SOFTMAX_REGS = E4M3 ? 200 : 208;
+    static constexpr int PRODUCT_REGS = E4M3 ? 32 : 80;
+    static constexpr int LOADER_REGS = 80;
+    static_assert(256 * SOFTMAX_REGS + 128 * PRODUCT_REGS + (E4M3 ? 128 * LOADER_REGS : 0) <= THREADS * LAUNCH_REGS,
+                  "the split is within the launch's registers");
     static constexpr int HALVES = D / 64;                                  // 128-byte columns of a block
     static constexpr int BLOCK_BYTES = kBlock * D * 2;
     static constexpr int STAGES = D == 128 ? 4 : 6;                        // K and V blocks in turn
@@ -121,6 +131,12 @@ k_attend_tile(AttnArgs a, AttnPlan pl, const __grid_constant__ CUtensorMap k_map
     tmem_fence_after();
     const uint32_t tmem = bars.tmem;
     bool ok = true;
+    if (warp < 8)
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(S::SOFTMAX_REGS));
+    else if (warp < 12)
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::PRODUCT_REGS));
+    else
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::LOADER_REGS));
 
     if (warp < 8) {
         // ------------------------------------------------------------ softmax
@@ -406,6 +422,8 @@ k_attend_tile(AttnArgs a, AttnPlan pl, const __grid_constant__ CUtensorMap k_map
         if (lane == 0) mma_commit(shared_addr(&bars.drain));
         __syncwarp();
         ok = bar_wait(shared_addr(&bars.drain), 0) && ok;
+    } else if (warp < S::FIRST_LOADER || warp >= S::FIRST_LOADER + S::LOADERS) {
+        // warps without work
     } else if constexpr (!E4M3) {
         // ------------------------------------------------------------ TMA
         const int per = a.pg.page_size < kBlock ? kBlock / a.pg.page_size : 1;         // pages of a block
@@ -461,7 +479,7 @@ k_attend_tile(AttnArgs a, AttnPlan pl, const __grid_constant__ CUtensorMap k_map
         constexpr int CPR = D / 16;                                        // 16-byte pieces of a row of codes
         constexpr int RPI = S::LOADERS * 32 / CPR;                         // rows in one step of all loader warps
         constexpr int N = kBlock / RPI;
-        const int tid = threadIdx.x - 9 * 32, c = tid % CPR, row_i = tid / CPR;
+        const int tid = threadIdx.x - S::FIRST_LOADER * 32, c = tid % CPR, row_i = tid / CPR;
         uint32_t at = 0, lap = 0;
         uint4 w[N];
         auto load = [&](int32_t j, int kv) {
