@@ -56,14 +56,14 @@ struct TileShape {
                   "the split is within the launch's registers");
     static constexpr int HALVES = D / 64;                                  // 128-byte columns of a block
     static constexpr int BLOCK_BYTES = kBlock * D * 2;
-    static constexpr int STAGES = D == 128 ? 4 : 6;                        // K and V blocks in turn
+    static constexpr int STAGES = D == 128 ? 5 : 8;                        // K and V blocks in turn
     static constexpr int Q_BYTES = kTileRows * D * 2;
     static constexpr int SMEM = 1024 + 2 * Q_BYTES + STAGES * BLOCK_BYTES; // 1024: alignment
 };
 
 struct TileBars {                          // shared memory
-    uint64_t full[6], empty[6];            // ring
-    uint64_t q_full[2], s_full[2], p_full[2], o_full[2], drain;
+    uint64_t full[8], empty[8];            // ring
+    uint64_t q_full[2], s_full[2], p_full[2][2], o_full[2], drain;
     uint32_t tmem, failed;
 };
 
@@ -118,7 +118,8 @@ k_attend_tile(AttnArgs a, AttnPlan pl, const __grid_constant__ CUtensorMap k_map
         for (int t = 0; t < 2; ++t) {
             bar_init(shared_addr(&bars.q_full[t]), kTileRows);
             bar_init(shared_addr(&bars.s_full[t]), 1);
-            bar_init(shared_addr(&bars.p_full[t]), kTileRows);
+            bar_init(shared_addr(&bars.p_full[t][0]), kTileRows);
+            bar_init(shared_addr(&bars.p_full[t][1]), kTileRows);
             bar_init(shared_addr(&bars.o_full[t]), 1);
         }
         bar_init(shared_addr(&bars.drain), 1);
@@ -252,12 +253,14 @@ k_attend_tile(AttnArgs a, AttnPlan pl, const __grid_constant__ CUtensorMap k_map
                         sum = add2(sum, pair(x, y));
                     p[c] = pack2<T>(x, y);
                 }
+                // Each half is released by itself: its product with V runs
+                // during the exponentials of the other.
                 tmem_st32(s_mem + h * 32, p);
+                tmem_wait_st();
+                tmem_fence_before();
+                bar_arrive(shared_addr(&bars.p_full[t][h]));
             }
             sum = add2(sum, part);
-            tmem_wait_st();
-            tmem_fence_before();
-            bar_arrive(shared_addr(&bars.p_full[t]));
         }
         float l, l1;
         unpair(sum, &l, &l1);
@@ -351,7 +354,7 @@ k_attend_tile(AttnArgs a, AttnPlan pl, const __grid_constant__ CUtensorMap k_map
             for (int t = 0; t < 2 && ok; ++t)
                 if ((t == 0 ? t0.b1 : t1.b1) > 0) ok = bar_wait(shared_addr(&bars.q_full[t]), 0);
             ok = ok && bar_wait(shared_addr(&bars.full[at]), lap);
-            if (__all_sync(0xffffffffu, ok) && lane == 0) {
+            if (__all_sync(0xffffffffu, ok) && elect_one()) {
                 for (int t = 0; t < 2; ++t)
                     if (in(t, j0)) scores(t, ring + at * S::BLOCK_BYTES);
                 mma_commit(shared_addr(&bars.empty[at]));
@@ -388,38 +391,40 @@ k_attend_tile(AttnArgs a, AttnPlan pl, const __grid_constant__ CUtensorMap k_map
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
                 const bool now = in(t, j), then = in(t, j + 1) && j + 1 < j1;
-                if (now) {
-                    ok = ok && bar_wait(shared_addr(&bars.p_full[t]), p_phase[t]);
-                    p_phase[t] ^= 1;
+                const bool first = j == (t == 0 ? t0.b0 : t1.b0);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    if (!now) continue;
+                    ok = bar_wait(shared_addr(&bars.p_full[t][h]), p_phase[t]) && ok;
+                    tmem_fence_after();
+                    if (__all_sync(0xffffffffu, ok) && elect_one()) {
+#pragma unroll
+                        for (int k = h * (kBlock / 32); k < (h + 1) * (kBlock / 32); ++k)
+                            mma_ts(tmem + 2 * kBlock + t * D, tmem + t * kBlock + k * 8,
+                                   operand_desc(v_smem + k * 2048, kBlock * 128, 1024), o_desc, !(first && k == 0));
+                    }
+                    __syncwarp();
                 }
+                if (now) p_phase[t] ^= 1;
                 if (!__all_sync(0xffffffffu, ok)) {
                     ok = false;
                     break;
                 }
-                tmem_fence_after();
-                if (lane == 0) {
-                    if (now) {
-                        const bool first = j == (t == 0 ? t0.b0 : t1.b0);
-#pragma unroll
-                        for (int k = 0; k < kBlock / 16; ++k)
-                            mma_ts(tmem + 2 * kBlock + t * D, tmem + t * kBlock + k * 8,
-                                   operand_desc(v_smem + k * 2048, kBlock * 128, 1024), o_desc, !(first && k == 0));
-                    }
+                if (elect_one()) {
+                    if (t == 1) mma_commit(shared_addr(&bars.empty[v_at]));
                     if (then)
                         scores(t, ring + at * S::BLOCK_BYTES);
                     else if (now)
                         mma_commit(shared_addr(&bars.o_full[t]));
+                    if (t == 1 && j + 1 < j1) mma_commit(shared_addr(&bars.empty[at]));
                 }
+                __syncwarp();
             }
             if (!ok) break;
-            if (lane == 0) {
-                mma_commit(shared_addr(&bars.empty[v_at]));
-                if (j + 1 < j1) mma_commit(shared_addr(&bars.empty[at]));
-            }
             if (j + 1 < j1) next();
         }
         // All products done before the CTA ends.
-        if (lane == 0) mma_commit(shared_addr(&bars.drain));
+        if (elect_one()) mma_commit(shared_addr(&bars.drain));
         __syncwarp();
         ok = bar_wait(shared_addr(&bars.drain), 0) && ok;
     } else if (warp < S::FIRST_LOADER || warp >= S::FIRST_LOADER + S::LOADERS) {
