@@ -16,8 +16,8 @@ heads' type, or E4M3 codes (torch.float8_e4m3fn or uint8).
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import functools
 from typing import Optional, Sequence
 
 import torch
@@ -95,186 +95,198 @@ def bevpool_attention_timeouts() -> int:
 _DTYPES = {torch.float16: BEVPOOL_F16, torch.bfloat16: BEVPOOL_BF16}
 _CACHE_DTYPES = {torch.float16: BEVPOOL_F16, torch.bfloat16: BEVPOOL_BF16, torch.float8_e4m3fn: BEVPOOL_E4M3,
                  torch.uint8: BEVPOOL_E4M3}
+_F32, _I32 = torch.float32, torch.int32
+
+# A decoding step calls these helpers for every layer, so they keep to a few
+# cheap tensor attributes each: device indexes instead of device objects, the
+# raw stream instead of a Stream object, one message built only on refusal.
 
 
 def _refuse(what: str, status: int = BEVPOOL_ERR_INVALID_ARG):
     raise BevpoolError(status, what)
 
 
-def _heads(name: str, t, like=None):
-    """Checks a [tokens, heads, head_dim] tensor; returns (pointer, token stride, head stride)."""
-    if t.dim() != 3 or not t.is_cuda:
-        _refuse(f"{name}: a [tokens, heads, head_dim] CUDA tensor is wanted")
-    if t.dtype not in _DTYPES:
-        _refuse(f"{name}: fp16 or bf16 is wanted, got {t.dtype}", BEVPOOL_ERR_UNSUPPORTED)
+def _heads(name: str, t, shape, dtype, dev: int) -> tuple:
+    """(pointer, token stride, head stride) of a [tokens, heads, head_dim] tensor of this shape, type and device."""
+    if t.shape != shape or t.dtype != dtype or t.get_device() != dev:
+        _refuse(f"{name}: a {dtype} tensor of shape {tuple(shape)} on CUDA device {dev} is wanted, got {t.dtype} "
+                f"{tuple(t.shape)} on {t.device}")
     ts, hs, es = t.stride()
-    if es != 1 and t.shape[2] != 1:
+    if es != 1:
         _refuse(f"{name}: the last axis must be contiguous")
-    if like is not None and (t.dtype != like.dtype or t.device != like.device or t.shape[0] != like.shape[0]
-                             or t.shape[2] != like.shape[2]):
-        _refuse(f"{name}: type, device, tokens and head_dim must match")
     # the stride of an axis of one entry is never used
-    return t.data_ptr(), (ts if t.shape[0] > 1 else 0), (hs if t.shape[1] > 1 else 0)
+    return t.data_ptr(), ts if shape[0] > 1 else 0, hs if shape[1] > 1 else 0
 
 
-def _out(name: str, t, like, heads: int):
-    if t is None:
-        return torch.empty((like.shape[0], heads, like.shape[2]), dtype=like.dtype, device=like.device)
-    if t.shape != (like.shape[0], heads, like.shape[2]) or t.dtype != like.dtype or t.device != like.device:
-        _refuse(f"{name}: shape, type or device does not match")
-    return t
+def _check_first(name: str, t) -> tuple:
+    """(shape, type, library type, device index) of the tensor that the others are checked against."""
+    if t.dim() != 3:
+        _refuse(f"{name}: a [tokens, heads, head_dim] tensor is wanted")
+    dtype, dev = t.dtype, t.get_device()
+    code = _DTYPES.get(dtype)
+    if code is None:
+        _refuse(f"{name}: fp16 or bf16 is wanted, got {dtype}", BEVPOOL_ERR_UNSUPPORTED)
+    if dev < 0 or dev != torch._C._cuda_getDevice():
+        _refuse(f"{name}: tensors must be on the current CUDA device")
+    return t.shape, dtype, code, dev
 
 
-def _vector(name: str, t, n: int, dtype, device):
+def _vector(name: str, t, n: int, dtype, dev: int):
     if t is None:
         return None
-    if t.dtype != dtype or t.device != device or t.numel() != n or not t.is_contiguous():
-        _refuse(f"{name}: a contiguous {dtype} tensor of {n} entries on {device} is wanted")
+    if t.dtype != dtype or t.get_device() != dev or t.numel() != n or not t.is_contiguous():
+        _refuse(f"{name}: a contiguous {dtype} tensor of {n} entries on CUDA device {dev} is wanted")
     return t.data_ptr()
 
 
-def _position_args(like, positions, inv_freq, sections: Optional[Sequence[int]], interleaved: bool) -> tuple:
-    T = like.shape[0]
-    n_axes = positions.shape[1] if positions.dim() == 2 else 1
-    if positions.dim() not in (1, 2) or positions.shape[0] != T or not 1 <= n_axes <= MAX_AXES:
+@functools.lru_cache(maxsize=64)
+def _sections(sections: tuple):
+    return (_i32 * len(sections))(*sections)
+
+
+def _position_args(T: int, dev: int, positions, inv_freq, sections: Optional[Sequence[int]], interleaved: bool) -> tuple:
+    shape = positions.shape
+    n_axes = shape[1] if len(shape) == 2 else 1
+    if not 1 <= len(shape) <= 2 or shape[0] != T or not 1 <= n_axes <= MAX_AXES:
         _refuse(f"positions: int32 [tokens] or [tokens, axes <= {MAX_AXES}] is wanted")
     n = inv_freq.numel()
-    sec = [n] if sections is None else list(sections)
+    sec = (n,) if sections is None else tuple(sections)
     if len(sec) != n_axes:
         _refuse("sections: one entry an axis is wanted")
-    return (_vector("positions", positions, T * n_axes, torch.int32, like.device), n_axes, (_i32 * n_axes)(*sec), 2 * n,
-            _vector("inv_freq", inv_freq, n, torch.float32, like.device), int(interleaved))
+    return (_vector("positions", positions, T * n_axes, _I32, dev), n_axes, _sections(sec), 2 * n,
+            _vector("inv_freq", inv_freq, n, _F32, dev), 1 if interleaved else 0)
 
 
-def _cache_args(k_cache, v_cache, block_table, kv_len, cu_q, like, n_k_heads: int) -> tuple:
-    """(cache dtype, (k pointer, v pointer), page arguments)."""
-    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or k_cache.dtype != v_cache.dtype:
-        _refuse("caches: two [n_pages, n_k_heads, page_size, head_dim] tensors of one type are wanted")
-    if k_cache.dtype not in _CACHE_DTYPES:
-        _refuse(f"caches: {k_cache.dtype}", BEVPOOL_ERR_UNSUPPORTED)
-    n_pages, heads, page_size, D = k_cache.shape
-    if heads != n_k_heads or D != like.shape[2] or k_cache.device != like.device or v_cache.device != like.device:
+def _cache_args(k_cache, v_cache, block_table, kv_len, cu_q, dev: int, n_k_heads: Optional[int], D: int) -> tuple:
+    """(cache type, pointers, page arguments); n_k_heads None: whatever the cache has."""
+    shape, dtype, strides = k_cache.shape, k_cache.dtype, k_cache.stride()
+    if len(shape) != 4 or v_cache.shape != shape or v_cache.dtype != dtype or v_cache.stride() != strides:
+        _refuse("caches: two [n_pages, n_k_heads, page_size, head_dim] tensors of one type and layout are wanted")
+    code = _CACHE_DTYPES.get(dtype)
+    if code is None:
+        _refuse(f"caches: {dtype}", BEVPOOL_ERR_UNSUPPORTED)
+    n_pages, heads, page_size, d = shape
+    if (n_k_heads is not None and heads != n_k_heads) or d != D or k_cache.get_device() != dev or v_cache.get_device() != dev:
         _refuse("caches: heads, head_dim or device does not match")
-    if k_cache.stride() != v_cache.stride() or k_cache.stride(3) != 1:
-        _refuse("caches: equal strides and a contiguous last axis are wanted")
-    if block_table.dim() != 2 or cu_q.numel() != block_table.shape[0] + 1:
-        _refuse("block_table [n_seqs, pages] and cu_q [n_seqs + 1] are wanted")
-    n_seqs, table_pages = block_table.shape
-    sp, sh, ss, _ = k_cache.stride()
-    dev = like.device
-    return (_CACHE_DTYPES[k_cache.dtype], (k_cache.data_ptr(), v_cache.data_ptr()),
+    sp, sh, ss, se = strides
+    if se != 1:
+        _refuse("caches: the last axis must be contiguous")
+    tshape = block_table.shape
+    if len(tshape) != 2:
+        _refuse("block_table: [n_seqs, pages] is wanted")
+    n_seqs, table_pages = tshape
+    return (code, (k_cache.data_ptr(), v_cache.data_ptr()),
             (sp if n_pages > 1 else 0, ss, sh if heads > 1 else 0, n_pages, page_size,
-             _vector("block_table", block_table, n_seqs * table_pages, torch.int32, dev), table_pages,
-             _vector("kv_len", kv_len, n_seqs, torch.int32, dev), _vector("cu_q", cu_q, n_seqs + 1, torch.int32, dev),
-             n_seqs))
+             _vector("block_table", block_table, n_seqs * table_pages, _I32, dev), table_pages,
+             _vector("kv_len", kv_len, n_seqs, _I32, dev), _vector("cu_q", cu_q, n_seqs + 1, _I32, dev), n_seqs))
 
 
-@contextlib.contextmanager
-def _torch_stream(stream):
-    with torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))):
-        yield
+def _stream_of(stream):
+    return stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
 
 
-def _on_stream(fn):
-    """Runs a helper with `stream` (a torch stream or a cudaStream_t; None: the
-    current one) as torch's current stream, so that what it allocates belongs
-    to the stream that uses it."""
-    def run(*args, stream=None, **kw):
-        if stream is None:
-            return fn(*args, stream=torch.cuda.current_stream().cuda_stream, **kw)
-        with _torch_stream(stream):
-            return fn(*args, stream=torch.cuda.current_stream().cuda_stream, **kw)
+# Each helper takes `stream` (a torch stream or a cudaStream_t; None: torch's
+# current one).  Another stream is made torch's current stream for the call, so
+# that what the helper allocates belongs to the stream that uses it.
 
-    run.__name__, run.__doc__ = fn.__name__, fn.__doc__
-    run.__wrapped__ = fn
-    return run
-
-
-def _check_device(t):
-    if t.device.index != torch.cuda.current_device():
-        _refuse("tensors must be on the current CUDA device")
-
-
-@_on_stream
 def qk_norm_rope(q, k, positions, inv_freq, *, sections=None, q_weight=None, k_weight=None, eps: float = 1e-6,
                  interleaved: bool = False, q_out=None, k_out=None, stream=None):
     """bevpool_qk_norm_rope: norms of q and k for each head (where the weight is
     given) and their rotary positions.  positions int32 [tokens] or [tokens,
     axes]; inv_freq float32 [rotary_dim / 2]; sections: pairs of each axis.
     Returns (q_out, k_out); q_out=q, k_out=k works in place."""
-    qa, ka = _heads("q", q), _heads("k", k, q)
-    _check_device(q)
-    D = q.shape[2]
-    pos = _position_args(q, positions, inv_freq, sections, interleaved)
-    w = (_vector("q_weight", q_weight, D, torch.float32, q.device), _vector("k_weight", k_weight, D, torch.float32, q.device))
-    q_out, k_out = _out("q_out", q_out, q, q.shape[1]), _out("k_out", k_out, k, k.shape[1])
-    st = bevpool_qk_norm_rope(_DTYPES[q.dtype], *qa, *ka, q.shape[0], q.shape[1], k.shape[1], D, *w, eps, *pos,
-                              *_heads("q_out", q_out), *_heads("k_out", k_out), stream)
+    if stream is not None:
+        with torch.cuda.stream(_stream_of(stream)):
+            return qk_norm_rope(q, k, positions, inv_freq, sections=sections, q_weight=q_weight, k_weight=k_weight, eps=eps,
+                                interleaved=interleaved, q_out=q_out, k_out=k_out)
+    qs, dtype, code, dev = _check_first("q", q)
+    T, Hq, D = qs
+    ks = (T, k.shape[1] if k.dim() == 3 else -1, D)
+    pos = _position_args(T, dev, positions, inv_freq, sections, interleaved)
+    qw, kw = _vector("q_weight", q_weight, D, _F32, dev), _vector("k_weight", k_weight, D, _F32, dev)
+    qa, ka = _heads("q", q, qs, dtype, dev), _heads("k", k, ks, dtype, dev)
+    if q_out is None:
+        q_out = q.new_empty(qs)
+    if k_out is None:
+        k_out = k.new_empty(ks)
+    st = _lib.bevpool_qk_norm_rope(code, *qa, *ka, T, Hq, ks[1], D, qw, kw, eps, *pos,
+                                   *_heads("q_out", q_out, qs, dtype, dev), *_heads("k_out", k_out, ks, dtype, dev),
+                                   torch._C._cuda_getCurrentRawStream(dev))
     if st != BEVPOOL_OK:
         raise BevpoolError(st, "bevpool_qk_norm_rope")
     return q_out, k_out
 
 
-@_on_stream
 def qk_norm_rope_backward(dq_out, dk_out, q, k, positions, inv_freq, *, sections=None, q_weight=None, k_weight=None,
                           eps: float = 1e-6, interleaved: bool = False, dq=None, dk=None, workspace=None, stream=None):
     """bevpool_qk_norm_rope_backward: gradients of qk_norm_rope's inputs and
     weights from those of its outputs.  Returns (dq, dk, dq_weight, dk_weight);
     a weight that is None has the gradient None."""
-    ga, ha, qa, ka = _heads("dq_out", dq_out, q), _heads("dk_out", dk_out, q), _heads("q", q), _heads("k", k, q)
-    _check_device(q)
-    T, Hq, D = q.shape
-    Hk = k.shape[1]
-    if dq_out.shape[1] != Hq or dk_out.shape[1] != Hk:
-        _refuse("dq_out, dk_out: heads must match q and k")
-    pos = _position_args(q, positions, inv_freq, sections, interleaved)
-    w = (_vector("q_weight", q_weight, D, torch.float32, q.device), _vector("k_weight", k_weight, D, torch.float32, q.device))
-    dq, dk = _out("dq", dq, q, Hq), _out("dk", dk, k, Hk)
-    dqw, dkw = (None if x is None else torch.empty(D, dtype=torch.float32, device=q.device) for x in (q_weight, k_weight))
-    if workspace is None and (q_weight is not None or k_weight is not None):
-        n = bevpool_qk_norm_rope_backward_workspace_size(T, Hq, Hk, D)
-        workspace = torch.empty(max(n, 1), dtype=torch.uint8, device=q.device)
-    st = bevpool_qk_norm_rope_backward(
-        _DTYPES[q.dtype], *ga, *ha, *qa, *ka, T, Hq, Hk, D, *w, eps, *pos, *_heads("dq", dq), *_heads("dk", dk),
-        None if dqw is None else dqw.data_ptr(), None if dkw is None else dkw.data_ptr(),
-        None if workspace is None else workspace.data_ptr(),
-        0 if workspace is None else workspace.numel() * workspace.element_size(), stream)
+    if stream is not None:
+        with torch.cuda.stream(_stream_of(stream)):
+            return qk_norm_rope_backward(dq_out, dk_out, q, k, positions, inv_freq, sections=sections, q_weight=q_weight,
+                                         k_weight=k_weight, eps=eps, interleaved=interleaved, dq=dq, dk=dk,
+                                         workspace=workspace)
+    qs, dtype, code, dev = _check_first("q", q)
+    T, Hq, D = qs
+    ks = (T, k.shape[1] if k.dim() == 3 else -1, D)
+    pos = _position_args(T, dev, positions, inv_freq, sections, interleaved)
+    qw, kw = _vector("q_weight", q_weight, D, _F32, dev), _vector("k_weight", k_weight, D, _F32, dev)
+    ga, ha = _heads("dq_out", dq_out, qs, dtype, dev), _heads("dk_out", dk_out, ks, dtype, dev)
+    qa, ka = _heads("q", q, qs, dtype, dev), _heads("k", k, ks, dtype, dev)
+    if dq is None:
+        dq = q.new_empty(qs)
+    if dk is None:
+        dk = k.new_empty(ks)
+    dqw = None if qw is None else torch.empty_like(q_weight)
+    dkw = None if kw is None else torch.empty_like(k_weight)
+    if workspace is None and not (qw is None and kw is None):
+        workspace = torch.empty(max(_lib.bevpool_qk_norm_rope_backward_workspace_size(T, Hq, ks[1], D), 1),
+                                dtype=torch.uint8, device=q.device)
+    st = _lib.bevpool_qk_norm_rope_backward(
+        code, *ga, *ha, *qa, *ka, T, Hq, ks[1], D, qw, kw, eps, *pos, *_heads("dq", dq, qs, dtype, dev),
+        *_heads("dk", dk, ks, dtype, dev), None if dqw is None else dqw.data_ptr(), None if dkw is None else dkw.data_ptr(),
+        None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.nbytes,
+        torch._C._cuda_getCurrentRawStream(dev))
     if st != BEVPOOL_OK:
         raise BevpoolError(st, "bevpool_qk_norm_rope_backward")
     return dq, dk, dqw, dkw
 
 
-@_on_stream
 def kv_append(k, v, k_cache, v_cache, block_table, kv_len, cu_q, positions, inv_freq, *, sections=None, k_weight=None,
               eps: float = 1e-6, interleaved: bool = False, k_scale: float = 1.0, v_scale: float = 1.0, q=None,
               q_weight=None, q_out=None, stream=None):
     """bevpool_kv_append: the keys (normed where k_weight is given, and turned)
     and values of new tokens into the paged cache; with q, its norm and rotation
     too.  kv_len counts the new tokens.  Returns q_out (None without q)."""
-    ka, va = _heads("k", k), _heads("v", v, k)
-    _check_device(k)
-    T, Hk, D = k.shape
-    if v.shape[1] != Hk:
-        _refuse("v: heads must match k")
-    pos = _position_args(k, positions, inv_freq, sections, interleaved)
-    cache_dtype, ptrs, pages = _cache_args(k_cache, v_cache, block_table, kv_len, cu_q, k, Hk)
-    w = (_vector("q_weight", q_weight, D, torch.float32, k.device), _vector("k_weight", k_weight, D, torch.float32, k.device))
-    if q is None:
-        if q_out is not None:
-            _refuse("q_out without q")
-        Hq, qa, oa = 0, (None, 0, 0), (None, 0, 0)
-    else:
-        Hq, qa = q.shape[1], _heads("q", q, k)
-        q_out = _out("q_out", q_out, q, Hq)
-        oa = _heads("q_out", q_out)
-    st = bevpool_kv_append(_DTYPES[k.dtype], cache_dtype, *ka, *va, *qa, T, Hq, Hk, D, *w, eps, *pos, *oa, *ptrs, *pages,
-                           k_scale, v_scale, stream)
+    if stream is not None:
+        with torch.cuda.stream(_stream_of(stream)):
+            return kv_append(k, v, k_cache, v_cache, block_table, kv_len, cu_q, positions, inv_freq, sections=sections,
+                             k_weight=k_weight, eps=eps, interleaved=interleaved, k_scale=k_scale, v_scale=v_scale, q=q,
+                             q_weight=q_weight, q_out=q_out)
+    ks, dtype, code, dev = _check_first("k", k)
+    T, Hk, D = ks
+    pos = _position_args(T, dev, positions, inv_freq, sections, interleaved)
+    cache_code, ptrs, pages = _cache_args(k_cache, v_cache, block_table, kv_len, cu_q, dev, Hk, D)
+    qw, kw = _vector("q_weight", q_weight, D, _F32, dev), _vector("k_weight", k_weight, D, _F32, dev)
+    Hq, qa, oa = 0, (None, 0, 0), (None, 0, 0)
+    if q is not None:
+        Hq = q.shape[1] if q.dim() == 3 else -1
+        qs = (T, Hq, D)
+        qa = _heads("q", q, qs, dtype, dev)
+        if q_out is None:
+            q_out = q.new_empty(qs)
+        oa = _heads("q_out", q_out, qs, dtype, dev)
+    elif q_out is not None:
+        _refuse("q_out without q")
+    st = _lib.bevpool_kv_append(code, cache_code, *_heads("k", k, ks, dtype, dev), *_heads("v", v, ks, dtype, dev), *qa, T, Hq,
+                                Hk, D, qw, kw, eps, *pos, *oa, *ptrs, *pages, k_scale, v_scale,
+                                torch._C._cuda_getCurrentRawStream(dev))
     if st != BEVPOOL_OK:
         raise BevpoolError(st, "bevpool_kv_append")
     return q_out
 
 
-@_on_stream
 def paged_attention(q, k_cache, v_cache, block_table, kv_len, cu_q, *, max_q_len: int, max_kv_len: int,
                     scale: Optional[float] = None, causal: bool = True, window: int = 0, k_scale: float = 1.0,
                     v_scale: float = 1.0, out=None, return_lse: bool = False, workspace=None, stream=None):
@@ -283,21 +295,28 @@ def paged_attention(q, k_cache, v_cache, block_table, kv_len, cu_q, *, max_q_len
     max_q_len and max_kv_len are host bounds of the requests' lengths.  Returns
     out, or (out, lse) with return_lse.  Rows of q outside every request keep
     what `out` held."""
-    qa = _heads("q", q)
-    _check_device(q)
-    T, Hq, D = q.shape
-    Hk = k_cache.shape[1] if k_cache.dim() == 4 else 0
-    cache_dtype, ptrs, pages = _cache_args(k_cache, v_cache, block_table, kv_len, cu_q, q, Hk)
-    out = _out("out", out, q, Hq)
-    lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device) if return_lse else None
+    if stream is not None:
+        with torch.cuda.stream(_stream_of(stream)):
+            return paged_attention(q, k_cache, v_cache, block_table, kv_len, cu_q, max_q_len=max_q_len,
+                                   max_kv_len=max_kv_len, scale=scale, causal=causal, window=window, k_scale=k_scale,
+                                   v_scale=v_scale, out=out, return_lse=return_lse, workspace=workspace)
+    qs, dtype, code, dev = _check_first("q", q)
+    T, Hq, D = qs
+    cache_code, ptrs, pages = _cache_args(k_cache, v_cache, block_table, kv_len, cu_q, dev, None, D)
+    Hk = k_cache.shape[1]
+    if out is None:
+        out = q.new_empty(qs)
+    lse = torch.empty((T, Hq), dtype=_F32, device=q.device) if return_lse else None
     if workspace is None:
-        n = bevpool_paged_attention_workspace_size(pages[-1], T, Hq, Hk, D, max_q_len, max_kv_len, window)
-        workspace = torch.empty(n, dtype=torch.uint8, device=q.device) if n else None
-    st = bevpool_paged_attention(
-        _DTYPES[q.dtype], cache_dtype, *qa, *ptrs, *pages, T, Hq, Hk, D, max_q_len, max_kv_len,
-        D ** -0.5 if scale is None else scale, int(causal), window, k_scale, v_scale, *_heads("out", out),
-        None if lse is None else lse.data_ptr(), None if workspace is None else workspace.data_ptr(),
-        0 if workspace is None else workspace.numel() * workspace.element_size(), stream)
+        n = _lib.bevpool_paged_attention_workspace_size(pages[9], T, Hq, Hk, D, max_q_len, max_kv_len, window)
+        if n:
+            workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
+    st = _lib.bevpool_paged_attention(
+        code, cache_code, *_heads("q", q, qs, dtype, dev), *ptrs, *pages, T, Hq, Hk, D, max_q_len, max_kv_len,
+        D ** -0.5 if scale is None else scale, 1 if causal else 0, window, k_scale, v_scale,
+        *_heads("out", out, qs, dtype, dev), None if lse is None else lse.data_ptr(),
+        None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.nbytes,
+        torch._C._cuda_getCurrentRawStream(dev))
     if st != BEVPOOL_OK:
         raise BevpoolError(st, "bevpool_paged_attention")
     return (out, lse) if return_lse else out

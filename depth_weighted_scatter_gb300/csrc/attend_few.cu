@@ -343,11 +343,10 @@ cudaError_t launch_attend_few(const AttnArgs &a, const AttnPlan &pl) {
     auto run = [&](auto t, auto e4m3, auto d) {
         constexpr bool E = decltype(e4m3)::value;
         constexpr int D = decltype(d)::value;
-        auto *kernel = k_attend_few<decltype(t), E, D>;
         constexpr int smem = FewShape<E, D>::SMEM;
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        const cudaError_t e = allow_smem<&k_attend_few<decltype(t), E, D>>(smem);
         if (e != cudaSuccess) return e;
-        kernel<<<dim3(static_cast<unsigned>(pl.n_chunks), static_cast<unsigned>(a.Hk), static_cast<unsigned>(a.pg.n_seqs)),
+        k_attend_few<decltype(t), E, D><<<dim3(static_cast<unsigned>(pl.n_chunks), static_cast<unsigned>(a.Hk), static_cast<unsigned>(a.pg.n_seqs)),
                  kFewWarps * 32, smem, a.stream>>>(a, pl);
         count_launch();
         return cudaGetLastError();

@@ -49,9 +49,9 @@ struct TileShape {
     static constexpr int FIRST_LOADER = E4M3 ? 12 : 9;
     static constexpr int THREADS = E4M3 ? 512 : 384;
     static constexpr int LAUNCH_REGS = E4M3 ? 128 : 168;
-    static constexpr int SOFTMAX_REGS = E4M3 ? 200 : 208;
-    static constexpr int PRODUCT_REGS = E4M3 ? 32 : 80;
-    static constexpr int LOADER_REGS = 80;
+    static constexpr int SOFTMAX_REGS = E4M3 ? 192 : 208;
+    static constexpr int PRODUCT_REGS = E4M3 ? 56 : 80;
+    static constexpr int LOADER_REGS = 72;
     static_assert(256 * SOFTMAX_REGS + 128 * PRODUCT_REGS + (E4M3 ? 128 * LOADER_REGS : 0) <= THREADS * LAUNCH_REGS,
                   "the split is within the launch's registers");
     static constexpr int HALVES = D / 64;                                  // 128-byte columns of a block
@@ -621,10 +621,9 @@ cudaError_t launch_attend_tile(const AttnArgs &a, const AttnPlan &pl) {
         constexpr bool E = decltype(e4m3)::value;
         constexpr int D = decltype(d)::value;
         using S = TileShape<E, D>;
-        auto *kernel = k_attend_tile<decltype(t), E, D>;
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
+        const cudaError_t e = allow_smem<&k_attend_tile<decltype(t), E, D>>(S::SMEM);
         if (e != cudaSuccess) return e;
-        kernel<<<dim3(static_cast<unsigned>(div_up(pl.rows, 2 * kTileRows) * a.Hk), static_cast<unsigned>(pl.n_chunks),
+        k_attend_tile<decltype(t), E, D><<<dim3(static_cast<unsigned>(div_up(pl.rows, 2 * kTileRows) * a.Hk), static_cast<unsigned>(pl.n_chunks),
                       static_cast<unsigned>(a.pg.n_seqs)),
                  S::THREADS, S::SMEM, a.stream>>>(a, pl, k_map, v_map);
         count_launch();

@@ -127,21 +127,34 @@ def test_helpers_refuse(A):
     """The tensor helpers check types and shapes before the call (CPU tensors are refused)."""
     from depth_weighted_scatter_gb300.bevpool import BevpoolError
 
+    def refused(fn, *args, **kw):
+        with pytest.raises(BevpoolError):
+            fn(*args, **kw)
+
     q = torch.zeros(3, 4, 64, dtype=torch.float16)
-    with pytest.raises(BevpoolError):
-        A._heads("q", q)
-    with pytest.raises(BevpoolError):
-        A._position_args(q, torch.zeros(3, 5, dtype=torch.int32), torch.zeros(32), [1] * 5, False)
-    with pytest.raises(BevpoolError):
-        A._position_args(q, torch.zeros(3, dtype=torch.int64), torch.zeros(32), None, False)
-    with pytest.raises(BevpoolError):
-        A._position_args(q, torch.zeros(3, 2, dtype=torch.int32), torch.zeros(32), [32], False)
+    pos, f = torch.zeros(3, dtype=torch.int32), torch.zeros(32)
+    refused(A.qk_norm_rope, q, q, pos, f)
+    refused(A.qk_norm_rope, q.float(), q.float(), pos, f)
+    refused(A.qk_norm_rope, q[0], q[0], pos, f)
+    refused(A.qk_norm_rope_backward, q, q, q, q, pos, f)
+    assert A._heads("q", q, (3, 4, 64), torch.float16, -1)[1:] == (256, 64)
+    refused(A._heads, "q", q, (3, 4, 64), torch.bfloat16, -1)
+    refused(A._heads, "q", q, (3, 2, 64), torch.float16, -1)
+    refused(A._heads, "q", q, (3, 4, 64), torch.float16, 0)
+    refused(A._heads, "q", torch.zeros(3, 64, 4, dtype=torch.float16).transpose(1, 2), (3, 4, 64), torch.float16, -1)
+    assert A._position_args(3, -1, pos, f, None, True)[1] == 1
+    refused(A._position_args, 3, -1, torch.zeros(3, 5, dtype=torch.int32), f, [1] * 5, False)
+    refused(A._position_args, 3, -1, pos.long(), f, None, False)
+    refused(A._position_args, 2, -1, pos, f, None, False)
+    refused(A._position_args, 3, -1, torch.zeros(3, 2, dtype=torch.int32), f, [32], False)
+    refused(A._position_args, 3, -1, pos, f.double(), None, False)
     c = torch.zeros(4, 2, 16, 64, dtype=torch.float16)
     t, n, cu = torch.zeros(3, 2, dtype=torch.int32), torch.zeros(3, dtype=torch.int32), torch.zeros(4, dtype=torch.int32)
-    assert A._cache_args(c, c.clone(), t, n, cu, q, 2)[0] == 0
+    assert A._cache_args(c, c.clone(), t, n, cu, -1, 2, 64)[0] == 0
     for bad in [(c, c[:3], t, n, cu), (c, c.float(), t, n, cu), (c.float(), c.float(), t, n, cu), (c, c, t, n, cu[:3]),
-                (c, c, t, n.long(), cu), (c, c, t.t(), n, cu), (c, c.transpose(1, 2).contiguous().transpose(1, 2), t, n, cu)]:
-        with pytest.raises(BevpoolError):
-            A._cache_args(*bad, q, 2)
-    with pytest.raises(BevpoolError):
-        A._cache_args(c, c, t, n, cu, q, 4)
+                (c, c, t, n.long(), cu), (c, c, t.t(), n, cu), (c, c, t[0], n, cu), (c[0], c[0], t, n, cu),
+                (c, c.transpose(1, 2).contiguous().transpose(1, 2), t, n, cu)]:
+        refused(A._cache_args, *bad, -1, 2, 64)
+    refused(A._cache_args, c, c, t, n, cu, -1, 4, 64)
+    refused(A._cache_args, c, c, t, n, cu, -1, 2, 128)
+    refused(A._cache_args, c, c, t, n, cu, 0, 2, 64)
