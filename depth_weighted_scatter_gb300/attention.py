@@ -206,9 +206,9 @@ def qk_norm_rope(q, k, positions, inv_freq, *, sections=None, q_weight=None, k_w
     qw, kw = _vector("q_weight", q_weight, D, _F32, dev), _vector("k_weight", k_weight, D, _F32, dev)
     qa, ka = _heads("q", q, qs, dtype, dev), _heads("k", k, ks, dtype, dev)
     if q_out is None:
-        q_out = q.new_empty(qs)
+        q_out = torch.empty(qs, dtype=dtype, device=q.device)
     if k_out is None:
-        k_out = k.new_empty(ks)
+        k_out = torch.empty(ks, dtype=dtype, device=q.device)
     st = _lib.bevpool_qk_norm_rope(code, *qa, *ka, T, Hq, ks[1], D, qw, kw, eps, *pos,
                                    *_heads("q_out", q_out, qs, dtype, dev), *_heads("k_out", k_out, ks, dtype, dev),
                                    torch._C._cuda_getCurrentRawStream(dev))
@@ -235,9 +235,9 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, positions, inv_freq, *, sections
     ga, ha = _heads("dq_out", dq_out, qs, dtype, dev), _heads("dk_out", dk_out, ks, dtype, dev)
     qa, ka = _heads("q", q, qs, dtype, dev), _heads("k", k, ks, dtype, dev)
     if dq is None:
-        dq = q.new_empty(qs)
+        dq = torch.empty(qs, dtype=dtype, device=q.device)
     if dk is None:
-        dk = k.new_empty(ks)
+        dk = torch.empty(ks, dtype=dtype, device=q.device)
     dqw = None if qw is None else torch.empty_like(q_weight)
     dkw = None if kw is None else torch.empty_like(k_weight)
     if workspace is None and not (qw is None and kw is None):
@@ -275,7 +275,7 @@ def kv_append(k, v, k_cache, v_cache, block_table, kv_len, cu_q, positions, inv_
         qs = (T, Hq, D)
         qa = _heads("q", q, qs, dtype, dev)
         if q_out is None:
-            q_out = q.new_empty(qs)
+            q_out = torch.empty(qs, dtype=dtype, device=q.device)
         oa = _heads("q_out", q_out, qs, dtype, dev)
     elif q_out is not None:
         _refuse("q_out without q")
@@ -305,7 +305,7 @@ def paged_attention(q, k_cache, v_cache, block_table, kv_len, cu_q, *, max_q_len
     cache_code, ptrs, pages = _cache_args(k_cache, v_cache, block_table, kv_len, cu_q, dev, None, D)
     Hk = k_cache.shape[1]
     if out is None:
-        out = q.new_empty(qs)
+        out = torch.empty(qs, dtype=dtype, device=q.device)
     lse = torch.empty((T, Hq), dtype=_F32, device=q.device) if return_lse else None
     if workspace is None:
         n = _lib.bevpool_paged_attention_workspace_size(pages[9], T, Hq, Hk, D, max_q_len, max_kv_len, window)

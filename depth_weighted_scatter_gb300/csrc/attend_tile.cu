@@ -28,6 +28,7 @@
 #include <cuda.h>
 
 #include "paged_attention.cuh"
+#include "packed.cuh"
 #include "tcgen05.cuh"
 
 namespace bevpool {

@@ -16,121 +16,61 @@ namespace bevpool {
 
 namespace {
 
-// Rows of one kind (q or k) that a warp takes in one step.
-template <int LPR>
-constexpr int kRowsPerStep = 32 / LPR;
+constexpr int kForwardDepth = 8, kBackDepth = 4;  // steps in flight a warp
 
-// Steps of a token: ceil(H / rows per step) for q, then for k.
-template <int LPR>
-__host__ __device__ __forceinline__ int steps_of(int H) {
-    return (H + kRowsPerStep<LPR> - 1) / kRowsPerStep<LPR>;
-}
-
-template <typename T, int LPR, bool IL>
-__device__ __forceinline__ void forward_rows(const HeadRows &in, const HeadRowsOut &out, int64_t t, int H, int s0, int s1,
-                                             int c, int rg, bool live, int src, bool turned, const float *cs,
-                                             const float *sn, const float *w, int cp, int D, float eps) {
-    constexpr int U = 4;                                   // rows in flight a lane
-    float a[8], b[8];
-    if (live) row_coefs(cs, sn, w, c, cp, IL, a, b);
-    const T *ip = static_cast<const T *>(in.p) + t * in.token_stride + c * 8;
-    T *op = static_cast<T *>(out.p) + t * out.token_stride + c * 8;
-    const float inv_d = 1.0f / static_cast<float>(D);
-    for (int s = s0; s < s1; s += U) {
-        uint4 x[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int h = (s + u) * kRowsPerStep<LPR> + rg;
-            const bool on = live && s + u < s1 && h < H;
-            x[u] = on ? *reinterpret_cast<const uint4 *>(ip + h * in.head_stride) : make_uint4(0, 0, 0, 0);
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (s + u >= s1) break;                        // the same for the whole warp
-            const int h = (s + u) * kRowsPerStep<LPR> + rg;
-            float y[8];
-            turn_row<T, LPR, IL>(x[u], src, turned, a, b, w != nullptr, inv_d, eps, y);
-            if (live && h < H) *reinterpret_cast<uint4 *>(op + h * out.head_stride) = pack8<T>(y);
-        }
-    }
-}
-
-template <typename T, int LPR, bool IL>
-__global__ void __launch_bounds__(kThreads)
+template <typename T, int LPR, bool IL, bool FULL>
+__global__ void __launch_bounds__(kThreads, 3)
 k_norm_rope(NormRopeArgs a, int split) {
-    __shared__ unsigned long long turns[kMaxHeadDim / 2];
-    load_turns(a.rot, turns);
-    __syncthreads();
-    const int lane = threadIdx.x & 31, c = lane % LPR, rg = lane / LPR;
-    const bool live = c * 8 < a.D;
-    const int src = partner_lane<IL>(a.rot, c, lane), cp = c + src - lane;
-    const bool turned = c * 8 < a.rot.rotary_dim;
-    const int nq = steps_of<LPR>(a.Hq), n = nq + steps_of<LPR>(a.Hk);
-    const int64_t units = static_cast<int64_t>(a.T) * split;
-    for (int64_t u = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5); u < units;
-         u += static_cast<int64_t>(gridDim.x) * kWarps) {
-        const int64_t t = u / split;
-        const int part = static_cast<int>(u - t * split);
-        const int s0 = part * n / split, s1 = (part + 1) * n / split;
-        float cs[8], sn[8];
-        lane_cos_sin<IL>(a.rot, turns, t, c, cs, sn);
-        if (s0 < nq)
-            forward_rows<T, LPR, IL>(a.q, a.q_out, t, a.Hq, s0, min(s1, nq), c, rg, live, src, turned, cs, sn, a.q_weight,
-                                     cp, a.D, a.eps);
-        if (s1 > nq)
-            forward_rows<T, LPR, IL>(a.k, a.k_out, t, a.Hk, max(s0 - nq, 0), s1 - nq, c, rg, live, src, turned, cs, sn,
-                                     a.k_weight, cp, a.D, a.eps);
+    using Stream = RowStream<LPR, 2, 1, kForwardDepth>;
+    __shared__ __align__(16) RowWeights weights;
+    __shared__ __align__(16) uint8_t ring[kWarps * Stream::BYTES];
+    __shared__ typename Stream::Part parts[2];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, rg = lane / LPR;
+    weights.load(a.q_weight, a.k_weight, a.D);
+    if (threadIdx.x == 0) {
+        parts[0].set(0, a.q);
+        parts[1].set(0, a.k);
+        parts[0].H = a.Hq, parts[0].end = steps_of<LPR>(a.Hq);
+        parts[1].H = a.Hk, parts[1].end = parts[0].end + steps_of<LPR>(a.Hk);
     }
-}
-
-template <typename T, int LPR, bool IL>
-__device__ __forceinline__ void backward_rows(const HeadRows &grad, const HeadRows &in, const HeadRowsOut &out, int64_t t,
-                                              int H, int s0, int s1, int c, int rg, bool live, int src, bool turned,
-                                              const float *cs, const float *sn, const float *w, int D, float eps,
-                                              float *dw) {
-    constexpr int U = 2;                                   // rows in flight a lane, two loads each
-    const T *gp = static_cast<const T *>(grad.p) + t * grad.token_stride + c * 8;
-    const T *ip = static_cast<const T *>(in.p) + t * in.token_stride + c * 8;
-    T *op = static_cast<T *>(out.p) + t * out.token_stride + c * 8;
-    const float inv_d = 1.0f / static_cast<float>(D);
-    float wt[8];
+    const LaneRow p = lane_row<IL>(a.rot, a.D, lane % LPR);
+    LaneTurns<LPR> turns(a.rot, p, rg);
+    __syncthreads();
+    const Units units(a.T, split);
+    if (units.first < units.n) turns.read(a.rot, units.token(units.first));
+    Stream in(units, parts, static_cast<uint32_t>(__cvta_generic_to_shared(ring)) + warp * Stream::BYTES, p, rg, a.D);
+    const float inv_d = 1.0f / static_cast<float>(a.D);
+    const int nq = parts[0].end, steps = parts[1].end;
+    for (uint32_t u = units.first; u < units.n; u += units.stride) {
+        const int64_t t = units.token(u);
+        int s0, s1;
+        units.steps(u, steps, &s0, &s1);
+        float cs[4], sn[4];
+        turns.cos_sin(p, cs, sn);
+        if (units.n - u > units.stride) turns.read(a.rot, units.token(u + units.stride));
 #pragma unroll
-    for (int i = 0; i < 8; ++i) wt[i] = live && w ? w[c * 8 + i] : 1.0f;
-    for (int s = s0; s < s1; s += U) {
-        uint4 gw[U], xw[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int h = (s + u) * kRowsPerStep<LPR> + rg;
-            const bool on = live && s + u < s1 && h < H;
-            gw[u] = on ? *reinterpret_cast<const uint4 *>(gp + h * grad.head_stride) : make_uint4(0, 0, 0, 0);
-            xw[u] = on && w ? *reinterpret_cast<const uint4 *>(ip + h * in.head_stride) : make_uint4(0, 0, 0, 0);
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (s + u >= s1) break;                        // the same for the whole warp
-            const int h = (s + u) * kRowsPerStep<LPR> + rg;
-            float g[8], gx[8], x[8];
-            const uint4 pw = partner_words<IL>(gw[u], src);
-            unpack8<T>(gw[u], g);
-            unpack8<T>(pw, gx);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) g[i] = turned ? fmaf(-sn[i], gx[i], cs[i] * g[i]) : g[i];
-            if (w) {                                       // the same for the whole grid
-                unpack8<T>(xw[u], x);
-                const float r = row_rstd<LPR>(x, inv_d, eps);
-                float dot = 0.0f;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    x[i] *= r;                             // xh
-                    dw[i] = fmaf(g[i], x[i], dw[i]);
-                    g[i] *= wt[i];
-                    dot = fmaf(g[i], x[i], dot);
-                }
-                dot = row_sum<LPR>(dot) * inv_d;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) g[i] = r * fmaf(-x[i], dot, g[i]);
+        for (int part = 0; part < 2; ++part) {
+            const int end = part ? s1 : min(s1, nq), first = part ? max(s0, nq) : s0;
+            if (first >= end) continue;
+            uint64_t fa[4], fb[4];
+            float wu[4], wv[4];
+            lane_weights(weights.w[part], p, wu, wv);
+            lane_factors<IL>(cs, sn, wu, wv, fa, fb);
+            const HeadRowsOut &o = part ? a.k_out : a.q_out;
+            const bool norm = (part ? a.k_weight : a.q_weight) != nullptr;
+            const int H = part ? a.Hk : a.Hq;
+            const int h = (part ? first - nq : first) * Stream::RPS + rg;
+            int rows = p.live ? (H - h + Stream::RPS - 1) / Stream::RPS : 0;   // steps in which this lane has a row
+            T *op = static_cast<T *>(o.p) + t * o.token_stride + h * o.head_stride;
+            const int64_t step = Stream::RPS * o.head_stride;
+            for (int s = first; s < end; ++s) {
+                LaneWords x;
+                in.next(&x);
+                uint64_t y[4];
+                turn_row<T, LPR, IL, FULL>(x, p, fa, fb, norm, inv_d, a.eps, y);
+                if (rows-- > 0) store_lane<IL, T>(op, p, y);
+                op += step;
             }
-            if (live && h < H) *reinterpret_cast<uint4 *>(op + h * out.head_stride) = pack8<T>(g);
         }
     }
 }
@@ -138,55 +78,120 @@ __device__ __forceinline__ void backward_rows(const HeadRows &grad, const HeadRo
 // The weights' gradients are summed over a lane's rows in registers, over a
 // warp by shuffles, over a CTA in shared memory, and over CTAs by k_sum_dw,
 // always in the same order.
-template <typename T, int LPR, bool IL>
-__global__ void __launch_bounds__(kThreads)
+template <typename T, int LPR, bool IL, bool FULL>
+__global__ void __launch_bounds__(kThreads, 2)
 k_norm_rope_back(NormRopeBackArgs a, int split) {
-    __shared__ unsigned long long turns[kMaxHeadDim / 2];
-    __shared__ float sums[kWarps][2][LPR * 8];
+    using Stream = RowStream<LPR, 2, 2, kBackDepth>;
+    __shared__ __align__(16) RowWeights weights;
+    __shared__ __align__(16) uint8_t ring[kWarps * Stream::BYTES];
+    __shared__ typename Stream::Part parts[2];
+    static_assert(sizeof(ring) >= kWarps * 2 * LPR * 8 * sizeof(float), "the warps' sums fit the ring");
     const NormRopeArgs &f = a.f;
-    load_turns(f.rot, turns);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, rg = lane / LPR;
+    weights.load(f.q_weight, f.k_weight, f.D);
+    if (threadIdx.x == 0) {
+        // without a norm the inputs are not needed: the gradient's rows stand in
+        parts[0].set(0, a.dq_out);
+        parts[0].set(1, f.q_weight ? f.q : a.dq_out);
+        parts[1].set(0, a.dk_out);
+        parts[1].set(1, f.k_weight ? f.k : a.dk_out);
+        parts[0].H = f.Hq, parts[0].end = steps_of<LPR>(f.Hq);
+        parts[1].H = f.Hk, parts[1].end = parts[0].end + steps_of<LPR>(f.Hk);
+    }
+    const LaneRow p = lane_row<IL>(f.rot, f.D, lane % LPR);
+    LaneTurns<LPR> turns(f.rot, p, rg);
     __syncthreads();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = lane % LPR, rg = lane / LPR;
-    const bool live = c * 8 < f.D;
-    const int src = partner_lane<IL>(f.rot, c, lane);
-    const bool turned = c * 8 < f.rot.rotary_dim;
-    const int nq = steps_of<LPR>(f.Hq), n = nq + steps_of<LPR>(f.Hk);
-    const int64_t units = static_cast<int64_t>(f.T) * split;
-    float dwq[8] = {}, dwk[8] = {};
-    for (int64_t u = static_cast<int64_t>(blockIdx.x) * kWarps + warp; u < units;
-         u += static_cast<int64_t>(gridDim.x) * kWarps) {
-        const int64_t t = u / split;
-        const int part = static_cast<int>(u - t * split);
-        const int s0 = part * n / split, s1 = (part + 1) * n / split;
-        float cs[8], sn[8];
-        lane_cos_sin<IL>(f.rot, turns, t, c, cs, sn);
-        if (s0 < nq)
-            backward_rows<T, LPR, IL>(a.dq_out, f.q, f.q_out, t, f.Hq, s0, min(s1, nq), c, rg, live, src, turned, cs, sn,
-                                      f.q_weight, f.D, f.eps, dwq);
-        if (s1 > nq)
-            backward_rows<T, LPR, IL>(a.dk_out, f.k, f.k_out, t, f.Hk, max(s0 - nq, 0), s1 - nq, c, rg, live, src, turned,
-                                      cs, sn, f.k_weight, f.D, f.eps, dwk);
+    const Units units(f.T, split);
+    if (units.first < units.n) turns.read(f.rot, units.token(units.first));
+    Stream in(units, parts, static_cast<uint32_t>(__cvta_generic_to_shared(ring)) + warp * Stream::BYTES, p, rg, f.D);
+    const float inv_d = 1.0f / static_cast<float>(f.D);
+    const int nq = parts[0].end, steps = parts[1].end;
+    uint64_t dw[2][4] = {};                                // all bits zero: two FP32 zeros
+    for (uint32_t u = units.first; u < units.n; u += units.stride) {
+        const int64_t t = units.token(u);
+        int s0, s1;
+        units.steps(u, steps, &s0, &s1);
+        float cs[4], sn[4];
+        turns.cos_sin(p, cs, sn);
+        if (units.n - u > units.stride) turns.read(f.rot, units.token(u + units.stride));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sn[i] = -sn[i];        // the turn by the negative angle
+        const float one[4] = {1.0f, 1.0f, 1.0f, 1.0f};
+        uint64_t fa[4], fb[4];
+        lane_factors<IL>(cs, sn, one, one, fa, fb);
+#pragma unroll
+        for (int part = 0; part < 2; ++part) {
+            const int end = part ? s1 : min(s1, nq), first = part ? max(s0, nq) : s0;
+            if (first >= end) continue;
+            float wu[4], wv[4];
+            lane_weights(weights.w[part], p, wu, wv);
+            const uint64_t wt[4] = {pair(wu[0], wu[1]), pair(wu[2], wu[3]), pair(wv[0], wv[1]), pair(wv[2], wv[3])};
+            const HeadRowsOut &o = part ? f.k_out : f.q_out;
+            const bool norm = (part ? f.k_weight : f.q_weight) != nullptr;
+            const int H = part ? f.Hk : f.Hq;
+            const int h = (part ? first - nq : first) * Stream::RPS + rg;
+            int rows = p.live ? (H - h + Stream::RPS - 1) / Stream::RPS : 0;   // steps in which this lane has a row
+            T *op = static_cast<T *>(o.p) + t * o.token_stride + h * o.head_stride;
+            const int64_t step = Stream::RPS * o.head_stride;
+            for (int s = first; s < end; ++s) {
+                LaneWords r[2];
+                in.next(r);
+                uint64_t d[4], g[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) d[i] = widen<T>(r[0].w[i]);
+                turn_lane<IL, FULL>(d, fa, fb, p.turned, g);
+                if (norm) {                                // the same for the whole grid
+                    uint64_t x[4], m[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        x[i] = widen<T>(r[1].w[i]);
+                        m[i] = mul2(g[i], wt[i]);
+                    }
+                    // both sums of the row at once: x^2, and g w x
+                    float sq = lane_dot(x, x), dot = lane_dot(m, x);
+#pragma unroll
+                    for (int k = LPR / 2; k > 0; k >>= 1) {
+                        sq += __shfl_xor_sync(0xffffffffu, sq, k);
+                        dot += __shfl_xor_sync(0xffffffffu, dot, k);
+                    }
+                    const float rs = rsqrtf(fmaf(sq, inv_d, f.eps));
+                    const float c = -dot * inv_d * rs * rs;
+                    const uint64_t r2 = pair(rs, rs), c2 = pair(c, c);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        dw[part][i] = fma2(mul2(x[i], r2), g[i], dw[part][i]);
+                        g[i] = mul2(fma2(x[i], c2, m[i]), r2);         // rs (g w - xh mean(g w xh))
+                    }
+                }
+                if (rows-- > 0) store_lane<IL, T>(op, p, g);
+                op += step;
+            }
+        }
     }
     grid_dep_allow();
     if (!f.q_weight && !f.k_weight) return;
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncthreads();
+    float *sums = reinterpret_cast<float *>(ring);         // [warp][2][LPR * 8]
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int part = 0; part < 2; ++part)
 #pragma unroll
-        for (int o = LPR; o < 32; o <<= 1) {
-            dwq[i] += __shfl_xor_sync(0xffffffffu, dwq[i], o);
-            dwk[i] += __shfl_xor_sync(0xffffffffu, dwk[i], o);
+        for (int i = 0; i < 4; ++i) {
+            float v[2];
+            unpair(dw[part][i], &v[0], &v[1]);
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+#pragma unroll
+                for (int k = LPR; k < 32; k <<= 1) v[x] += __shfl_xor_sync(0xffffffffu, v[x], k);
+                if (rg == 0 && p.live) sums[(warp * 2 + part) * (LPR * 8) + (i < 2 ? p.e0 : p.e1) + 2 * (i & 1) + x] = v[x];
+            }
         }
-        if (rg == 0) {
-            sums[warp][0][c * 8 + i] = dwq[i];
-            sums[warp][1][c * 8 + i] = dwk[i];
-        }
-    }
     __syncthreads();
     for (int j = threadIdx.x; j < 2 * f.D; j += kThreads) {
-        const int which = j >= f.D ? 1 : 0, d = j - which * f.D;
+        const int part = j >= f.D ? 1 : 0, d = j - part * f.D;
         float s = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) s += sums[w][which][d];
+        for (int w = 0; w < kWarps; ++w) s += sums[(w * 2 + part) * (LPR * 8) + d];
         a.partial[static_cast<int64_t>(blockIdx.x) * 2 * f.D + j] = s;
     }
 }
@@ -231,13 +236,16 @@ int steps_for(int D, int H) {
     return (H + rows - 1) / rows;
 }
 
-constexpr int64_t kForwardCtasMax = 152 * 8;               // 8 CTAs of 256 threads an SM
-constexpr int64_t kBackCtasMax = 152 * 4;
+constexpr int64_t kForwardCtasMax = 152 * 3;               // 3 CTAs of 256 threads an SM, one wave
+constexpr int64_t kBackCtasMax = 152 * 2;
 
 template <typename F>
-cudaError_t with_shape(int dtype, int D, bool il, F &&f) {
+cudaError_t with_shape(int dtype, int D, const RotaryArgs &r, F &&f) {
+    auto by_full = [&](auto t, auto lpr, auto il) {
+        return r.rotary_dim == D ? f(t, lpr, il, std::true_type{}) : f(t, lpr, il, std::false_type{});
+    };
     auto by_il = [&](auto t, auto lpr) {
-        return il ? f(t, lpr, std::true_type{}) : f(t, lpr, std::false_type{});
+        return r.interleaved ? by_full(t, lpr, std::true_type{}) : by_full(t, lpr, std::false_type{});
     };
     auto by_lpr = [&](auto t) {
         switch (lanes_per_row(D)) {
@@ -256,8 +264,8 @@ cudaError_t launch_norm_rope(const NormRopeArgs &a) {
     const int split = split_of(a.T, steps_for(a.D, a.Hq) + steps_for(a.D, a.Hk));
     int64_t grid = div_up(static_cast<int64_t>(a.T) * split, kWarps);
     if (grid > kForwardCtasMax) grid = kForwardCtasMax;
-    return with_shape(a.dtype, a.D, a.rot.interleaved != 0, [&](auto t, auto lpr, auto il) {
-        k_norm_rope<decltype(t), decltype(lpr)::value, decltype(il)::value>
+    return with_shape(a.dtype, a.D, a.rot, [&](auto t, auto lpr, auto il, auto full) {
+        k_norm_rope<decltype(t), decltype(lpr)::value, decltype(il)::value, decltype(full)::value>
             <<<static_cast<int>(grid), kThreads, 0, a.stream>>>(a, split);
         count_launch();
         return cudaGetLastError();
@@ -275,8 +283,8 @@ cudaError_t launch_norm_rope_back(const NormRopeBackArgs &a) {
     const int split = split_of(f.T, steps_for(f.D, f.Hq) + steps_for(f.D, f.Hk));
     const int grid = norm_rope_back_ctas(f.T, f.Hq, f.Hk, f.D);
     if (grid > 0) {
-        const cudaError_t e = with_shape(f.dtype, f.D, f.rot.interleaved != 0, [&](auto t, auto lpr, auto il) {
-            k_norm_rope_back<decltype(t), decltype(lpr)::value, decltype(il)::value>
+        const cudaError_t e = with_shape(f.dtype, f.D, f.rot, [&](auto t, auto lpr, auto il, auto full) {
+            k_norm_rope_back<decltype(t), decltype(lpr)::value, decltype(il)::value, decltype(full)::value>
                 <<<grid, kThreads, 0, f.stream>>>(a, split);
             count_launch();
             return cudaGetLastError();

@@ -234,8 +234,8 @@ bevpool_status bevpool_kv_append(
     g.cache_e4m3 = e4m3;
     g.k_cache = k_cache;
     g.v_cache = v_cache;
-    g.k_scale = k_scale;
-    g.v_scale = v_scale;
+    g.k_inv = 1.0f / k_scale;
+    g.v_inv = 1.0f / v_scale;
     return cuda_status(launch_kv_append(g));
 }
 
