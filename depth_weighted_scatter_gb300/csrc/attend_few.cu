@@ -13,7 +13,14 @@
 // E4M3 codes stay codes in shared memory and are widened in registers.  For
 // K a thread's four consecutive codes serve as its four places along the
 // product's inner axis (Q is loaded in the same order); for V a transposed
-// load of 2-byte units yields two columns at once.
+// load of 2-byte units yields two columns at once.  Both products are then of
+// fp16, which holds every code and is one conversion away (bf16 would be four):
+// a bf16 query row is first scaled by the power of two that brings its largest
+// element to 2^14 (elements 2^-31 of it and more keep all their bits), and its
+// scores by the inverse.
+//
+// fp16 weights carry a factor of 2^14, so that they keep 11 bits down to 2^-28
+// of the largest.
 #include "paged_attention.cuh"
 
 namespace bevpool {
@@ -79,6 +86,8 @@ template <typename T, bool E4M3, int D>
 __global__ void __launch_bounds__(kFewWarps * 32, 2)
 k_attend_few(AttnArgs a, AttnPlan pl) {
     using S = FewShape<E4M3, D>;
+    using M = typename std::conditional<E4M3, __half, T>::type;             // type of both products
+    constexpr float kLift = std::is_same<M, __half>::value ? 14.0f : 0.0f;  // log2 of the weights' factor
     constexpr int KS = D / 16, NT = D / 8, KG = S::KT / 16;                // k steps of S, columns tiles of O, 16-key groups
     extern __shared__ __align__(128) uint8_t smem[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, qd = lane & 3;
@@ -106,6 +115,29 @@ k_attend_few(AttnArgs a, AttnPlan pl) {
         for (int k = 0; k < KS; ++k) {
             qf[k][x] = *reinterpret_cast<const uint32_t *>(qp + 16 * k + (E4M3 ? 4 * qd : 2 * qd));
             qf[k][x + 2] = *reinterpret_cast<const uint32_t *>(qp + 16 * k + (E4M3 ? 4 * qd + 2 : 2 * qd + 8));
+        }
+    }
+    // scale of a row's scores (base 2)
+    float scale[2] = {a.scale_log2, a.scale_log2};
+    if constexpr (E4M3 && !std::is_same<T, __half>::value) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            float top = 0.0f;
+#pragma unroll
+            for (int k = 0; k < KS; ++k)
+#pragma unroll
+                for (int y = x; y < 4; y += 2)
+                    top = fmaxf(top, fmaxf(fabsf(__uint_as_float(qf[k][y] << 16)), fabsf(__uint_as_float(qf[k][y] & 0xffff0000u))));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            const int e = min(max(static_cast<int>(__float_as_uint(top) >> 23) - 127, -100), 100);     // its exponent
+            const float up = __uint_as_float(static_cast<uint32_t>(127 + 14 - e) << 23);               // 2^(14 - e)
+            scale[x] *= __uint_as_float(static_cast<uint32_t>(127 - 14 + e) << 23);
+#pragma unroll
+            for (int k = 0; k < KS; ++k)
+#pragma unroll
+                for (int y = x; y < 4; y += 2)
+                    qf[k][y] = pack2<__half>(__uint_as_float(qf[k][y] << 16) * up, __uint_as_float(qf[k][y] & 0xffff0000u) * up);
         }
     }
     int32_t first, last, tmp;                              // keys that any row sees
@@ -194,10 +226,10 @@ k_attend_few(AttnArgs a, AttnPlan pl) {
                 ldm4(kt + row * S::RB + S::swz(row, c + piece) * 16, w);
                 if constexpr (E4M3) {
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) mma<T>(s[n], qf[c + x], widen2<T>(w[x] & 0xffff), widen2<T>(w[x] >> 16));
+                    for (int x = 0; x < 4; ++x) mma<M>(s[n], qf[c + x], widen2<M>(w[x] & 0xffff), widen2<M>(w[x] >> 16));
                 } else {
-                    mma<T>(s[n], qf[c / 2], w[0], w[1]);
-                    mma<T>(s[n], qf[c / 2 + 1], w[2], w[3]);
+                    mma<M>(s[n], qf[c / 2], w[0], w[1]);
+                    mma<M>(s[n], qf[c / 2 + 1], w[2], w[3]);
                 }
             }
         }
@@ -206,7 +238,7 @@ k_attend_few(AttnArgs a, AttnPlan pl) {
 #pragma unroll
         for (int n = 0; n < S::KT / 8; ++n)
 #pragma unroll
-            for (int x = 0; x < 4; ++x) s[n][x] *= a.scale_log2;
+            for (int x = 0; x < 4; ++x) s[n][x] *= scale[x >> 1];
         if (!__all_sync(0xffffffffu, whole)) {
 #pragma unroll
             for (int n = 0; n < S::KT / 8; ++n)
@@ -228,8 +260,8 @@ k_attend_few(AttnArgs a, AttnPlan pl) {
         for (int x = 0; x < 2; ++x) {
             mn[x] = fmaxf(mn[x], __shfl_xor_sync(0xffffffffu, mn[x], 1));
             mn[x] = fmaxf(mn[x], __shfl_xor_sync(0xffffffffu, mn[x], 2));
-            from[x] = mn[x] == -INFINITY ? 0.0f : mn[x];
-            keep[x] = pow2(m[x] - from[x]);
+            from[x] = (mn[x] == -INFINITY ? 0.0f : mn[x]) - kLift;
+            keep[x] = pow2(m[x] - kLift - from[x]);
             l[x] *= keep[x];
         }
         if (__any_sync(0xffffffffu, mn[0] != m[0] || mn[1] != m[1])) {
@@ -254,8 +286,8 @@ k_attend_few(AttnArgs a, AttnPlan pl) {
                 const float p2 = pow2(s[2 * x + n][2] - from[1]), p3 = pow2(s[2 * x + n][3] - from[1]);
                 l[0] += p0 + p1;
                 l[1] += p2 + p3;
-                pf[2 * n] = pack2<T>(p0, p1);
-                pf[2 * n + 1] = pack2<T>(p2, p3);
+                pf[2 * n] = pack2<M>(p0, p1);
+                pf[2 * n + 1] = pack2<M>(p2, p3);
             }
             const int row = 16 * x + (lane & 15), piece = lane >> 4;
 #pragma unroll
@@ -266,13 +298,13 @@ k_attend_few(AttnArgs a, AttnPlan pl) {
 #pragma unroll
                     for (int y = 0; y < 2; ++y) {
                         const uint32_t w0 = w[2 * y], w1 = w[2 * y + 1];
-                        mma<T>(o[2 * (c + y)], pf, widen2<T>(__byte_perm(w0, 0, 0x4420)), widen2<T>(__byte_perm(w1, 0, 0x4420)));
-                        mma<T>(o[2 * (c + y) + 1], pf, widen2<T>(__byte_perm(w0, 0, 0x4431)),
-                               widen2<T>(__byte_perm(w1, 0, 0x4431)));
+                        mma<M>(o[2 * (c + y)], pf, widen2<M>(__byte_perm(w0, 0, 0x4420)), widen2<M>(__byte_perm(w1, 0, 0x4420)));
+                        mma<M>(o[2 * (c + y) + 1], pf, widen2<M>(__byte_perm(w0, 0, 0x4431)),
+                               widen2<M>(__byte_perm(w1, 0, 0x4431)));
                     }
                 } else {
-                    mma<T>(o[c], pf, w[0], w[1]);
-                    mma<T>(o[c + 1], pf, w[2], w[3]);
+                    mma<M>(o[c], pf, w[0], w[1]);
+                    mma<M>(o[c + 1], pf, w[2], w[3]);
                 }
             }
         }
@@ -293,7 +325,7 @@ k_attend_few(AttnArgs a, AttnPlan pl) {
         l[x] += __shfl_xor_sync(0xffffffffu, l[x], 2);
         const int row = g + 8 * x;
         if (qd == 0) {
-            sm[(warp * 16 + row) * 2] = m[x];
+            sm[(warp * 16 + row) * 2] = m[x] - kLift;
             sm[(warp * 16 + row) * 2 + 1] = l[x];
         }
 #pragma unroll
