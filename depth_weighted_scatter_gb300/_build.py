@@ -1,8 +1,11 @@
-"""Builds libbevpool.so in-tree with nvcc for sm_103a.
+"""Builds libbevpool.so in-tree with nvcc for sm_103a, and the native module
+_token_ops of the tensor helpers.
 
 Each .cu file under csrc/ is compiled in parallel to an object, then linked
 into depth_weighted_scatter_gb300/libbevpool.so against the shared CUDA
-runtime.  Rebuilds only when a source is newer than the library.
+runtime.  csrc/binding.cpp, compiled beside them by the host compiler against
+PyTorch's headers, becomes _token_ops.so, which calls the library.  Rebuilds
+only when a source is newer.
 """
 from __future__ import annotations
 
@@ -16,6 +19,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libbevpool.so")
+BINDING = os.path.join(HERE, "_token_ops.so")
 OBJDIR = os.path.join(ROOT, "_build")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CUDA_HOME = os.environ.get("CUDA_HOME", "/usr/local/cuda")
@@ -57,14 +61,64 @@ def _compile(src: str, extra: list) -> str:
     return obj
 
 
+def _binding_deps() -> list:
+    return [os.path.join(CSRC, "binding.cpp"), os.path.join(ROOT, "include", "bevpool.h"), os.path.abspath(__file__)]
+
+
+def binding_up_to_date() -> bool:
+    if not os.path.exists(BINDING):
+        return False
+    t = os.path.getmtime(BINDING)
+    return all(os.path.getmtime(d) <= t for d in _binding_deps())
+
+
+def _compile_binding() -> str:
+    import sysconfig
+
+    import torch
+
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    obj = os.path.join(OBJDIR, "binding.o")
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", inc,
+           "-I", os.path.join(inc, "torch", "csrc", "api", "include"), "-I", sysconfig.get_paths()["include"],
+           "-I", os.path.join(CUDA_HOME, "include"), "-c", os.path.join(CSRC, "binding.cpp"), "-o", obj]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for binding.cpp:\n{r.stdout}\n{r.stderr}")
+    return obj
+
+
+def _link_binding(obj: str) -> None:
+    import torch
+
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = ["g++", "-shared", "-o", tmp, obj, "-L", lib, "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda",
+           "-L", HERE, "-l:libbevpool.so", "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + lib]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link of the binding failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
+
+
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
-    """Compile every CUDA source and link libbevpool.so; returns its path."""
-    if not force and up_to_date():
-        return LIB
+    """Compile every source and link libbevpool.so and _token_ops.so; returns
+    the library's path."""
     os.makedirs(OBJDIR, exist_ok=True)
+    with concurrent.futures.ThreadPoolExecutor(max_workers=1) as ex:
+        binding = None if not force and binding_up_to_date() else ex.submit(_compile_binding)
+        if force or not up_to_date():
+            _build_library(verbose_ptxas)
+        if binding is not None:
+            _link_binding(binding.result())
+    return LIB
+
+
+def _build_library(verbose_ptxas: bool) -> str:
     extra = ["-Xptxas", "-v"] if verbose_ptxas else []
     srcs = _sources()
-    with concurrent.futures.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
+    with concurrent.futures.ThreadPoolExecutor(max_workers=min(16, len(srcs))) as ex:
         objs = list(ex.map(lambda s: _compile(s, extra), srcs))
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [nvcc()] + ARCH + ["-shared", "-cudart", "shared", "-o", tmp] + objs + [

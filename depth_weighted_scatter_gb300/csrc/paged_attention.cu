@@ -1,15 +1,25 @@
 // paged_attention.cu -- attention of new tokens over the paged cache: how a
 // call is laid out, and its launches.
+#include <cmath>
+
 #include "paged_attention.cuh"
 
 namespace bevpool {
 
 namespace {
 
-// CTAs that a few-rows call's chunks make of its longest requests: about four
-// for each of the two places of an SM, so that ragged lengths even out; the
-// partial results stay below 1 % of the cache's bytes.
-constexpr int64_t kFewCtas = 152 * 2 * 4;
+// CTAs that a few-rows call's chunks make of its longest requests.  An SM holds
+// two, so a multiple w of 304: each wave costs its start, about 4 us, while w
+// waves leave about 1 / (2 w) of the time t of the read to ragged lengths, so w
+// is near sqrt(t / 8 us); a lone request is not ragged.  Measured with w = 1 /
+// 2 / 4 / 8: one request of 40000 keys (8 key heads of 128, bf16) - / 41 / 49 /
+// 55 us, 64 of up to 8192 - / 248 / 240 / 236 us.
+int64_t few_ctas(int64_t keys, int64_t pairs, int32_t n_seqs, int32_t D) {
+    if (n_seqs == 1) return 152 * 2;
+    const double t = static_cast<double>(keys) * static_cast<double>(pairs) * D * 4 / 6.7e6;      // us, 16-bit cache
+    const int64_t w = static_cast<int64_t>(std::sqrt(t / 8) + 0.5);
+    return 152 * 2 * (w < 1 ? 1 : w > 6 ? 6 : w);
+}
 
 // What the plan of the few-rows kernel cuts keys by, and of the tiled one.
 constexpr int32_t kFewAlign = 64, kTileAlign = 128;
@@ -51,12 +61,12 @@ AttnPlan attention_plan(const AttnSizes &z) {
     pl.few = pl.rows <= 16;
     pl.align = pl.few ? kFewAlign : kTileAlign;
     const int64_t keys = keys_of(q_len, z.max_kv_len, z.window, pl.align), pairs = static_cast<int64_t>(z.n_seqs) * z.Hk;
-    int64_t chunk;
-    if (pl.few)
-        chunk = div_up(keys * pairs, kFewCtas);
+    int64_t n = 1;
+    if (pl.few && pairs > 0)
+        n = (few_ctas(keys, pairs, z.n_seqs, z.D) + pairs / 2) / pairs;
     else
-        chunk = div_up(keys, tile_chunks(div_up(pl.rows, 256) * pairs, keys));
-    chunk = div_up(chunk, pl.align) * pl.align;
+        n = tile_chunks(div_up(pl.rows, 256) * pairs, keys);
+    int64_t chunk = div_up(div_up(keys, n < 1 ? 1 : n), pl.align) * pl.align;
     if (chunk > keys) chunk = div_up(keys, pl.align) * pl.align;
     pl.chunk = static_cast<int32_t>(chunk);
     pl.n_chunks = static_cast<int32_t>(div_up(keys, chunk));

@@ -133,28 +133,62 @@ def test_helpers_refuse(A):
 
     q = torch.zeros(3, 4, 64, dtype=torch.float16)
     pos, f = torch.zeros(3, dtype=torch.int32), torch.zeros(32)
-    refused(A.qk_norm_rope, q, q, pos, f)
-    refused(A.qk_norm_rope, q.float(), q.float(), pos, f)
-    refused(A.qk_norm_rope, q[0], q[0], pos, f)
-    refused(A.qk_norm_rope_backward, q, q, q, q, pos, f)
-    assert A._heads("q", q, (3, 4, 64), torch.float16, -1)[1:] == (256, 64)
-    refused(A._heads, "q", q, (3, 4, 64), torch.bfloat16, -1)
-    refused(A._heads, "q", q, (3, 2, 64), torch.float16, -1)
-    refused(A._heads, "q", q, (3, 4, 64), torch.float16, 0)
-    refused(A._heads, "q", torch.zeros(3, 64, 4, dtype=torch.float16).transpose(1, 2), (3, 4, 64), torch.float16, -1)
-    assert A._position_args(3, -1, pos, f, None, True)[1] == 1
-    refused(A._position_args, 3, -1, torch.zeros(3, 5, dtype=torch.int32), f, [1] * 5, False)
-    refused(A._position_args, 3, -1, pos.long(), f, None, False)
-    refused(A._position_args, 2, -1, pos, f, None, False)
-    refused(A._position_args, 3, -1, torch.zeros(3, 2, dtype=torch.int32), f, [32], False)
-    refused(A._position_args, 3, -1, pos, f.double(), None, False)
-    c = torch.zeros(4, 2, 16, 64, dtype=torch.float16)
+    c = torch.zeros(4, 4, 16, 64, dtype=torch.float16)
     t, n, cu = torch.zeros(3, 2, dtype=torch.int32), torch.zeros(3, dtype=torch.int32), torch.zeros(4, dtype=torch.int32)
-    assert A._cache_args(c, c.clone(), t, n, cu, -1, 2, 64)[0] == 0
+    # no CUDA tensors
+    refused(A.qk_norm_rope, q, q, pos, f)
+    refused(A.qk_norm_rope_backward, q, q, q, q, pos, f)
+    refused(A.kv_append, q, q, c, c, t, n, cu, pos, f)
+    refused(A.paged_attention, q, c, c, t, n, cu, max_q_len=1, max_kv_len=4)
+    # no head tensors, no 16-bit type, no tensors
+    refused(A.qk_norm_rope, q[0], q[0], pos, f)
+    refused(A.qk_norm_rope, q.float(), q.float(), pos, f)
+    refused(A.qk_norm_rope, [1.0], q, pos, f)
+    refused(A.paged_attention, q, c, None, t, n, cu, max_q_len=1, max_kv_len=4)
+    with pytest.raises(BevpoolError) as e:
+        A.qk_norm_rope(q.double(), q, pos, f)
+    assert e.value.status == 3
+
+
+@pytest.mark.gpu
+def test_helpers_refuse_on_the_gpu(A):
+    """What does not match is refused before anything is enqueued."""
+    from depth_weighted_scatter_gb300.bevpool import BevpoolError
+
+    if not torch.cuda.is_available():
+        pytest.fail("GPU tests need a CUDA device")
+
+    def refused(fn, *args, **kw):
+        with pytest.raises(BevpoolError):
+            fn(*args, **kw)
+
+    z = lambda *s, dtype=torch.float16: torch.zeros(*s, dtype=dtype, device="cuda")  # noqa: E731
+    q, k, pos, f = z(3, 4, 64), z(3, 2, 64), z(3, dtype=torch.int32), z(32, dtype=torch.float32)
+    assert A.qk_norm_rope(q, k, pos, f)[0].shape == q.shape
+    for bad in [(q, k[:2], pos, f), (q, k.bfloat16(), pos, f), (q, k.cpu(), pos, f), (q, z(3, 64, 2).transpose(1, 2), pos, f),
+                (q, k, pos.long(), f), (q, k, pos[:2], f), (q, k, z(3, 5, dtype=torch.int32), f), (q, k, pos, f.double()),
+                (q, k, pos, f[:4]), (q, k, pos.cpu(), f), (q, k, z(3, 2, dtype=torch.int32), f)]:
+        refused(A.qk_norm_rope, *bad)
+    for more in [dict(sections=[31]), dict(sections=[16, 16]), dict(q_weight=z(64)), dict(k_weight=z(32, dtype=torch.float32)),
+                 dict(q_out=z(3, 2, 64)), dict(k_out=k.float()), dict(eps=-1.0)]:
+        refused(A.qk_norm_rope, q, k, pos, f, **more)
+    refused(A.qk_norm_rope_backward, k, k, q, k, pos, f)
+    w = z(64, dtype=torch.float32)
+    refused(A.qk_norm_rope_backward, q, k, q, k, pos, f, q_weight=w, workspace=z(16, dtype=torch.uint8))
+    c, t, n, cu = z(4, 2, 16, 64), z(3, 2, dtype=torch.int32), z(3, dtype=torch.int32), z(4, dtype=torch.int32)
+    assert A.paged_attention(q, c, c.clone(), t, n, cu, max_q_len=1, max_kv_len=4).shape == q.shape
     for bad in [(c, c[:3], t, n, cu), (c, c.float(), t, n, cu), (c.float(), c.float(), t, n, cu), (c, c, t, n, cu[:3]),
                 (c, c, t, n.long(), cu), (c, c, t.t(), n, cu), (c, c, t[0], n, cu), (c[0], c[0], t, n, cu),
-                (c, c.transpose(1, 2).contiguous().transpose(1, 2), t, n, cu)]:
-        refused(A._cache_args, *bad, -1, 2, 64)
-    refused(A._cache_args, c, c, t, n, cu, -1, 4, 64)
-    refused(A._cache_args, c, c, t, n, cu, -1, 2, 128)
-    refused(A._cache_args, c, c, t, n, cu, 0, 2, 64)
+                (c, c.transpose(1, 2).contiguous().transpose(1, 2), t, n, cu), (c.bfloat16(), c.bfloat16(), t, n, cu),
+                (z(4, 2, 24, 64), z(4, 2, 24, 64), t, n, cu), (z(4, 2, 16, 32), z(4, 2, 16, 32), t, n, cu),
+                (z(4, 3, 16, 64), z(4, 3, 16, 64), t, n, cu)]:
+        refused(A.paged_attention, q, *bad, max_q_len=1, max_kv_len=4)
+        refused(A.kv_append, k, k, *bad, pos, f)
+    for more in [dict(max_q_len=-1), dict(max_kv_len=1 << 40), dict(window=-1), dict(window=4, causal=False), dict(scale=0.0),
+                 dict(out=q.bfloat16()), dict(out=z(3, 64, 4).transpose(1, 2))]:
+        refused(A.paged_attention, q, c, c, t, n, cu, **{**dict(max_q_len=1, max_kv_len=4), **more})
+    refused(A.kv_append, k, q, c, c, t, n, cu, pos, f)
+    refused(A.kv_append, k, k, c, c, t, n, cu, pos, f, q_out=q)
+    refused(A.kv_append, k, k, c.view(torch.uint8)[..., :64].contiguous(), c.view(torch.uint8)[..., :64].contiguous(), t, n, cu,
+            pos, f, k_scale=0.0)
+    torch.cuda.synchronize()
