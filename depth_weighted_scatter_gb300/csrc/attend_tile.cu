@@ -6,9 +6,9 @@
 // walks the keys in blocks of 128:
 //   warps 0-3, 4-7   softmax of tile 0, 1 (one row a thread): S from tensor
 //                    memory, running maximum and sum, P (16 bits) back over S
-//   warp 8           issues the products: S = Q K^T (both from shared memory)
-//                    and O += P V (P from tensor memory), O in tensor memory
-//   warp 9           loads K and V: a TMA box for each page and 64 elements of
+//   warps 8, 9       issue the products of tile 0, 1: S = Q K^T (both from shared
+//                    memory) and O += P V (P from tensor memory), O in tensor memory
+//   warp 10          loads K and V: a TMA box for each page and 64 elements of
 //                    the head, into a ring of 128-byte-swizzled blocks
 //   warps 12-15      (E4M3 cache instead) load codes, widen them to 16 bits and
 //                    store them in the same layout
@@ -47,12 +47,12 @@ struct TileShape {
     // one of loaders.  Registers a thread, by setmaxnreg; their sum is within
     // what the launch gives (168 a thread of 384, 128 of 512).
     static constexpr int LOADERS = E4M3 ? 4 : 1;                           // warps
-    static constexpr int FIRST_LOADER = E4M3 ? 12 : 9;
+    static constexpr int FIRST_LOADER = E4M3 ? 12 : 10;
     static constexpr int THREADS = E4M3 ? 512 : 384;
     static constexpr int LAUNCH_REGS = E4M3 ? 128 : 168;
-    static constexpr int SOFTMAX_REGS = E4M3 ? 192 : 208;
+    static constexpr int SOFTMAX_REGS = E4M3 ? 184 : 208;
     static constexpr int PRODUCT_REGS = E4M3 ? 56 : 80;
-    static constexpr int LOADER_REGS = 72;
+    static constexpr int LOADER_REGS = 88;
     static_assert(256 * SOFTMAX_REGS + 128 * PRODUCT_REGS + (E4M3 ? 128 * LOADER_REGS : 0) <= THREADS * LAUNCH_REGS,
                   "the split is within the launch's registers");
     static constexpr int HALVES = D / 64;                                  // 128-byte columns of a block
@@ -64,7 +64,7 @@ struct TileShape {
 
 struct TileBars {                          // shared memory
     uint64_t full[8], empty[8];            // ring
-    uint64_t q_full[2], s_full[2], p_full[2][2], o_full[2], drain;
+    uint64_t q_full[2], s_full[2], p_full[2][2], o_full[2], drain[2];
     uint32_t tmem, failed;
 };
 
@@ -114,7 +114,7 @@ k_attend_tile(AttnArgs a, AttnPlan pl, const __grid_constant__ CUtensorMap k_map
     if (threadIdx.x == 0) {
         for (int i = 0; i < S::STAGES; ++i) {
             bar_init(shared_addr(&bars.full[i]), E4M3 ? S::LOADERS * 32 : 1);
-            bar_init(shared_addr(&bars.empty[i]), 1);
+            bar_init(shared_addr(&bars.empty[i]), 2);
         }
         for (int t = 0; t < 2; ++t) {
             bar_init(shared_addr(&bars.q_full[t]), kTileRows);
@@ -122,8 +122,8 @@ k_attend_tile(AttnArgs a, AttnPlan pl, const __grid_constant__ CUtensorMap k_map
             bar_init(shared_addr(&bars.p_full[t][0]), kTileRows);
             bar_init(shared_addr(&bars.p_full[t][1]), kTileRows);
             bar_init(shared_addr(&bars.o_full[t]), 1);
+            bar_init(shared_addr(&bars.drain[t]), 1);
         }
-        bar_init(shared_addr(&bars.drain), 1);
         bars.failed = 0;
         bar_init_fence();
     }
@@ -146,17 +146,31 @@ k_attend_tile(AttnArgs a, AttnPlan pl, const __grid_constant__ CUtensorMap k_map
         const TileRange tr = t == 0 ? t0 : t1;
         const int32_t tile0 = row0 + t * kTileRows;
         if (tr.b1 > tr.b0) {
-            constexpr int CPR = D / 8;                                     // 16-byte pieces of a row
-            for (int x = tid; x < kTileRows * CPR; x += kTileRows) {
-                const int row = x / CPR, c = x % CPR;
-                const int32_t gr = tile0 + row;
-                uint4 w = make_uint4(0, 0, 0, 0);
-                if (gr < rows)
-                    w = *reinterpret_cast<const uint4 *>(static_cast<const T *>(a.q.p) +
-                                                         static_cast<int64_t>(r.q0 + gr / a.G) * a.q.token_stride +
-                                                         (hk * a.G + gr % a.G) * a.q.head_stride + c * 8);
-                const uint32_t d = q_smem + t * S::Q_BYTES + (c >> 3) * (kTileRows * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4);
-                asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(d), "r"(w.x), "r"(w.y), "r"(w.z), "r"(w.w) : "memory");
+            // 16-byte pieces of a row, rows of one step of the warpgroup; eight
+            // pieces in flight a thread
+            constexpr int CPR = D / 8, RPI = kTileRows / CPR, N = kTileRows / RPI;
+            const int c = tid % CPR;
+#pragma unroll 1
+            for (int i0 = 0; i0 < N; i0 += 8) {
+                uint4 w[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int32_t gr = tile0 + (i0 + i) * RPI + tid / CPR;
+                    w[i] = make_uint4(0, 0, 0, 0);
+                    if (gr < rows)
+                        w[i] = *reinterpret_cast<const uint4 *>(static_cast<const T *>(a.q.p) +
+                                                                static_cast<int64_t>(r.q0 + gr / a.G) * a.q.token_stride +
+                                                                (hk * a.G + gr % a.G) * a.q.head_stride + c * 8);
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int row = (i0 + i) * RPI + tid / CPR;
+                    const uint32_t d =
+                        q_smem + t * S::Q_BYTES + (c >> 3) * (kTileRows * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4);
+                    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(d), "r"(w[i].x), "r"(w[i].y), "r"(w[i].z),
+                                 "r"(w[i].w)
+                                 : "memory");
+                }
             }
             fence_shared_async();
             bar_arrive(shared_addr(&bars.q_full[t]));
@@ -207,30 +221,27 @@ k_attend_tile(AttnArgs a, AttnPlan pl, const __grid_constant__ CUtensorMap k_map
 #pragma unroll
             for (int x = 0; x < 4; ++x) mx[x] = __uint_as_float(s[x]);
 #pragma unroll
-            for (int c = 4; c < kBlock; c += 8) {
+            for (int c = 4; c < kBlock - 4; c += 8)
 #pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    mx[x] = fmaxf(mx[x], __uint_as_float(s[c + x]));
-                    if (c + 4 < kBlock) mx[x] = fmaxf(mx[x], __uint_as_float(s[c + 4 + x]));
-                }
-            }
-            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
+                for (int x = 0; x < 4; ++x) mx[x] = max3(mx[x], __uint_as_float(s[c + x]), __uint_as_float(s[c + 4 + x]));
+#pragma unroll
+            for (int x = 0; x < 4; ++x) mx[x] = fmaxf(mx[x], __uint_as_float(s[kBlock - 4 + x]));
+            const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * a.scale_log2;
             const bool grown = top > m + kGrow || (m == -INFINITY && top > m);
             if (__any_sync(0xffffffffu, grown)) {
                 const float mn = grown ? top : m;
                 const float f = grown ? pow2(m - mn) : 1.0f;               // m = -inf: 0
                 m = mn;
                 if (j > tr.b0) {
-                    const uint64_t f2 = pair(f, f);
-                    sum = mul2(sum, f2);
-#pragma unroll
-                    for (int c = 0; c < D; c += 32) {
-                        uint32_t o[32];
-                        tmem_ld32(o_mem + c, o);
+                    sum = mul2(sum, pair(f, f));
+#pragma unroll 1
+                    for (int c = 0; c < D; c += 8) {                       // few registers: S is held beside
+                        uint32_t o[8];
+                        tmem_ld8(o_mem + c, o);
                         tmem_wait_ld();
 #pragma unroll
-                        for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
-                        tmem_st32(o_mem + c, o);
+                        for (int x = 0; x < 8; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
+                        tmem_st8(o_mem + c, o);
                     }
                 }
             }
@@ -239,24 +250,27 @@ k_attend_tile(AttnArgs a, AttnPlan pl, const __grid_constant__ CUtensorMap k_map
             uint64_t part = pair(0.0f, 0.0f);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                uint32_t p[32];
+                // eight words at a time, so that P needs few registers beside S
 #pragma unroll
-                for (int c = 0; c < 32; ++c) {
-                    const int at = h * 64 + 2 * c;
-                    const uint64_t e = fma2(pair(__uint_as_float(s[at]), __uint_as_float(s[at + 1])), scale2, from2);
-                    float x, y;
-                    unpair(e, &x, &y);
-                    x = pow2(x);
-                    y = pow2(y);
-                    if (c & 1)
-                        part = add2(part, pair(x, y));
-                    else
-                        sum = add2(sum, pair(x, y));
-                    p[c] = pack2<T>(x, y);
+                for (int g = 0; g < 4; ++g) {
+                    uint32_t p[8];
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) {
+                        const int at = h * 64 + g * 16 + 2 * c;
+                        float x, y;
+                        unpair(fma2(pair(__uint_as_float(s[at]), __uint_as_float(s[at + 1])), scale2, from2), &x, &y);
+                        x = pow2(x);
+                        y = pow2(y);
+                        if (c & 1)
+                            part = add2(part, pair(x, y));
+                        else
+                            sum = add2(sum, pair(x, y));
+                        p[c] = pack2<T>(x, y);
+                    }
+                    tmem_st8(s_mem + h * 32 + g * 8, p);
                 }
                 // Each half is released by itself: its product with V runs
                 // during the exponentials of the other.
-                tmem_st32(s_mem + h * 32, p);
                 tmem_wait_st();
                 tmem_fence_before();
                 bar_arrive(shared_addr(&bars.p_full[t][h]));
@@ -329,19 +343,23 @@ k_attend_tile(AttnArgs a, AttnPlan pl, const __grid_constant__ CUtensorMap k_map
                 store_row<T, D / 32>(a, pl, r, b, hk, rr / a.G, hk * a.G + rr % a.G, rr, chunk, n_used, m1, s1, acc);
             }
         }
-    } else if (warp == 8) {
+    } else if (warp < 10) {
         // ------------------------------------------------------------ products
+        // A warp a tile: while one waits the other's products run.
+        const int t = warp - 8;
+        const TileRange tr = t == 0 ? t0 : t1;
         constexpr int format = std::is_same<T, __half>::value ? 0 : 1;
         constexpr uint32_t s_desc = mma_desc(format, kBlock, false), o_desc = mma_desc(format, D, true);
-        auto in = [&](int t, int32_t j) { return t == 0 ? j >= t0.b0 && j < t0.b1 : j >= t1.b0 && j < t1.b1; };
-        auto scores = [&](int t, uint32_t k_smem) {
+        auto in = [&](int32_t j) { return j >= tr.b0 && j < tr.b1; };
+        const uint32_t s_bar = shared_addr(&bars.s_full[t]), p_bar = shared_addr(&bars.p_full[t][0]);
+        auto scores = [&](uint32_t k_smem) {
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) {
                 const uint32_t off = (k >> 2) * (kBlock * 128) + (k & 3) * 32;
                 mma_ss(tmem + t * kBlock, operand_desc(q_smem + t * S::Q_BYTES + off, 16, 1024),
                        operand_desc(k_smem + off, 16, 1024), s_desc, k > 0);
             }
-            mma_commit(shared_addr(&bars.s_full[t]));
+            mma_commit(s_bar);
         };
         uint32_t at = 0, lap = 0;                                          // place in the ring and its phase
         auto next = [&]() {
@@ -350,55 +368,51 @@ k_attend_tile(AttnArgs a, AttnPlan pl, const __grid_constant__ CUtensorMap k_map
                 lap ^= 1;
             }
         };
-        uint32_t p_phase[2] = {0, 0};
+        uint32_t p_phase = 0;
+        // A wait that ran out ends the products, not the walk: both warps meet at
+        // the tail's barrier.
+        auto wait = [&](uint32_t bar, uint32_t parity) {
+            if (ok) ok = __all_sync(0xffffffffu, bar_wait(bar, parity));
+        };
+        // Every block's K and V are let go by both warps, used or not.
         if (j1 > j0) {
-            for (int t = 0; t < 2 && ok; ++t)
-                if ((t == 0 ? t0.b1 : t1.b1) > 0) ok = bar_wait(shared_addr(&bars.q_full[t]), 0);
-            ok = ok && bar_wait(shared_addr(&bars.full[at]), lap);
-            if (__all_sync(0xffffffffu, ok) && elect_one()) {
-                for (int t = 0; t < 2; ++t)
-                    if (in(t, j0)) scores(t, ring + at * S::BLOCK_BYTES);
+            if (tr.b1 > 0) wait(shared_addr(&bars.q_full[t]), 0);
+            wait(shared_addr(&bars.full[at]), lap);
+            if (ok && elect_one()) {
+                if (in(j0)) scores(ring + at * S::BLOCK_BYTES);
                 mma_commit(shared_addr(&bars.empty[at]));
             }
+            __syncwarp();
             next();
         }
         for (int32_t j = j0; j < j1; ++j) {
-            ok = ok && bar_wait(shared_addr(&bars.full[at]), lap);
-            if (!__all_sync(0xffffffffu, ok)) {
-                ok = false;
-                break;
-            }
+            wait(shared_addr(&bars.full[at]), lap);
             const uint32_t v_at = at, v_smem = ring + at * S::BLOCK_BYTES;
             next();
             // Values past the request's last key are whatever the page holds:
             // zeros in their place (the weights there are 0, but 0 * NaN is not).
             if (!E4M3 && (j + 1) * static_cast<int64_t>(kBlock) > r.kv_len) {
-                const int dead = r.kv_len - j * kBlock;                    // first row to clear
-                for (int x = dead * 8 + lane; x < kBlock * 8; x += 32)
+                if (t == 0 && ok) {
+                    const int dead = r.kv_len - j * kBlock;                // first row to clear
+                    for (int x = dead * 8 + lane; x < kBlock * 8; x += 32)
 #pragma unroll
-                    for (int h = 0; h < S::HALVES; ++h)
-                        asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(v_smem + h * (kBlock * 128) + x * 16), "r"(0)
-                                     : "memory");
-                fence_shared_async();
-                __syncwarp();
-            }
-            if (j + 1 < j1) {
-                ok = bar_wait(shared_addr(&bars.full[at]), lap);
-                if (!__all_sync(0xffffffffu, ok)) {
-                    ok = false;
-                    break;
+                        for (int h = 0; h < S::HALVES; ++h)
+                            asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(v_smem + h * (kBlock * 128) + x * 16),
+                                         "r"(0)
+                                         : "memory");
+                    fence_shared_async();
                 }
+                asm volatile("bar.sync 1, 64;" ::: "memory");              // both product warps
             }
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                const bool now = in(t, j), then = in(t, j + 1) && j + 1 < j1;
-                const bool first = j == (t == 0 ? t0.b0 : t1.b0);
+            const bool then = j + 1 < j1;
+            if (then) wait(shared_addr(&bars.full[at]), lap);
+            const bool now = in(j), first = j == tr.b0;
+            if (now) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    if (!now) continue;
-                    ok = bar_wait(shared_addr(&bars.p_full[t][h]), p_phase[t]) && ok;
+                    wait(p_bar + h * 8, p_phase);
                     tmem_fence_after();
-                    if (__all_sync(0xffffffffu, ok) && elect_one()) {
+                    if (ok && elect_one()) {
 #pragma unroll
                         for (int k = h * (kBlock / 32); k < (h + 1) * (kBlock / 32); ++k)
                             mma_ts(tmem + 2 * kBlock + t * D, tmem + t * kBlock + k * 8,
@@ -406,28 +420,23 @@ k_attend_tile(AttnArgs a, AttnPlan pl, const __grid_constant__ CUtensorMap k_map
                     }
                     __syncwarp();
                 }
-                if (now) p_phase[t] ^= 1;
-                if (!__all_sync(0xffffffffu, ok)) {
-                    ok = false;
-                    break;
-                }
-                if (elect_one()) {
-                    if (t == 1) mma_commit(shared_addr(&bars.empty[v_at]));
-                    if (then)
-                        scores(t, ring + at * S::BLOCK_BYTES);
-                    else if (now)
-                        mma_commit(shared_addr(&bars.o_full[t]));
-                    if (t == 1 && j + 1 < j1) mma_commit(shared_addr(&bars.empty[at]));
-                }
-                __syncwarp();
+                p_phase ^= 1;
             }
-            if (!ok) break;
-            if (j + 1 < j1) next();
+            if (ok && elect_one()) {
+                mma_commit(shared_addr(&bars.empty[v_at]));
+                if (then && in(j + 1))
+                    scores(ring + at * S::BLOCK_BYTES);
+                else if (now)
+                    mma_commit(shared_addr(&bars.o_full[t]));
+                if (then) mma_commit(shared_addr(&bars.empty[at]));
+            }
+            __syncwarp();
+            if (then) next();
         }
         // All products done before the CTA ends.
-        if (elect_one()) mma_commit(shared_addr(&bars.drain));
+        if (elect_one()) mma_commit(shared_addr(&bars.drain[t]));
         __syncwarp();
-        ok = bar_wait(shared_addr(&bars.drain), 0) && ok;
+        ok = bar_wait(shared_addr(&bars.drain[t]), 0) && ok;
     } else if (warp < S::FIRST_LOADER || warp >= S::FIRST_LOADER + S::LOADERS) {
         // warps without work
     } else if constexpr (!E4M3) {
