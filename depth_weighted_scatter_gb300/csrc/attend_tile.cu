@@ -64,7 +64,7 @@ struct TileShape {
 
 struct TileBars {                          // shared memory
     uint64_t full[8], empty[8];            // ring
-    uint64_t q_full[2], s_full[2], p_full[2][2], o_full[2], drain[2];
+    uint64_t q_full[2], s_full[2], p_full[2][2], o_full[2], turn[2], drain[2];
     uint32_t tmem, failed;
 };
 
@@ -122,6 +122,7 @@ k_attend_tile(AttnArgs a, AttnPlan pl, const __grid_constant__ CUtensorMap k_map
             bar_init(shared_addr(&bars.p_full[t][0]), kTileRows);
             bar_init(shared_addr(&bars.p_full[t][1]), kTileRows);
             bar_init(shared_addr(&bars.o_full[t]), 1);
+            bar_init(shared_addr(&bars.turn[t]), 1);
             bar_init(shared_addr(&bars.drain[t]), 1);
         }
         bars.failed = 0;
@@ -345,16 +346,24 @@ k_attend_tile(AttnArgs a, AttnPlan pl, const __grid_constant__ CUtensorMap k_map
         }
     } else if (warp < 10) {
         // ------------------------------------------------------------ products
-        // A warp a tile: while one waits the other's products run.
+        // A warp a tile: while one waits the other's products run.  They take
+        // turns, a block's products of one tile after those of the other, so that
+        // one tile is in its softmax while the other's products run; left to
+        // themselves both tiles fell into step and the tensor core idled in both
+        // softmaxes (8192-token prompt: 496 us against TURNS).  The turn passes
+        // before the last products are issued, as issuing waits for the queue.
         const int t = warp - 8;
         const TileRange tr = t == 0 ? t0 : t1;
         constexpr int format = std::is_same<T, __half>::value ? 0 : 1;
         constexpr uint32_t s_desc = mma_desc(format, kBlock, false), o_desc = mma_desc(format, D, true);
         auto in = [&](int32_t j) { return j >= tr.b0 && j < tr.b1; };
         const uint32_t s_bar = shared_addr(&bars.s_full[t]), p_bar = shared_addr(&bars.p_full[t][0]);
-        auto scores = [&](uint32_t k_smem) {
+        const uint32_t my_turn = shared_addr(&bars.turn[t]), your_turn = shared_addr(&bars.turn[t ^ 1]);
+        uint32_t turn_phase = 0;
+        auto scores = [&](uint32_t k_smem, bool pass) {
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) {
+                if (pass && k == D / 16 - 3) bar_arrive(your_turn);
                 const uint32_t off = (k >> 2) * (kBlock * 128) + (k & 3) * 32;
                 mma_ss(tmem + t * kBlock, operand_desc(q_smem + t * S::Q_BYTES + off, 16, 1024),
                        operand_desc(k_smem + off, 16, 1024), s_desc, k > 0);
@@ -379,7 +388,7 @@ k_attend_tile(AttnArgs a, AttnPlan pl, const __grid_constant__ CUtensorMap k_map
             if (tr.b1 > 0) wait(shared_addr(&bars.q_full[t]), 0);
             wait(shared_addr(&bars.full[at]), lap);
             if (ok && elect_one()) {
-                if (in(j0)) scores(ring + at * S::BLOCK_BYTES);
+                if (in(j0)) scores(ring + at * S::BLOCK_BYTES, false);
                 mma_commit(shared_addr(&bars.empty[at]));
             }
             __syncwarp();
@@ -407,10 +416,15 @@ k_attend_tile(AttnArgs a, AttnPlan pl, const __grid_constant__ CUtensorMap k_map
             const bool then = j + 1 < j1;
             if (then) wait(shared_addr(&bars.full[at]), lap);
             const bool now = in(j), first = j == tr.b0;
+            if (now) wait(p_bar, p_phase);
+            if (j > j0 || t == 1) {
+                wait(my_turn, turn_phase);
+                turn_phase ^= 1;
+            }
             if (now) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    wait(p_bar + h * 8, p_phase);
+                    if (h == 1) wait(p_bar + 8, p_phase);
                     tmem_fence_after();
                     if (ok && elect_one()) {
 #pragma unroll
@@ -424,10 +438,12 @@ k_attend_tile(AttnArgs a, AttnPlan pl, const __grid_constant__ CUtensorMap k_map
             }
             if (ok && elect_one()) {
                 mma_commit(shared_addr(&bars.empty[v_at]));
-                if (then && in(j + 1))
-                    scores(ring + at * S::BLOCK_BYTES);
-                else if (now)
-                    mma_commit(shared_addr(&bars.o_full[t]));
+                if (then && in(j + 1)) {
+                    scores(ring + at * S::BLOCK_BYTES, true);
+                } else {
+                    bar_arrive(your_turn);
+                    if (now) mma_commit(shared_addr(&bars.o_full[t]));
+                }
                 if (then) mma_commit(shared_addr(&bars.empty[at]));
             }
             __syncwarp();
