@@ -147,16 +147,15 @@ k_attend_tile(AttnArgs a, AttnPlan pl, const __grid_constant__ CUtensorMap k_map
         const TileRange tr = t == 0 ? t0 : t1;
         const int32_t tile0 = row0 + t * kTileRows;
         if (tr.b1 > tr.b0) {
-            // 16-byte pieces of a row, rows of one step of the warpgroup; eight
-            // pieces in flight a thread
+            // 16-byte pieces of a row, rows of one step of the warpgroup; all
+            // pieces of a thread in flight
             constexpr int CPR = D / 8, RPI = kTileRows / CPR, N = kTileRows / RPI;
             const int c = tid % CPR;
-#pragma unroll 1
-            for (int i0 = 0; i0 < N; i0 += 8) {
-                uint4 w[8];
+            {
+                uint4 w[N];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int32_t gr = tile0 + (i0 + i) * RPI + tid / CPR;
+                for (int i = 0; i < N; ++i) {
+                    const int32_t gr = tile0 + i * RPI + tid / CPR;
                     w[i] = make_uint4(0, 0, 0, 0);
                     if (gr < rows)
                         w[i] = *reinterpret_cast<const uint4 *>(static_cast<const T *>(a.q.p) +
@@ -164,8 +163,8 @@ k_attend_tile(AttnArgs a, AttnPlan pl, const __grid_constant__ CUtensorMap k_map
                                                                 (hk * a.G + gr % a.G) * a.q.head_stride + c * 8);
                 }
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int row = (i0 + i) * RPI + tid / CPR;
+                for (int i = 0; i < N; ++i) {
+                    const int row = i * RPI + tid / CPR;
                     const uint32_t d =
                         q_smem + t * S::Q_BYTES + (c >> 3) * (kTileRows * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4);
                     asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(d), "r"(w[i].x), "r"(w[i].y), "r"(w[i].z),
@@ -218,6 +217,41 @@ k_attend_tile(AttnArgs a, AttnPlan pl, const __grid_constant__ CUtensorMap k_map
                 for (int c = 0; c < kBlock; ++c)
                     if (c < from || c >= to || ((holes >> (c / 16)) & 1)) s[c] = 0xff800000u;      // -inf
             }
+            // P of one half and its sum, at the scale m.
+            const uint64_t scale2 = pair(a.scale_log2, a.scale_log2);
+            auto weights = [&](int h, uint32_t *p) {
+                const float base2 = m == -INFINITY ? 0.0f : -m;
+                const uint64_t from2 = pair(base2, base2);
+                uint64_t u = pair(0.0f, 0.0f), v = u;
+#pragma unroll
+                for (int c = 0; c < 32; ++c) {
+                    const int at = h * 64 + 2 * c;
+                    float x, y;
+                    unpair(fma2(pair(__uint_as_float(s[at]), __uint_as_float(s[at + 1])), scale2, from2), &x, &y);
+                    x = pow2(x);
+                    y = pow2(y);
+                    if (c & 1)
+                        v = add2(v, pair(x, y));
+                    else
+                        u = add2(u, pair(x, y));
+                    p[c] = pack2<T>(x, y);
+                }
+                return add2(u, v);
+            };
+            // Each half is released by itself: its product with V runs during
+            // the exponentials of the other.
+            auto release = [&](int h, const uint32_t *p) {
+#pragma unroll
+                for (int g = 0; g < 4; ++g) tmem_st8(s_mem + h * 32 + g * 8, p + g * 8);
+                tmem_wait_st();
+                tmem_fence_before();
+                bar_arrive(shared_addr(&bars.p_full[t][h]));
+            };
+            // The first half's weights are worked out at the scale in use while
+            // the row's maximum is still being found (other units do that), and
+            // again in the rare case that the maximum has outgrown the scale.
+            uint32_t p[32];
+            uint64_t part = weights(0, p);
             float mx[4];
 #pragma unroll
             for (int x = 0; x < 4; ++x) mx[x] = __uint_as_float(s[x]);
@@ -245,37 +279,12 @@ k_attend_tile(AttnArgs a, AttnPlan pl, const __grid_constant__ CUtensorMap k_map
                         tmem_st8(o_mem + c, o);
                     }
                 }
+                part = weights(0, p);
             }
-            const float base2 = m == -INFINITY ? 0.0f : -m;
-            const uint64_t scale2 = pair(a.scale_log2, a.scale_log2), from2 = pair(base2, base2);
-            uint64_t part = pair(0.0f, 0.0f);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                // eight words at a time, so that P needs few registers beside S
-#pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    uint32_t p[8];
-#pragma unroll
-                    for (int c = 0; c < 8; ++c) {
-                        const int at = h * 64 + g * 16 + 2 * c;
-                        float x, y;
-                        unpair(fma2(pair(__uint_as_float(s[at]), __uint_as_float(s[at + 1])), scale2, from2), &x, &y);
-                        x = pow2(x);
-                        y = pow2(y);
-                        if (c & 1)
-                            part = add2(part, pair(x, y));
-                        else
-                            sum = add2(sum, pair(x, y));
-                        p[c] = pack2<T>(x, y);
-                    }
-                    tmem_st8(s_mem + h * 32 + g * 8, p);
-                }
-                // Each half is released by itself: its product with V runs
-                // during the exponentials of the other.
-                tmem_wait_st();
-                tmem_fence_before();
-                bar_arrive(shared_addr(&bars.p_full[t][h]));
-            }
+            release(0, p);
+            sum = add2(sum, part);
+            part = weights(1, p);
+            release(1, p);
             sum = add2(sum, part);
         }
         float l, l1;
@@ -286,42 +295,94 @@ k_attend_tile(AttnArgs a, AttnPlan pl, const __grid_constant__ CUtensorMap k_map
             ok = false;
         } else {
             tmem_fence_after();
-            // O to its row: two 16-byte stores for each 32-byte sector of a row.
             const bool some = !(l == 0.0f);
             const int64_t token = r.q0 + (used ? row / a.G : 0);
             const int32_t h = hk * a.G + (used ? row % a.G : 0);
             const float inv = some ? a.v_scale / l : 0.0f;
-            T *op = static_cast<T *>(a.out.p) + token * a.out.token_stride + h * a.out.head_stride;
             const int64_t part = n_used > 1 && used ? part_row(a, pl, b, hk, chunk, row) : 0;
             bool fine = l - l == 0.0f;
-            if (tr.b1 > tr.b0) {
+            // O leaves through shared memory (where this warp's queries were), so
+            // that a warp's stores cover whole rows.
+            const int32_t warp0 = tile0 + (warp & 3) * 32;                 // the warp's first row
+            const uint32_t stage = q_smem + t * S::Q_BYTES + (warp & 3) * 32 * (D * 2);
+            auto row_out = [&](int x, int64_t *token_x, int32_t *h_x) {
+                *token_x = r.q0 + (warp0 + x) / a.G;
+                *h_x = hk * a.G + (warp0 + x) % a.G;
+            };
+            if (n_used == 1) {
+                constexpr int CPR = D / 8;                                 // 16-byte pieces of a row
+#pragma unroll
+                for (int c = 0; c < D; c += 32) {
+                    uint32_t o[32] = {};
+                    if (tr.b1 > tr.b0) {
+                        tmem_ld32(o_mem + c, o);
+                        tmem_wait_ld();
+                    }
+#pragma unroll
+                    for (int x = 0; x < 32; x += 8) {
+                        float f[8];
+#pragma unroll
+                        for (int y = 0; y < 8; ++y) {
+                            f[y] = some ? __uint_as_float(o[x + y]) * inv : 0.0f;
+                            fine = fine && f[y] - f[y] == 0.0f;
+                        }
+                        const uint4 w = pack8<T>(f);
+                        const uint32_t d = stage + lane * (D * 2) + ((((c + x) / 8) ^ (lane & 7)) << 4);
+                        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(d), "r"(w.x), "r"(w.y), "r"(w.z), "r"(w.w)
+                                     : "memory");
+                    }
+                }
+                __syncwarp();
+                const int c = lane % CPR;
+#pragma unroll 4
+                for (int x = lane / CPR; x < 32; x += 32 / CPR) {
+                    uint4 w;
+                    const uint32_t d = stage + x * (D * 2) + ((c ^ (x & 7)) << 4);
+                    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w) : "r"(d)
+                                 : "memory");
+                    if (warp0 + x < rows) {
+                        int64_t token_x;
+                        int32_t h_x;
+                        row_out(x, &token_x, &h_x);
+                        *reinterpret_cast<uint4 *>(static_cast<T *>(a.out.p) + token_x * a.out.token_stride +
+                                                   h_x * a.out.head_stride + c * 8) = w;
+                    }
+                }
+                __syncwarp();
+            } else if (tr.b1 > tr.b0) {
 #pragma unroll
                 for (int c = 0; c < D; c += 32) {
                     uint32_t o[32];
                     tmem_ld32(o_mem + c, o);
                     tmem_wait_ld();
-                    float f[32];
 #pragma unroll
-                    for (int x = 0; x < 32; ++x) {
-                        f[x] = __uint_as_float(o[x]);
-                        fine = fine && f[x] - f[x] == 0.0f;
+                    for (int x = 0; x < 32; ++x) fine = fine && __uint_as_float(o[x]) - __uint_as_float(o[x]) == 0.0f;
+                    // 64 bytes of a row at a time
+                    const uint32_t d0 = stage + lane * 64;
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+#pragma unroll
+                        for (int x = 0; x < 4; ++x)
+                            asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(d0 + ((x ^ ((lane >> 1) & 3)) << 4)),
+                                         "r"(o[half * 16 + 4 * x]), "r"(o[half * 16 + 4 * x + 1]),
+                                         "r"(o[half * 16 + 4 * x + 2]), "r"(o[half * 16 + 4 * x + 3])
+                                         : "memory");
+                        __syncwarp();
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int x = i * 8 + lane / 4, y = lane & 3;
+                            uint4 w;
+                            asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                                         : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
+                                         : "r"(stage + x * 64 + ((y ^ ((x >> 1) & 3)) << 4))
+                                         : "memory");
+                            if (warp0 + x < rows)
+                                *reinterpret_cast<uint4 *>(a.part_o + part_row(a, pl, b, hk, chunk, warp0 + x) * D + c +
+                                                           half * 16 + y * 4) = w;
+                        }
+                        __syncwarp();
                     }
-                    if (used && n_used > 1) {
-#pragma unroll
-                        for (int x = 0; x < 32; x += 4)
-                            *reinterpret_cast<float4 *>(a.part_o + part * D + c + x) =
-                                make_float4(f[x], f[x + 1], f[x + 2], f[x + 3]);
-                    } else if (used) {
-#pragma unroll
-                        for (int x = 0; x < 32; ++x) f[x] = some ? f[x] * inv : 0.0f;
-#pragma unroll
-                        for (int x = 0; x < 32; x += 8) *reinterpret_cast<uint4 *>(op + c + x) = pack8<T>(f + x);
-                    }
-                    __syncwarp();
                 }
-            } else if (used && n_used == 1) {
-#pragma unroll
-                for (int c = 0; c < D; c += 8) *reinterpret_cast<uint4 *>(op + c) = make_uint4(0, 0, 0, 0);
             }
             if (used) {
                 if (n_used > 1)
