@@ -55,6 +55,11 @@ struct TileShape {
     static constexpr int LOADER_REGS = 88;
     static_assert(256 * SOFTMAX_REGS + 128 * PRODUCT_REGS + (E4M3 ? 128 * LOADER_REGS : 0) <= THREADS * LAUNCH_REGS,
                   "the split is within the launch's registers");
+    // At head_dim 64 tensor memory has room for P beside S: the next block's S is
+    // then made while this block is in its softmax.
+    static constexpr bool AHEAD = D == 64;
+    static constexpr int P_COL = AHEAD ? 2 * kBlock + 2 * D : 0;           // P's first column; tile t's are 64 t (128 t over S) on
+    static constexpr int P_STEP = AHEAD ? kBlock / 2 : kBlock;
     static constexpr int HALVES = D / 64;                                  // 128-byte columns of a block
     static constexpr int BLOCK_BYTES = kBlock * D * 2;
     static constexpr int STAGES = D == 128 ? 5 : 8;                        // K and V blocks in turn
@@ -64,7 +69,7 @@ struct TileShape {
 
 struct TileBars {                          // shared memory
     uint64_t full[8], empty[8];            // ring
-    uint64_t q_full[2], s_full[2], p_full[2][2], o_full[2], turn[2], drain[2];
+    uint64_t q_full[2], s_full[2], p_full[2][2], s_read[2], o_full[2], turn[2], drain[2];
     uint32_t tmem, failed;
 };
 
@@ -121,6 +126,7 @@ k_attend_tile(AttnArgs a, AttnPlan pl, const __grid_constant__ CUtensorMap k_map
             bar_init(shared_addr(&bars.s_full[t]), 1);
             bar_init(shared_addr(&bars.p_full[t][0]), kTileRows);
             bar_init(shared_addr(&bars.p_full[t][1]), kTileRows);
+            bar_init(shared_addr(&bars.s_read[t]), kTileRows);
             bar_init(shared_addr(&bars.o_full[t]), 1);
             bar_init(shared_addr(&bars.turn[t]), 1);
             bar_init(shared_addr(&bars.drain[t]), 1);
@@ -180,7 +186,7 @@ k_attend_tile(AttnArgs a, AttnPlan pl, const __grid_constant__ CUtensorMap k_map
         int32_t lo = 0, hi = INT32_MAX;                                    // a place past the last row sees all, and is not kept
         if (used) seen_keys(a, r, row / a.G, &lo, &hi);
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-        const uint32_t s_mem = tmem + lanes + t * kBlock, o_mem = tmem + lanes + 2 * kBlock + t * D;
+        const uint32_t s_mem = tmem + lanes + t * kBlock, p_mem = tmem + lanes + S::P_COL + t * S::P_STEP, o_mem = tmem + lanes + 2 * kBlock + t * D;
         float m = -INFINITY;                                               // the scale in use (base 2)
         uint64_t sum = pair(0.0f, 0.0f);
         // Groups of 16 keys that lie on no page, one bit each; read a block ahead.
@@ -210,6 +216,10 @@ k_attend_tile(AttnArgs a, AttnPlan pl, const __grid_constant__ CUtensorMap k_map
 #pragma unroll
             for (int c = 0; c < kBlock; c += 32) tmem_ld32(s_mem + c, s + c);
             tmem_wait_ld();
+            if constexpr (S::AHEAD) {                                      // S may be made again
+                tmem_fence_before();
+                bar_arrive(shared_addr(&bars.s_read[t]));
+            }
             const int32_t k0 = j * kBlock;
             if (!__all_sync(0xffffffffu, holes == 0 && lo <= k0 && hi - kBlock >= k0)) {
                 const int32_t from = lo - k0, to = hi - k0;
@@ -242,7 +252,7 @@ k_attend_tile(AttnArgs a, AttnPlan pl, const __grid_constant__ CUtensorMap k_map
             // the exponentials of the other.
             auto release = [&](int h, const uint32_t *p) {
 #pragma unroll
-                for (int g = 0; g < 4; ++g) tmem_st8(s_mem + h * 32 + g * 8, p + g * 8);
+                for (int g = 0; g < 4; ++g) tmem_st8(p_mem + h * 32 + g * 8, p + g * 8);
                 tmem_wait_st();
                 tmem_fence_before();
                 bar_arrive(shared_addr(&bars.p_full[t][h]));
@@ -262,6 +272,16 @@ k_attend_tile(AttnArgs a, AttnPlan pl, const __grid_constant__ CUtensorMap k_map
 #pragma unroll
             for (int x = 0; x < 4; ++x) mx[x] = fmaxf(mx[x], __uint_as_float(s[kBlock - 4 + x]));
             const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * a.scale_log2;
+            // O and P are free once the last block's O += P V is done (where S and
+            // P share their place, S says so)
+            if (S::AHEAD && j > tr.b0) {
+                ok = bar_wait(shared_addr(&bars.o_full[t]), phase ^ 1);
+                if (!__all_sync(0xffffffffu, ok)) {
+                    ok = false;
+                    break;
+                }
+                tmem_fence_after();
+            }
             const bool grown = top > m + kGrow || (m == -INFINITY && top > m);
             if (__any_sync(0xffffffffu, grown)) {
                 const float mn = grown ? top : m;
@@ -290,7 +310,7 @@ k_attend_tile(AttnArgs a, AttnPlan pl, const __grid_constant__ CUtensorMap k_map
         float l, l1;
         unpair(sum, &l, &l1);
         l += l1;
-        if (ok && tr.b1 > tr.b0) ok = bar_wait(shared_addr(&bars.o_full[t]), 0);
+        if (ok && tr.b1 > tr.b0) ok = bar_wait(shared_addr(&bars.o_full[t]), S::AHEAD ? phase ^ 1 : 0);
         if (!__all_sync(0xffffffffu, ok)) {
             ok = false;
         } else {
@@ -407,20 +427,14 @@ k_attend_tile(AttnArgs a, AttnPlan pl, const __grid_constant__ CUtensorMap k_map
         }
     } else if (warp < 10) {
         // ------------------------------------------------------------ products
-        // A warp a tile: while one waits the other's products run.  They take
-        // turns, a block's products of one tile after those of the other, so that
-        // one tile is in its softmax while the other's products run; left to
-        // themselves both tiles fell into step and the tensor core idled in both
-        // softmaxes (8192-token prompt: 496 us against TURNS).  The turn passes
-        // before the last products are issued, as issuing waits for the queue.
+        // A warp a tile: while one waits the other's products run.
         const int t = warp - 8;
         const TileRange tr = t == 0 ? t0 : t1;
         constexpr int format = std::is_same<T, __half>::value ? 0 : 1;
         constexpr uint32_t s_desc = mma_desc(format, kBlock, false), o_desc = mma_desc(format, D, true);
         auto in = [&](int32_t j) { return j >= tr.b0 && j < tr.b1; };
         const uint32_t s_bar = shared_addr(&bars.s_full[t]), p_bar = shared_addr(&bars.p_full[t][0]);
-        const uint32_t my_turn = shared_addr(&bars.turn[t]), your_turn = shared_addr(&bars.turn[t ^ 1]);
-        uint32_t turn_phase = 0;
+        const uint32_t your_turn = shared_addr(&bars.turn[t ^ 1]);
         auto scores = [&](uint32_t k_smem, bool pass) {
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) {
@@ -455,60 +469,107 @@ k_attend_tile(AttnArgs a, AttnPlan pl, const __grid_constant__ CUtensorMap k_map
             __syncwarp();
             next();
         }
-        for (int32_t j = j0; j < j1; ++j) {
-            wait(shared_addr(&bars.full[at]), lap);
-            const uint32_t v_at = at, v_smem = ring + at * S::BLOCK_BYTES;
-            next();
-            // Values past the request's last key are whatever the page holds:
-            // zeros in their place (the weights there are 0, but 0 * NaN is not).
-            if (!E4M3 && (j + 1) * static_cast<int64_t>(kBlock) > r.kv_len) {
-                if (t == 0 && ok) {
-                    const int dead = r.kv_len - j * kBlock;                // first row to clear
-                    for (int x = dead * 8 + lane; x < kBlock * 8; x += 32)
+        // Values past the request's last key are whatever the page holds: zeros in
+        // their place (the weights there are 0, but 0 * NaN is not).
+        auto clear_tail = [&](int32_t j, uint32_t v_smem) {
+            if (E4M3 || (j + 1) * static_cast<int64_t>(kBlock) <= r.kv_len) return;
+            if (t == 0 && ok) {
+                const int dead = r.kv_len - j * kBlock;                    // first row to clear
+                for (int x = dead * 8 + lane; x < kBlock * 8; x += 32)
 #pragma unroll
-                        for (int h = 0; h < S::HALVES; ++h)
-                            asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(v_smem + h * (kBlock * 128) + x * 16),
-                                         "r"(0)
-                                         : "memory");
-                    fence_shared_async();
-                }
-                asm volatile("bar.sync 1, 64;" ::: "memory");              // both product warps
+                    for (int h = 0; h < S::HALVES; ++h)
+                        asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(v_smem + h * (kBlock * 128) + x * 16), "r"(0)
+                                     : "memory");
+                fence_shared_async();
             }
-            const bool then = j + 1 < j1;
-            if (then) wait(shared_addr(&bars.full[at]), lap);
-            const bool now = in(j), first = j == tr.b0;
-            if (now) wait(p_bar, p_phase);
-            if (j > j0 || t == 1) {
-                wait(my_turn, turn_phase);
-                turn_phase ^= 1;
-            }
-            if (now) {
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    if (h == 1) wait(p_bar + 8, p_phase);
-                    tmem_fence_after();
-                    if (ok && elect_one()) {
-#pragma unroll
-                        for (int k = h * (kBlock / 32); k < (h + 1) * (kBlock / 32); ++k)
-                            mma_ts(tmem + 2 * kBlock + t * D, tmem + t * kBlock + k * 8,
-                                   operand_desc(v_smem + k * 2048, kBlock * 128, 1024), o_desc, !(first && k == 0));
-                    }
-                    __syncwarp();
-                }
-                p_phase ^= 1;
-            }
+            asm volatile("bar.sync 1, 64;" ::: "memory");                  // both product warps
+        };
+        // O += P V, half of the keys as soon as their weights are there.
+        auto half_product = [&](int h, uint32_t v_smem, bool first) {
+            tmem_fence_after();
             if (ok && elect_one()) {
-                mma_commit(shared_addr(&bars.empty[v_at]));
-                if (then && in(j + 1)) {
-                    scores(ring + at * S::BLOCK_BYTES, true);
-                } else {
-                    bar_arrive(your_turn);
-                    if (now) mma_commit(shared_addr(&bars.o_full[t]));
-                }
-                if (then) mma_commit(shared_addr(&bars.empty[at]));
+#pragma unroll
+                for (int k = h * (kBlock / 32); k < (h + 1) * (kBlock / 32); ++k)
+                    mma_ts(tmem + 2 * kBlock + t * D, tmem + S::P_COL + t * S::P_STEP + k * 8,
+                           operand_desc(v_smem + k * 2048, kBlock * 128, 1024), o_desc, !(first && k == 0));
             }
             __syncwarp();
-            if (then) next();
+        };
+        if constexpr (S::AHEAD) {
+            uint32_t read_phase = 0;
+            for (int32_t j = j0; j < j1; ++j) {
+                const uint32_t v_at = at, v_lap = lap, v_smem = ring + at * S::BLOCK_BYTES;
+                const bool now = in(j), then = j + 1 < j1;
+                next();
+                if (then) {                                                // the next block's S first
+                    wait(shared_addr(&bars.full[at]), lap);
+                    if (now) {
+                        wait(shared_addr(&bars.s_read[t]), read_phase);
+                        read_phase ^= 1;
+                    }
+                    tmem_fence_after();
+                    if (ok && elect_one()) {
+                        if (in(j + 1)) scores(ring + at * S::BLOCK_BYTES, false);
+                        mma_commit(shared_addr(&bars.empty[at]));
+                    }
+                    __syncwarp();
+                    next();
+                }
+                wait(shared_addr(&bars.full[v_at]), v_lap);
+                clear_tail(j, v_smem);
+                if (now) {
+                    wait(p_bar, p_phase);
+                    half_product(0, v_smem, j == tr.b0);
+                    wait(p_bar + 8, p_phase);
+                    half_product(1, v_smem, j == tr.b0);
+                    p_phase ^= 1;
+                }
+                if (ok && elect_one()) {
+                    if (now) mma_commit(shared_addr(&bars.o_full[t]));
+                    mma_commit(shared_addr(&bars.empty[v_at]));
+                }
+                __syncwarp();
+            }
+        } else {
+            // They take turns, a block's products of one tile after those of the
+            // other, so that one tile is in its softmax while the other's products
+            // run; left to themselves both tiles fell into step and the tensor core
+            // idled in both softmaxes (8192-token prompt: 496 us against 473).
+            // The turn passes before the last products are issued, as issuing
+            // waits for the queue.
+            const uint32_t my_turn = shared_addr(&bars.turn[t]);
+            uint32_t turn_phase = 0;
+            for (int32_t j = j0; j < j1; ++j) {
+                wait(shared_addr(&bars.full[at]), lap);
+                const uint32_t v_at = at, v_smem = ring + at * S::BLOCK_BYTES;
+                next();
+                clear_tail(j, v_smem);
+                const bool then = j + 1 < j1, now = in(j);
+                if (then) wait(shared_addr(&bars.full[at]), lap);
+                if (now) wait(p_bar, p_phase);
+                if (j > j0 || t == 1) {
+                    wait(my_turn, turn_phase);
+                    turn_phase ^= 1;
+                }
+                if (now) {
+                    half_product(0, v_smem, j == tr.b0);
+                    wait(p_bar + 8, p_phase);
+                    half_product(1, v_smem, j == tr.b0);
+                    p_phase ^= 1;
+                }
+                if (ok && elect_one()) {
+                    mma_commit(shared_addr(&bars.empty[v_at]));
+                    if (then && in(j + 1)) {
+                        scores(ring + at * S::BLOCK_BYTES, true);
+                    } else {
+                        bar_arrive(your_turn);
+                        if (now) mma_commit(shared_addr(&bars.o_full[t]));
+                    }
+                    if (then) mma_commit(shared_addr(&bars.empty[at]));
+                }
+                __syncwarp();
+                if (then) next();
+            }
         }
         // All products done before the CTA ends.
         if (elect_one()) mma_commit(shared_addr(&bars.drain[t]));
