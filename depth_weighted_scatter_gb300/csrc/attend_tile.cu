@@ -67,10 +67,8 @@ struct TileShape {
     static constexpr int SMEM = 1024 + 2 * Q_BYTES + STAGES * BLOCK_BYTES; // 1024: alignment
 };
 
-struct __align__(16) TileBars {            // shared memory
+struct TileBars {                          // shared memory
     uint64_t full[8], empty[8];            // ring
-    uint64_t claim_full, claim_empty;      // the next CTA to take over
-    uint4 claim;
     uint64_t q_full[2], s_full[2], p_full[2][2], s_read[2], o_full[2], turn[2], drain[2];
     uint32_t tmem, failed;
 };
@@ -92,57 +90,6 @@ __device__ __forceinline__ TileRange tile_range(const AttnArgs &a, const Request
     return {lo / kBlock, (hi - 1) / kBlock + 1};
 }
 
-// What the CTA at (x, y, z) of the grid computes: two row tiles over a chunk of a
-// request's keys.  x: row tiles (the longest first) by key heads; y: chunks; z:
-// requests.
-struct TileWork {
-    int hk, b, chunk, n_used;
-    Request r;
-    int32_t rows, row0, c0;
-    int64_t c1;
-    TileRange t0, t1;
-    int32_t j0, j1;                        // blocks of either tile
-    const int32_t *table;
-    bool some;                             // false: nothing
-
-    __device__ __forceinline__ TileWork(const AttnArgs &a, const AttnPlan &pl, int x, int y, int z) {
-        hk = x % a.Hk;
-        b = z;
-        chunk = y;
-        r = request_of(a, b);
-        rows = r.q_rows * a.G;
-        row0 = static_cast<int32_t>(gridDim.x / a.Hk - 1 - x / a.Hk) * (2 * kTileRows);
-        int32_t base;
-        n_used = chunks_of(a, r, pl.chunk, pl.n_chunks, pl.align, &base);
-        some = row0 < rows && chunk < n_used;
-        c0 = base + chunk * pl.chunk;
-        c1 = static_cast<int64_t>(c0) + pl.chunk;
-        if (some) {
-            t0 = tile_range(a, r, row0, rows, c0, c1);
-            t1 = tile_range(a, r, row0 + kTileRows, rows, c0, c1);
-        } else {
-            t0 = t1 = {0, 0};
-        }
-        j0 = t0.b1 == 0 ? t1.b0 : t1.b1 == 0 ? t0.b0 : min(t0.b0, t1.b0);
-        j1 = max(t0.b1, t1.b1);
-        table = a.pg.block_table + static_cast<int64_t>(b) * a.pg.table_pages;
-    }
-};
-
-// A row that could not be finished.
-template <typename T, int D>
-__device__ __noinline__ void nan_row(const AttnArgs &a, const AttnPlan &pl, const TileWork &wk, int32_t row) {
-    if (wk.n_used > 1) {
-        *reinterpret_cast<float2 *>(a.part_ml + part_row(a, pl, wk.b, wk.hk, wk.chunk, row) * 2) = make_float2(NAN, NAN);
-        return;
-    }
-    const int64_t token = wk.r.q0 + row / a.G;
-    const int32_t h = wk.hk * a.G + row % a.G;
-    T *op = static_cast<T *>(a.out.p) + token * a.out.token_stride + h * a.out.head_stride;
-    for (int c = 0; c < D; ++c) op[c] = static_cast<T>(NAN);
-    if (a.lse) a.lse[token * a.Hq + h] = NAN;
-}
-
 template <typename T, bool E4M3, int D>
 __global__ void __launch_bounds__(TileShape<E4M3, D>::THREADS, 1)
 k_attend_tile(AttnArgs a, AttnPlan pl, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
@@ -150,6 +97,22 @@ k_attend_tile(AttnArgs a, AttnPlan pl, const __grid_constant__ CUtensorMap k_map
     extern __shared__ uint8_t raw_smem[];
     __shared__ TileBars bars;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+
+    // x: row tiles (the longest first) by key heads; y: chunks; z: requests.
+    const int hk = blockIdx.x % a.Hk, b = blockIdx.z, chunk = blockIdx.y;
+    const Request r = request_of(a, b);
+    const int32_t rows = r.q_rows * a.G;
+    const int32_t row0 = static_cast<int32_t>(gridDim.x / a.Hk - 1 - blockIdx.x / a.Hk) * (2 * kTileRows);
+    if (row0 >= rows) return;
+    int32_t base;
+    const int n_used = chunks_of(a, r, pl.chunk, pl.n_chunks, pl.align, &base);
+    if (chunk >= n_used) return;
+    const int32_t c0 = base + chunk * pl.chunk;
+    const int64_t c1 = static_cast<int64_t>(c0) + pl.chunk;
+    const TileRange t0 = tile_range(a, r, row0, rows, c0, c1), t1 = tile_range(a, r, row0 + kTileRows, rows, c0, c1);
+    const int32_t j0 = t0.b1 == 0 ? t1.b0 : t1.b1 == 0 ? t0.b0 : min(t0.b0, t1.b0);
+    const int32_t j1 = max(t0.b1, t1.b1);
+    const int32_t *table = a.pg.block_table + static_cast<int64_t>(b) * a.pg.table_pages;
 
     const uint32_t smem = (shared_addr(raw_smem) + 1023) & ~1023u;
     const uint32_t q_smem = smem, ring = smem + 2 * S::Q_BYTES;
@@ -168,9 +131,6 @@ k_attend_tile(AttnArgs a, AttnPlan pl, const __grid_constant__ CUtensorMap k_map
             bar_init(shared_addr(&bars.turn[t]), 1);
             bar_init(shared_addr(&bars.drain[t]), 1);
         }
-        bar_init(shared_addr(&bars.claim_full), 1);
-        bar_init(shared_addr(&bars.claim_empty), 10 + S::LOADERS);         // softmax, product and loader warps
-        bars.claim = make_uint4(0, 0, 0, 0);
         bars.failed = 0;
         bar_init_fence();
     }
@@ -180,31 +140,6 @@ k_attend_tile(AttnArgs a, AttnPlan pl, const __grid_constant__ CUtensorMap k_map
     tmem_fence_after();
     const uint32_t tmem = bars.tmem;
     bool ok = true;
-    // The SM's next piece of work: each warp that works reads the answer to the
-    // loader's claim.  The CTA goes on with another's place in the grid, so that
-    // its set-up is paid once and the next keys are on their way during this
-    // work's end; which CTA gets what is settled as SMs come free.
-    int x = blockIdx.x, y = blockIdx.y, z = blockIdx.z;
-    uint32_t claims = 0;
-    const uint32_t claim = shared_addr(&bars.claim), claim_full = shared_addr(&bars.claim_full),
-                   claim_empty = shared_addr(&bars.claim_empty);
-    auto next_work = [&]() {
-        const bool answered = __all_sync(0xffffffffu, bar_wait(claim_full, claims & 1));
-        ++claims;
-        ok = ok && answered;
-        if (!ok) return false;
-        const bool more = claimed_cta(claim, &x, &y, &z);
-        __syncwarp();
-        if (lane == 0) bar_arrive(claim_empty);
-        return more;
-    };
-    auto claim_next = [&]() {                                              // one thread
-        if (!bar_wait(claim_empty, (claims & 1) ^ 1)) return false;        // everyone has read the last answer
-        fence_shared_async();
-        bar_expect(claim_full, 16);
-        claim_cta(claim, claim_full);
-        return true;
-    };
     if (warp < 8)
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(S::SOFTMAX_REGS));
     else if (warp < 12)
@@ -215,49 +150,43 @@ k_attend_tile(AttnArgs a, AttnPlan pl, const __grid_constant__ CUtensorMap k_map
     if (warp < 8) {
         // ------------------------------------------------------------ softmax
         const int t = warp >> 2, tid = threadIdx.x & 127;
-        uint32_t phase = 0, o_phase = 0;
-        do {
-        const TileWork wk(a, pl, x, y, z);
-        if (!wk.some) continue;
-        const Request &r = wk.r;
-        const int hk = wk.hk, b = wk.b, chunk = wk.chunk, n_used = wk.n_used;
-        const int32_t rows = wk.rows, c0 = wk.c0;
-        const int64_t c1 = wk.c1;
-        const TileRange tr = t == 0 ? wk.t0 : wk.t1;
-        const int32_t tile0 = wk.row0 + t * kTileRows;
+        const TileRange tr = t == 0 ? t0 : t1;
+        const int32_t tile0 = row0 + t * kTileRows;
+        const int32_t row = tile0 + tid, warp0 = tile0 + (warp & 3) * 32;  // this thread's row, the warp's first
+        const bool used = row < rows;
+        int32_t lo = 0, hi = INT32_MAX;                                    // a place past the last row sees all, and is not kept
+        int64_t token = 0;
+        int32_t h = 0;
+        if (used) {
+            const int32_t i = row / a.G;
+            token = r.q0 + i;
+            h = hk * a.G + row - i * a.G;
+            seen_keys(a, r, i, &lo, &hi);
+        }
         if (tr.b1 > tr.b0) {
-            // 16-byte pieces of a row, rows of one step of the warpgroup; all
-            // pieces of a thread in flight
-            constexpr int CPR = D / 8, RPI = kTileRows / CPR, N = kTileRows / RPI;
-            const int c = tid % CPR;
-            {
-                uint4 w[N];
+            // The warp's 32 rows of queries, 16 bytes a lane and all of them in
+            // flight; where a row starts is known to its own lane.
+            constexpr int CPR = D / 8, RPI = 32 / CPR, N = 32 / RPI;       // 16-byte pieces of a row; rows a load
+            const int64_t at = token * a.q.token_stride + h * a.q.head_stride;
+            const int c = lane % CPR;
+            uint4 w[N];
 #pragma unroll
-                for (int i = 0; i < N; ++i) {
-                    const int32_t gr = tile0 + i * RPI + tid / CPR;
-                    w[i] = make_uint4(0, 0, 0, 0);
-                    if (gr < rows)
-                        w[i] = *reinterpret_cast<const uint4 *>(static_cast<const T *>(a.q.p) +
-                                                                static_cast<int64_t>(r.q0 + gr / a.G) * a.q.token_stride +
-                                                                (hk * a.G + gr % a.G) * a.q.head_stride + c * 8);
-                }
+            for (int i = 0; i < N; ++i) {
+                const int x = i * RPI + lane / CPR;
+                const int64_t at_x = __shfl_sync(0xffffffffu, at, x);
+                w[i] = make_uint4(0, 0, 0, 0);
+                if (warp0 + x < rows) w[i] = *reinterpret_cast<const uint4 *>(static_cast<const T *>(a.q.p) + at_x + c * 8);
+            }
 #pragma unroll
-                for (int i = 0; i < N; ++i) {
-                    const int row = i * RPI + tid / CPR;
-                    const uint32_t d =
-                        q_smem + t * S::Q_BYTES + (c >> 3) * (kTileRows * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4);
-                    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(d), "r"(w[i].x), "r"(w[i].y), "r"(w[i].z),
-                                 "r"(w[i].w)
-                                 : "memory");
-                }
+            for (int i = 0; i < N; ++i) {
+                const int x = (warp & 3) * 32 + i * RPI + lane / CPR;
+                const uint32_t d = q_smem + t * S::Q_BYTES + (c >> 3) * (kTileRows * 128) + x * 128 + (((c & 7) ^ (x & 7)) << 4);
+                asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(d), "r"(w[i].x), "r"(w[i].y), "r"(w[i].z), "r"(w[i].w)
+                             : "memory");
             }
             fence_shared_async();
             bar_arrive(shared_addr(&bars.q_full[t]));
         }
-        const int32_t row = tile0 + tid;
-        const bool used = row < rows;
-        int32_t lo = 0, hi = INT32_MAX;                                    // a place past the last row sees all, and is not kept
-        if (used) seen_keys(a, r, row / a.G, &lo, &hi);
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t s_mem = tmem + lanes + t * kBlock, p_mem = tmem + lanes + S::P_COL + t * S::P_STEP, o_mem = tmem + lanes + 2 * kBlock + t * D;
         float m = -INFINITY;                                               // the scale in use (base 2)
@@ -268,13 +197,14 @@ k_attend_tile(AttnArgs a, AttnPlan pl, const __grid_constant__ CUtensorMap k_map
             if (lane < kBlock / 16) {
                 const int32_t k = j * kBlock + lane * 16;
                 if (k < r.kv_len) {
-                    const int32_t p = wk.table[k >> a.pg.page_shift];
+                    const int32_t p = table[k >> a.pg.page_shift];
                     hole = p < 0 || p >= a.pg.n_pages;
                 }
             }
             return hole;
         };
         bool hole = tr.b1 > tr.b0 ? holes_of(tr.b0) : false;
+        uint32_t phase = 0;
         for (int32_t j = tr.b0; j < tr.b1; ++j, phase ^= 1) {
             const uint32_t holes = __ballot_sync(0xffffffffu, hole);
             if (j + 1 < tr.b1) hole = holes_of(j + 1);
@@ -347,12 +277,11 @@ k_attend_tile(AttnArgs a, AttnPlan pl, const __grid_constant__ CUtensorMap k_map
             // O and P are free once the last block's O += P V is done (where S and
             // P share their place, S says so)
             if (S::AHEAD && j > tr.b0) {
-                ok = bar_wait(shared_addr(&bars.o_full[t]), o_phase);
+                ok = bar_wait(shared_addr(&bars.o_full[t]), phase ^ 1);
                 if (!__all_sync(0xffffffffu, ok)) {
                     ok = false;
                     break;
                 }
-                o_phase ^= 1;
                 tmem_fence_after();
             }
             const bool grown = top > m + kGrow || (m == -INFINITY && top > m);
@@ -383,29 +312,18 @@ k_attend_tile(AttnArgs a, AttnPlan pl, const __grid_constant__ CUtensorMap k_map
         float l, l1;
         unpair(sum, &l, &l1);
         l += l1;
-        if (ok && tr.b1 > tr.b0) {
-            ok = bar_wait(shared_addr(&bars.o_full[t]), o_phase);
-            o_phase ^= 1;
-        }
-        if (!__all_sync(0xffffffffu, ok)) {                                // rows of NaN
+        if (ok && tr.b1 > tr.b0) ok = bar_wait(shared_addr(&bars.o_full[t]), S::AHEAD ? phase ^ 1 : 0);
+        if (!__all_sync(0xffffffffu, ok)) {
             ok = false;
-            if (used) nan_row<T, D>(a, pl, wk, row);
         } else {
             tmem_fence_after();
             const bool some = !(l == 0.0f);
-            const int64_t token = r.q0 + (used ? row / a.G : 0);
-            const int32_t h = hk * a.G + (used ? row % a.G : 0);
             const float inv = some ? a.v_scale / l : 0.0f;
             const int64_t part = n_used > 1 && used ? part_row(a, pl, b, hk, chunk, row) : 0;
             bool fine = l - l == 0.0f;
-            // O leaves through shared memory (where this warp's queries were), so
+            // O leaves through shared memory (over the queries, read by now), so
             // that a warp's stores cover whole rows.
-            const int32_t warp0 = tile0 + (warp & 3) * 32;                 // the warp's first row
             const uint32_t stage = q_smem + t * S::Q_BYTES + (warp & 3) * 32 * (D * 2);
-            auto row_out = [&](int x, int64_t *token_x, int32_t *h_x) {
-                *token_x = r.q0 + (warp0 + x) / a.G;
-                *h_x = hk * a.G + (warp0 + x) % a.G;
-            };
             if (n_used == 1) {
                 constexpr int CPR = D / 8;                                 // 16-byte pieces of a row
 #pragma unroll
@@ -431,19 +349,15 @@ k_attend_tile(AttnArgs a, AttnPlan pl, const __grid_constant__ CUtensorMap k_map
                 }
                 __syncwarp();
                 const int c = lane % CPR;
+                const int64_t at = token * a.out.token_stride + h * a.out.head_stride;
 #pragma unroll 4
                 for (int x = lane / CPR; x < 32; x += 32 / CPR) {
                     uint4 w;
                     const uint32_t d = stage + x * (D * 2) + ((c ^ (x & 7)) << 4);
                     asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w) : "r"(d)
                                  : "memory");
-                    if (warp0 + x < rows) {
-                        int64_t token_x;
-                        int32_t h_x;
-                        row_out(x, &token_x, &h_x);
-                        *reinterpret_cast<uint4 *>(static_cast<T *>(a.out.p) + token_x * a.out.token_stride +
-                                                   h_x * a.out.head_stride + c * 8) = w;
-                    }
+                    const int64_t at_x = __shfl_sync(0xffffffffu, at, x);
+                    if (warp0 + x < rows) *reinterpret_cast<uint4 *>(static_cast<T *>(a.out.p) + at_x + c * 8) = w;
                 }
                 __syncwarp();
             } else if (tr.b1 > tr.b0) {
@@ -502,13 +416,14 @@ k_attend_tile(AttnArgs a, AttnPlan pl, const __grid_constant__ CUtensorMap k_map
                 store_row<T, D / 32>(a, pl, r, b, hk, rr / a.G, hk * a.G + rr % a.G, rr, chunk, n_used, m1, s1, acc);
             }
         }
-        } while (next_work());
     } else if (warp < 10) {
         // ------------------------------------------------------------ products
         // A warp a tile: while one waits the other's products run.
         const int t = warp - 8;
+        const TileRange tr = t == 0 ? t0 : t1;
         constexpr int format = std::is_same<T, __half>::value ? 0 : 1;
         constexpr uint32_t s_desc = mma_desc(format, kBlock, false), o_desc = mma_desc(format, D, true);
+        auto in = [&](int32_t j) { return j >= tr.b0 && j < tr.b1; };
         const uint32_t s_bar = shared_addr(&bars.s_full[t]), p_bar = shared_addr(&bars.p_full[t][0]);
         const uint32_t your_turn = shared_addr(&bars.turn[t ^ 1]);
         auto scores = [&](uint32_t k_smem, bool pass) {
@@ -528,24 +443,15 @@ k_attend_tile(AttnArgs a, AttnPlan pl, const __grid_constant__ CUtensorMap k_map
                 lap ^= 1;
             }
         };
-        uint32_t p_phase = 0, q_phase = 0, read_phase = 0, turn_phase = 0;
-        bool turns = t == 1;                                               // whether the other has passed a turn
+        uint32_t p_phase = 0;
         // A wait that ran out ends the products, not the walk: both warps meet at
         // the tail's barrier.
         auto wait = [&](uint32_t bar, uint32_t parity) {
-            if (ok) ok = __all_sync(0xffffffffu, bar_wait(bar, parity));
+            if (ok) ok = bar_wait(bar, parity);
         };
-        do {
-        const TileWork wk(a, pl, x, y, z);
-        const int32_t j0 = wk.j0, j1 = wk.j1;
-        const TileRange tr = t == 0 ? wk.t0 : wk.t1;
-        auto in = [&](int32_t j) { return j >= tr.b0 && j < tr.b1; };
         // Every block's K and V are let go by both warps, used or not.
         if (j1 > j0) {
-            if (tr.b1 > 0) {
-                wait(shared_addr(&bars.q_full[t]), q_phase);
-                q_phase ^= 1;
-            }
+            if (tr.b1 > 0) wait(shared_addr(&bars.q_full[t]), 0);
             wait(shared_addr(&bars.full[at]), lap);
             if (ok && elect_one()) {
                 if (in(j0)) scores(ring + at * S::BLOCK_BYTES, false);
@@ -557,9 +463,9 @@ k_attend_tile(AttnArgs a, AttnPlan pl, const __grid_constant__ CUtensorMap k_map
         // Values past the request's last key are whatever the page holds: zeros in
         // their place (the weights there are 0, but 0 * NaN is not).
         auto clear_tail = [&](int32_t j, uint32_t v_smem) {
-            if (E4M3 || (j + 1) * static_cast<int64_t>(kBlock) <= wk.r.kv_len) return;
+            if (E4M3 || (j + 1) * static_cast<int64_t>(kBlock) <= r.kv_len) return;
             if (t == 0 && ok) {
-                const int dead = wk.r.kv_len - j * kBlock;                    // first row to clear
+                const int dead = r.kv_len - j * kBlock;                    // first row to clear
                 for (int x = dead * 8 + lane; x < kBlock * 8; x += 32)
 #pragma unroll
                     for (int h = 0; h < S::HALVES; ++h)
@@ -581,16 +487,17 @@ k_attend_tile(AttnArgs a, AttnPlan pl, const __grid_constant__ CUtensorMap k_map
             __syncwarp();
         };
         if constexpr (S::AHEAD) {
+            uint32_t read_phase = 0;
             for (int32_t j = j0; j < j1; ++j) {
                 const uint32_t v_at = at, v_lap = lap, v_smem = ring + at * S::BLOCK_BYTES;
                 const bool now = in(j), then = j + 1 < j1;
                 next();
-                if (then) wait(shared_addr(&bars.full[at]), lap);
-                if (now) {
-                    wait(shared_addr(&bars.s_read[t]), read_phase);
-                    read_phase ^= 1;
-                }
                 if (then) {                                                // the next block's S first
+                    wait(shared_addr(&bars.full[at]), lap);
+                    if (now) {
+                        wait(shared_addr(&bars.s_read[t]), read_phase);
+                        read_phase ^= 1;
+                    }
                     tmem_fence_after();
                     if (ok && elect_one()) {
                         if (in(j + 1)) scores(ring + at * S::BLOCK_BYTES, false);
@@ -622,6 +529,7 @@ k_attend_tile(AttnArgs a, AttnPlan pl, const __grid_constant__ CUtensorMap k_map
             // The turn passes before the last products are issued, as issuing
             // waits for the queue.
             const uint32_t my_turn = shared_addr(&bars.turn[t]);
+            uint32_t turn_phase = 0;
             for (int32_t j = j0; j < j1; ++j) {
                 wait(shared_addr(&bars.full[at]), lap);
                 const uint32_t v_at = at, v_smem = ring + at * S::BLOCK_BYTES;
@@ -630,11 +538,10 @@ k_attend_tile(AttnArgs a, AttnPlan pl, const __grid_constant__ CUtensorMap k_map
                 const bool then = j + 1 < j1, now = in(j);
                 if (then) wait(shared_addr(&bars.full[at]), lap);
                 if (now) wait(p_bar, p_phase);
-                if (turns) {
+                if (j > j0 || t == 1) {
                     wait(my_turn, turn_phase);
                     turn_phase ^= 1;
                 }
-                turns = true;
                 if (now) {
                     half_product(0, v_smem, j == tr.b0);
                     wait(p_bar + 8, p_phase);
@@ -655,7 +562,6 @@ k_attend_tile(AttnArgs a, AttnPlan pl, const __grid_constant__ CUtensorMap k_map
                 if (then) next();
             }
         }
-        } while (next_work());
         // All products done before the CTA ends.
         if (elect_one()) mma_commit(shared_addr(&bars.drain[t]));
         __syncwarp();
@@ -669,22 +575,19 @@ k_attend_tile(AttnArgs a, AttnPlan pl, const __grid_constant__ CUtensorMap k_map
         const int boxes = per * S::HALVES;
         const int page_i = lane / S::HALVES, half = lane % S::HALVES;
         uint32_t at = 0, lap = 0;
-        int issued = 0;
-        do {
-        const TileWork wk(a, pl, x, y, z);
-        const int32_t j0 = wk.j0, j1 = wk.j1;
         // Page of this lane's box in block j; n_pages (past the pool: the box
         // fills with zeros) where there is none.
         auto page_of = [&](int32_t j) {
             const int32_t k = j * kBlock + page_i * high;
             int32_t p = a.pg.n_pages;
-            if (lane < boxes && j < j1 && k < wk.r.kv_len) {
-                const int32_t x = wk.table[k >> a.pg.page_shift];
+            if (lane < boxes && j < j1 && k < r.kv_len) {
+                const int32_t x = table[k >> a.pg.page_shift];
                 if (x >= 0 && x < a.pg.n_pages) p = x;
             }
             return p;
         };
         int32_t page = page_of(j0);
+        int issued = 0;
         for (int32_t j = j0; j < j1 && ok; ++j) {
             const int32_t now = page;
             page = page_of(j + 1);
@@ -701,7 +604,7 @@ k_attend_tile(AttnArgs a, AttnPlan pl, const __grid_constant__ CUtensorMap k_map
                 __syncwarp();
                 if (lane < boxes)
                     tma_load_4d(ring + at * S::BLOCK_BYTES + half * (kBlock * 128) + page_i * high * 128, kv ? &v_map : &k_map,
-                                full, half * 64, slot, wk.hk, now);
+                                full, half * 64, slot, hk, now);
                 ++issued;
                 if (++at == S::STAGES) {
                     at = 0;
@@ -709,9 +612,6 @@ k_attend_tile(AttnArgs a, AttnPlan pl, const __grid_constant__ CUtensorMap k_map
                 }
             }
         }
-        if (lane == 0) ok = claim_next() && ok;
-        ok = __all_sync(0xffffffffu, ok);
-        } while (next_work());
         // All copies landed before the CTA ends.
         for (int i = 0; i < S::STAGES && i < issued; ++i) {
             if (at == 0) lap ^= 1;
@@ -725,9 +625,6 @@ k_attend_tile(AttnArgs a, AttnPlan pl, const __grid_constant__ CUtensorMap k_map
         constexpr int N = kBlock / RPI;
         const int tid = threadIdx.x - S::FIRST_LOADER * 32, c = tid % CPR, row_i = tid / CPR;
         uint32_t at = 0, lap = 0;
-        do {
-        const TileWork wk(a, pl, x, y, z);
-        const int32_t j0 = wk.j0, j1 = wk.j1;
         uint4 w[N];
         auto load = [&](int32_t j, int kv) {
             const uint8_t *cache = static_cast<const uint8_t *>(kv ? a.v_cache : a.k_cache);
@@ -735,7 +632,7 @@ k_attend_tile(AttnArgs a, AttnPlan pl, const __grid_constant__ CUtensorMap k_map
 #pragma unroll
             for (int i = 0; i < N; ++i) {
                 const int32_t k = j * kBlock + i * RPI + row_i;
-                p[i] = j < j1 && k < wk.r.kv_len ? wk.table[k >> a.pg.page_shift] : -1;
+                p[i] = j < j1 && k < r.kv_len ? table[k >> a.pg.page_shift] : -1;
             }
 #pragma unroll
             for (int i = 0; i < N; ++i) {
@@ -744,7 +641,7 @@ k_attend_tile(AttnArgs a, AttnPlan pl, const __grid_constant__ CUtensorMap k_map
                 if (p[i] >= 0 && p[i] < a.pg.n_pages)
                     w[i] = *reinterpret_cast<const uint4 *>(cache + p[i] * a.pg.page_stride +
                                                             (k & (a.pg.page_size - 1)) * a.pg.slot_stride +
-                                                            wk.hk * a.pg.head_stride + c * 16);
+                                                            hk * a.pg.head_stride + c * 16);
             }
         };
         auto store = [&](int kv) {
@@ -786,23 +683,29 @@ k_attend_tile(AttnArgs a, AttnPlan pl, const __grid_constant__ CUtensorMap k_map
                 }
             }
         }
-        if (tid == 0) ok = claim_next() && ok;
-        ok = __all_sync(0xffffffffu, ok);
-        } while (next_work());
     }
     if (!ok && lane == 0) bars.failed = 1;
     tmem_fence_before();
     __syncthreads();
     tmem_fence_after();
     if (warp == 8) tmem_free<512>(tmem);
-    if (bars.failed) {                                                     // a wait ran out: counted, and a claim not worked off is NaN
+    if (bars.failed) {                                                     // a wait ran out: rows of NaN, and counted
         if (threadIdx.x == 0) atomicAdd(&g_attention_timeouts, 1ull);
-        if (claimed_cta(claim, &x, &y, &z)) {
-            const TileWork wk(a, pl, x, y, z);
-            const int32_t row = wk.row0 + static_cast<int32_t>(threadIdx.x);
-            if (wk.some && threadIdx.x < 2 * kTileRows && row < wk.rows) nan_row<T, D>(a, pl, wk, row);
+        const int32_t row = row0 + static_cast<int32_t>(threadIdx.x);
+        if (warp < 8 && row < rows) {
+            const int64_t token = r.q0 + row / a.G;
+            const int32_t h = hk * a.G + row % a.G;
+            T *op = static_cast<T *>(a.out.p) + token * a.out.token_stride + h * a.out.head_stride;
+            if (n_used > 1) {
+                const int64_t part = part_row(a, pl, b, hk, chunk, row);
+                *reinterpret_cast<float2 *>(a.part_ml + part * 2) = make_float2(NAN, NAN);
+            } else {
+                for (int c = 0; c < D; ++c) op[c] = static_cast<T>(NAN);
+                if (a.lse) a.lse[token * a.Hq + h] = NAN;
+            }
         }
     }
+    grid_dep_allow();
 }
 
 // The driver's tensor-map encoder, found through the runtime.

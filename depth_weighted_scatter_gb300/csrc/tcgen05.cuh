@@ -52,32 +52,6 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity) {
 // Generic writes to shared memory before reads by TMA or the tensor core.
 __device__ __forceinline__ void fence_shared_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
-// ---------------------------------------------------------------- taking over CTAs
-
-// Asks for a CTA of this grid that has not been launched; the answer (16 bytes)
-// is counted by bar.
-__device__ __forceinline__ void claim_cta(uint32_t answer, uint32_t bar) {
-    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(answer),
-                 "r"(bar)
-                 : "memory");
-}
-// Whether there was one, and its place in the grid.
-__device__ __forceinline__ bool claimed_cta(uint32_t answer, int *x, int *y, int *z) {
-    uint32_t got, a, b, c;
-    asm volatile(
-        "{\n\t.reg .b128 h;\n\t.reg .pred p;\n\t"
-        "ld.shared.b128 h, [%4];\n\t"
-        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t"
-        "mov.u32 %1, 0;\n\tmov.u32 %2, 0;\n\tmov.u32 %3, 0;\n\t"
-        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%1, %2, %3, _}, h;\n\t}"
-        : "=r"(got), "=r"(a), "=r"(b), "=r"(c)
-        : "r"(answer)
-        : "memory");
-    *x = static_cast<int>(a), *y = static_cast<int>(b), *z = static_cast<int>(c);
-    return got != 0;
-}
-
 // ---------------------------------------------------------------- TMA
 
 // A box of a 4-D tensor into shared memory; its bytes are counted by bar.

@@ -539,3 +539,51 @@ def test_operators_in_a_graph(A):
         want = step(kc2, vc2)
         assert torch.equal(y, want)
     assert torch.equal(kc, kc2) and torch.equal(vc, vc2)
+
+
+MANY = [
+    # q_len, kv_len, Hq, Hk, D, causal, window, dtype, cache, page, token_major: several hundred row tiles and chunks
+    ([700, 1300, 64, 900, 1111], [700, 1500, 4000, 901, 3333], 16, 16, 64, True, 0, F16, "same", 16, False),
+    ([700, 1300, 64, 900, 1111], [700, 1500, 4000, 901, 3333], 16, 8, 128, True, 0, BF16, "same", 64, False),
+    ([1300, 500, 1200], [2000, 3000, 1201], 12, 12, 64, False, 0, BF16, "e4m3", 64, True),
+    ([1300, 500, 1200], [2000, 3000, 1201], 24, 8, 128, True, 600, F16, "e4m3", 32, False),
+    ([300] * 9, [20000, 300, 5000, 9000, 301, 12000, 700, 16000, 8000], 4, 1, 64, True, 0, F16, "same", 128, False),
+    ([90] * 12, [9000 - 700 * i for i in range(12)], 4, 2, 128, True, 0, BF16, "e4m3", 16, False),
+    ([1] * 150, [1 + 37 * i for i in range(150)], 8, 4, 128, True, 0, BF16, "same", 16, False),
+]
+
+
+@pytest.mark.parametrize("case", MANY, ids=lambda c: str(c)[:70])
+def test_attention_many_tiles(A, case):
+    """More row tiles and chunks than the GPU has SMs; rows drawn from all over are held to their definition, and
+    nothing that the call leaves changes when it is made again."""
+    q_len, kv_len, Hq, Hk, D, causal, window, dtype, cache, page, _ = case
+    x = attend_inputs(case, seed=600)
+    poison(x)
+    out, lse = attend(A, x)
+    again = attend(A, x)
+    assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
+    assert out.isfinite().all() and lse.isfinite().all()
+    ks, vs = x.get("k_scale", 1.0), x.get("v_scale", 1.0)
+    u, cu, rng = ref.U[dtype], np.concatenate([[0], np.cumsum(q_len)]), np.random.default_rng(7)
+    for b, (n, m) in enumerate(zip(q_len, kv_len)):
+        pg = x["block_table"][b, :-(-m // page)].long()
+        for i in sorted({0, n - 1, n // 2, *rng.integers(0, n, 5).tolist()}):
+            pos = m - n + i
+            hi, lo = (pos + 1 if causal else m), (max(0, pos - window + 1) if window else 0)
+            for h in {0, Hk - 1, int(rng.integers(0, Hk))}:
+                k, v = (c.float()[pg, h].reshape(-1, D)[lo:hi].double() * f if cache != "e4m3" else
+                        c.view(torch.uint8)[pg, h].view(c.dtype).float().reshape(-1, D)[lo:hi].double() * f
+                        for c, f in ((x["k_cache"], ks), (x["v_cache"], vs)))
+                rows = slice(h * (Hq // Hk), (h + 1) * (Hq // Hk))
+                q = x["q"][cu[b] + i, rows].double()
+                z = q @ k.T * D ** -0.5
+                d = (D + 8) * 2.0 ** -23 * D ** -0.5 * (q.abs() @ k.abs().T).max(-1).values
+                want = torch.logsumexp(z, -1)
+                p = torch.exp(z - want[:, None])
+                o, mag = p @ v, p @ v.abs()
+                sub = 2.0 ** -24 * v.abs().sum(0)[None] if dtype == F16 else 0.0
+                within(out[cu[b] + i, rows], o.cpu(), ((u + 2 * d[:, None] + 2.0 ** -18) * mag + sub + u * o.abs()
+                                                       + ref.tiny(dtype)).cpu(), f"out {b} {i} {h}")
+                within(lse[cu[b] + i, rows], want.cpu(), (d + 2.0 ** -18 + 2.0 ** -22 * want.abs()).cpu(), "lse")
+    assert A.bevpool_attention_timeouts() == 0
