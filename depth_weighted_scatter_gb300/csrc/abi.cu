@@ -145,7 +145,7 @@ const char *bevpool_status_string(bevpool_status status) {
     }
 }
 
-int32_t bevpool_version(void) { return 300; }   // 0.3.0: launch-plan query, gather probe
+int32_t bevpool_version(void) { return 400; }   // 0.4.0: token operators
 
 int64_t bevpool_kernel_launches(void) { return g_kernel_launches.load(std::memory_order_relaxed); }
 

