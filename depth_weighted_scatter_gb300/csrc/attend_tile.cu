@@ -234,10 +234,16 @@ k_attend_tile(AttnArgs a, AttnPlan pl, const __grid_constant__ CUtensorMap k_map
             }
             const int32_t k0 = j * kBlock;
             if (!__all_sync(0xffffffffu, holes == 0 && lo <= k0 && hi - kBlock >= k0)) {
-                const int32_t from = lo - k0, to = hi - k0;
+                // seen keys of the block, 32 a word
 #pragma unroll
-                for (int c = 0; c < kBlock; ++c)
-                    if (c < from || c >= to || ((holes >> (c / 16)) & 1)) s[c] = 0xff800000u;      // -inf
+                for (int w = 0; w < kBlock / 32; ++w) {
+                    const int from = min(max(lo - k0 - 32 * w, 0), 32), to = min(max(hi - k0 - 32 * w, 0), 32);
+                    uint32_t seen = static_cast<uint32_t>((1ull << to) - 1) & ~static_cast<uint32_t>((1ull << from) - 1);
+                    if ((holes >> (2 * w)) & 1) seen &= 0xffff0000u;
+                    if ((holes >> (2 * w)) & 2) seen &= 0x0000ffffu;
+#pragma unroll
+                    for (int c = 0; c < 32; ++c) s[32 * w + c] = (seen >> c) & 1 ? s[32 * w + c] : 0xff800000u;   // -inf
+                }
             }
             // P of one half and its sum, at the scale m.
             const uint64_t scale2 = pair(a.scale_log2, a.scale_log2);
@@ -470,6 +476,12 @@ k_attend_tile(AttnArgs a, AttnPlan pl, const __grid_constant__ CUtensorMap k_map
             __syncwarp();
             next();
         }
+        // V's rows: groups of `high` (a page's, or a block's) of all of the head's
+        // 64-element columns in turn, so that a page's V is one box.
+        const int high = E4M3 || a.pg.page_size > kBlock ? kBlock : a.pg.page_size;
+        auto v_row = [&](int row) {                                        // its first column's bytes
+            return ((row & ~(high - 1)) * S::HALVES + (row & (high - 1))) * 128;
+        };
         // Values past the request's last key are whatever the page holds: zeros in
         // their place (the weights there are 0, but 0 * NaN is not).
         auto clear_tail = [&](int32_t j, uint32_t v_smem) {
@@ -479,12 +491,17 @@ k_attend_tile(AttnArgs a, AttnPlan pl, const __grid_constant__ CUtensorMap k_map
                 for (int x = dead * 8 + lane; x < kBlock * 8; x += 32)
 #pragma unroll
                     for (int h = 0; h < S::HALVES; ++h)
-                        asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(v_smem + h * (kBlock * 128) + x * 16), "r"(0)
+                        asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(v_smem + v_row(x / 8) + h * (high * 128) +
+                                                                                  (x & 7) * 16),
+                                     "r"(0)
                                      : "memory");
                 fence_shared_async();
             }
             asm volatile("bar.sync 1, 64;" ::: "memory");                  // both product warps
         };
+        uint32_t v_off[kBlock / 16];
+#pragma unroll
+        for (int k = 0; k < kBlock / 16; ++k) v_off[k] = v_row(16 * k);
         // O += P V, half of the keys as soon as their weights are there.
         auto half_product = [&](int h, uint32_t v_smem, bool first) {
             tmem_fence_after();
@@ -492,7 +509,7 @@ k_attend_tile(AttnArgs a, AttnPlan pl, const __grid_constant__ CUtensorMap k_map
 #pragma unroll
                 for (int k = h * (kBlock / 32); k < (h + 1) * (kBlock / 32); ++k)
                     mma_ts(tmem + 2 * kBlock + t * D, tmem + S::P_COL + t * S::P_STEP + k * 8,
-                           operand_desc(v_smem + k * 2048, kBlock * 128, 1024), o_desc, !(first && k == 0));
+                           operand_desc(v_smem + v_off[k], high * 128, 1024), o_desc, !(first && k == 0));
             }
             __syncwarp();
         };
@@ -602,6 +619,8 @@ k_attend_tile(AttnArgs a, AttnPlan pl, const __grid_constant__ CUtensorMap k_map
             const int32_t now = page;
             page = page_of(j + 1);
             const int32_t slot = (j * kBlock + page_i * high) & (a.pg.page_size - 1);
+            const int32_t v_now = __shfl_sync(0xffffffffu, now, lane * S::HALVES);   // V's boxes: a lane a page
+            const int32_t v_slot = (j * kBlock + lane * high) & (a.pg.page_size - 1);
 #pragma unroll
             for (int kv = 0; kv < 2; ++kv) {
                 ok = bar_wait(shared_addr(&bars.empty[at]), lap ^ 1);
@@ -612,9 +631,11 @@ k_attend_tile(AttnArgs a, AttnPlan pl, const __grid_constant__ CUtensorMap k_map
                 const uint32_t full = shared_addr(&bars.full[at]);
                 if (lane == 0) bar_expect(full, S::BLOCK_BYTES);
                 __syncwarp();
-                if (lane < boxes)
-                    tma_load_4d(ring + at * S::BLOCK_BYTES + half * (kBlock * 128) + page_i * high * 128, kv ? &v_map : &k_map,
-                                full, half * 64, slot, hk, now);
+                const uint32_t dst = ring + at * S::BLOCK_BYTES;
+                if (kv == 0 && lane < boxes)
+                    tma_load_4d(dst + half * (kBlock * 128) + page_i * high * 128, &k_map, full, half * 64, slot, hk, now);
+                if (kv == 1 && lane < per)
+                    tma_load_5d(dst + lane * high * (S::HALVES * 128), &v_map, full, 0, v_slot, 0, hk, v_now);
                 ++issued;
                 if (++at == S::STAGES) {
                     at = 0;
@@ -735,23 +756,30 @@ EncodeTiled encode_tiled() {
     return fn;
 }
 
-// A 16-bit cache as a 4-D tensor (element, slot, head, page), in boxes of 64
-// elements by the slots of a page that a block takes.
-bool cache_map(const AttnArgs &a, const void *cache, CUtensorMap *map) {
+// A 16-bit cache as a tensor (element, slot, head, page) in boxes of 64 elements
+// by the slots of a page that a block takes; for V the head's 64-element columns
+// are an axis of their own, all of them in a box.  (K's columns have to lie a
+// whole block apart, as one product takes all of its rows.)  Half as many boxes
+// for V count with pages of 16 slots: six ragged chunks 304 us before, 260
+// after.
+bool cache_map(const AttnArgs &a, const void *cache, bool columns, CUtensorMap *map) {
     const EncodeTiled encode = encode_tiled();
     if (!encode) return false;
-    const cuuint64_t dims[4] = {static_cast<cuuint64_t>(a.D), static_cast<cuuint64_t>(a.pg.page_size),
-                                static_cast<cuuint64_t>(a.Hk), static_cast<cuuint64_t>(a.pg.n_pages)};
+    const cuuint64_t slots = static_cast<cuuint64_t>(a.pg.page_size), heads = static_cast<cuuint64_t>(a.Hk),
+                     pages = static_cast<cuuint64_t>(a.pg.n_pages);
     // the stride of an axis of one entry is never used
     const auto stride = [&](int64_t s, int64_t n) { return static_cast<cuuint64_t>(n > 1 ? s : a.D) * 2; };
-    const cuuint64_t strides[3] = {stride(a.pg.slot_stride, a.pg.page_size), stride(a.pg.head_stride, a.Hk),
-                                   stride(a.pg.page_stride, a.pg.n_pages)};
-    const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(a.pg.page_size < kBlock ? a.pg.page_size : kBlock), 1, 1};
-    const cuuint32_t ones[4] = {1, 1, 1, 1};
-    return encode(map, a.dtype == BEVPOOL_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
-                  const_cast<void *>(cache), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    const cuuint64_t slot_s = stride(a.pg.slot_stride, a.pg.page_size), head_s = stride(a.pg.head_stride, a.Hk),
+                     page_s = stride(a.pg.page_stride, a.pg.n_pages);
+    const cuuint32_t high = static_cast<cuuint32_t>(a.pg.page_size < kBlock ? a.pg.page_size : kBlock);
+    const cuuint32_t wide = static_cast<cuuint32_t>(a.D / 64);
+    const cuuint64_t dims4[4] = {static_cast<cuuint64_t>(a.D), slots, heads, pages}, dims5[5] = {64, slots, wide, heads, pages};
+    const cuuint64_t strides4[3] = {slot_s, head_s, page_s}, strides5[4] = {slot_s, 128, head_s, page_s};
+    const cuuint32_t box4[4] = {64, high, 1, 1}, box5[5] = {64, high, wide, 1, 1}, ones[5] = {1, 1, 1, 1, 1};
+    return encode(map, a.dtype == BEVPOOL_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                  columns ? 5 : 4, const_cast<void *>(cache), columns ? dims5 : dims4, columns ? strides5 : strides4,
+                  columns ? box5 : box4, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace
@@ -765,7 +793,7 @@ cudaError_t attention_timeouts(int64_t *count) {
 
 cudaError_t launch_attend_tile(const AttnArgs &a, const AttnPlan &pl) {
     CUtensorMap k_map = {}, v_map = {};
-    if (!a.cache_e4m3 && (!cache_map(a, a.k_cache, &k_map) || !cache_map(a, a.v_cache, &v_map))) return cudaErrorInvalidValue;
+    if (!a.cache_e4m3 && (!cache_map(a, a.k_cache, false, &k_map) || !cache_map(a, a.v_cache, true, &v_map))) return cudaErrorInvalidValue;
     auto run = [&](auto t, auto e4m3, auto d) {
         constexpr bool E = decltype(e4m3)::value;
         constexpr int D = decltype(d)::value;
