@@ -65,6 +65,8 @@ struct TileShape {
     static constexpr int LOADER_REGS = 88;
     static_assert(256 * SOFTMAX_REGS + 128 * PRODUCT_REGS + (E4M3 ? 128 * LOADER_REGS : 0) <= THREADS * LAUNCH_REGS,
                   "the split is within the launch's registers");
+    static_assert(SOFTMAX_REGS >= LAUNCH_REGS && PRODUCT_REGS <= LAUNCH_REGS && (!E4M3 || LOADER_REGS <= LAUNCH_REGS),
+                  "softmax threads gain registers, the others lose some");
     // At head_dim 64 tensor memory has room for P beside S: the next block's S is
     // then made while this block is in its softmax.
     static constexpr bool AHEAD = D == 64;
@@ -72,9 +74,10 @@ struct TileShape {
     static constexpr int P_STEP = AHEAD ? kBlock / 2 : kBlock;
     static constexpr int HALVES = D / 64;                                  // 128-byte columns of a block
     static constexpr int BLOCK_BYTES = kBlock * D * 2;
-    static constexpr int STAGES = D == 128 ? 5 : 8;                        // K and V blocks in turn
+    static constexpr int STAGES = D == 64 ? 8 : E4M3 ? 4 : 5;              // K and V blocks in turn
+    static constexpr int RAW_BYTES = E4M3 ? 2 * kBlock * D : 0;            // two blocks of codes on their way
     static constexpr int Q_BYTES = kTileRows * D * 2;
-    static constexpr int SMEM = 1024 + 2 * Q_BYTES + STAGES * BLOCK_BYTES; // 1024: alignment
+    static constexpr int SMEM = 1024 + 2 * Q_BYTES + STAGES * BLOCK_BYTES + RAW_BYTES;     // 1024: alignment
 };
 
 struct TileBars {                          // shared memory
@@ -279,6 +282,7 @@ k_attend_tile(AttnArgs a, AttnPlan pl, const __grid_constant__ CUtensorMap k_map
             // the row's maximum is still being found (other units do that), and
             // again in the rare case that the maximum has outgrown the scale.
             uint32_t p[32];
+            const uint32_t o_free = S::AHEAD ? bar_test(shared_addr(&bars.o_full[t]), phase ^ 1) : 0;
             uint64_t part = weights(0, p);
             float mx[4];
 #pragma unroll
@@ -293,7 +297,7 @@ k_attend_tile(AttnArgs a, AttnPlan pl, const __grid_constant__ CUtensorMap k_map
             // O and P are free once the last block's O += P V is done (where S and
             // P share their place, S says so)
             if (S::AHEAD && j > tr.b0) {
-                ok = bar_wait(shared_addr(&bars.o_full[t]), phase ^ 1);
+                if (!o_free) ok = bar_wait(shared_addr(&bars.o_full[t]), phase ^ 1);
                 if (!__all_sync(0xffffffffu, ok)) {
                     ok = false;
                     break;
@@ -465,6 +469,14 @@ k_attend_tile(AttnArgs a, AttnPlan pl, const __grid_constant__ CUtensorMap k_map
         auto wait = [&](uint32_t bar, uint32_t parity) {
             if (ok) ok = bar_wait(bar, parity);
         };
+        // The next two places of the ring (a block's V, the next one's K): asked
+        // for before the waits that they are needed after.
+        uint32_t here = 0, after = 0;
+        auto ask_ring = [&]() {
+            const uint32_t at1 = at + 1 == S::STAGES ? 0 : at + 1, lap1 = at + 1 == S::STAGES ? lap ^ 1 : lap;
+            here = bar_test(shared_addr(&bars.full[at]), lap);
+            after = bar_test(shared_addr(&bars.full[at1]), lap1);
+        };
         // Every block's K and V are let go by both warps, used or not.
         if (j1 > j0) {
             if (tr.b1 > 0) wait(shared_addr(&bars.q_full[t]), 0);
@@ -516,11 +528,11 @@ k_attend_tile(AttnArgs a, AttnPlan pl, const __grid_constant__ CUtensorMap k_map
         if constexpr (S::AHEAD) {
             uint32_t read_phase = 0;
             for (int32_t j = j0; j < j1; ++j) {
-                const uint32_t v_at = at, v_lap = lap, v_smem = ring + at * S::BLOCK_BYTES;
+                const uint32_t v_at = at, v_lap = lap, v_smem = ring + at * S::BLOCK_BYTES, v_here = here;
                 const bool now = in(j), then = j + 1 < j1;
                 next();
                 if (then) {                                                // the next block's S first
-                    wait(shared_addr(&bars.full[at]), lap);
+                    if (!after) wait(shared_addr(&bars.full[at]), lap);
                     if (now) {
                         wait(shared_addr(&bars.s_read[t]), read_phase);
                         read_phase ^= 1;
@@ -533,7 +545,7 @@ k_attend_tile(AttnArgs a, AttnPlan pl, const __grid_constant__ CUtensorMap k_map
                     __syncwarp();
                     next();
                 }
-                wait(shared_addr(&bars.full[v_at]), v_lap);
+                if (!v_here) wait(shared_addr(&bars.full[v_at]), v_lap);
                 clear_tail(j, v_smem);
                 if (now) {
                     wait(p_bar, p_phase);
@@ -542,6 +554,7 @@ k_attend_tile(AttnArgs a, AttnPlan pl, const __grid_constant__ CUtensorMap k_map
                     half_product(1, v_smem, j == tr.b0);
                     p_phase ^= 1;
                 }
+                ask_ring();
                 if (ok && elect_one()) {
                     if (now) mma_commit(shared_addr(&bars.o_full[t]));
                     mma_commit(shared_addr(&bars.empty[v_at]));
@@ -558,12 +571,12 @@ k_attend_tile(AttnArgs a, AttnPlan pl, const __grid_constant__ CUtensorMap k_map
             const uint32_t my_turn = shared_addr(&bars.turn[t]);
             uint32_t turn_phase = 0;
             for (int32_t j = j0; j < j1; ++j) {
-                wait(shared_addr(&bars.full[at]), lap);
+                if (!here) wait(shared_addr(&bars.full[at]), lap);
                 const uint32_t v_at = at, v_smem = ring + at * S::BLOCK_BYTES;
                 next();
                 clear_tail(j, v_smem);
                 const bool then = j + 1 < j1, now = in(j);
-                if (then) wait(shared_addr(&bars.full[at]), lap);
+                if (then && !after) wait(shared_addr(&bars.full[at]), lap);
                 if (now) wait(p_bar, p_phase);
                 if (j > j0 || t == 1) {
                     wait(my_turn, turn_phase);
@@ -587,6 +600,7 @@ k_attend_tile(AttnArgs a, AttnPlan pl, const __grid_constant__ CUtensorMap k_map
                 }
                 __syncwarp();
                 if (then) next();
+                ask_ring();
             }
         }
         // All products done before the CTA ends.
@@ -656,24 +670,41 @@ k_attend_tile(AttnArgs a, AttnPlan pl, const __grid_constant__ CUtensorMap k_map
         constexpr int N = kBlock / RPI;
         const int tid = threadIdx.x - S::FIRST_LOADER * 32, c = tid % CPR, row_i = tid / CPR;
         uint32_t at = 0, lap = 0;
+        // Codes arrive by asynchronous copies two blocks ahead, each thread's own
+        // pieces at its own place, so that it needs no other to widen them.
+        const uint32_t raw = ring + S::STAGES * S::BLOCK_BYTES + tid * 16;
         uint4 w[N];
-        auto load = [&](int32_t j, int kv) {
-            const uint8_t *cache = static_cast<const uint8_t *>(kv ? a.v_cache : a.k_cache);
-            int32_t p[N];
+        int32_t pages[N], ahead[N];                                        // of the rows that this thread loads
+        auto look_up = [&](int32_t j, int32_t *p) {
 #pragma unroll
             for (int i = 0; i < N; ++i) {
                 const int32_t k = j * kBlock + i * RPI + row_i;
                 p[i] = j < j1 && k < r.kv_len ? table[k >> a.pg.page_shift] : -1;
             }
+        };
+        auto fetch = [&](int32_t j, int kv) {
+            const uint8_t *cache = static_cast<const uint8_t *>(kv ? a.v_cache : a.k_cache);
 #pragma unroll
             for (int i = 0; i < N; ++i) {
                 const int32_t k = j * kBlock + i * RPI + row_i;
-                w[i] = make_uint4(0, 0, 0, 0);
-                if (p[i] >= 0 && p[i] < a.pg.n_pages)
-                    w[i] = *reinterpret_cast<const uint4 *>(cache + p[i] * a.pg.page_stride +
-                                                            (k & (a.pg.page_size - 1)) * a.pg.slot_stride +
-                                                            hk * a.pg.head_stride + c * 16);
+                const bool on = pages[i] >= 0 && pages[i] < a.pg.n_pages;                  // else zeros
+                const int64_t at_i = on ? pages[i] * a.pg.page_stride + (k & (a.pg.page_size - 1)) * a.pg.slot_stride +
+                                              hk * a.pg.head_stride + c * 16
+                                        : 0;
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(raw + kv * (kBlock * D) + i * (S::LOADERS * 512)),
+                             "l"(cache + at_i), "r"(on ? 16 : 0)
+                             : "memory");
             }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+        auto take = [&](int kv) {                                          // the older of the two blocks on their way
+            asm volatile("cp.async.wait_group 1;" ::: "memory");
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                             : "=r"(w[i].x), "=r"(w[i].y), "=r"(w[i].z), "=r"(w[i].w)
+                             : "r"(raw + kv * (kBlock * D) + i * (S::LOADERS * 512))
+                             : "memory");
         };
         auto store = [&](int kv) {
             const uint32_t dst = ring + at * S::BLOCK_BYTES + (c >> 2) * (kBlock * 128);
@@ -695,17 +726,24 @@ k_attend_tile(AttnArgs a, AttnPlan pl, const __grid_constant__ CUtensorMap k_map
                                  : "memory");
             }
         };
-        if (j1 > j0) load(j0, 0);
+        if (j1 > j0) {
+            look_up(j0, pages);
+            fetch(j0, 0);
+            fetch(j0, 1);
+            look_up(j0 + 1, pages);
+            look_up(j0 + 2, ahead);                                        // a block ahead, off the path of its loads
+        }
         for (int32_t j = j0; j < j1 && ok; ++j) {
 #pragma unroll
             for (int kv = 0; kv < 2; ++kv) {
+                take(kv);
                 ok = bar_wait(shared_addr(&bars.empty[at]), lap ^ 1);
                 if (!__all_sync(0xffffffffu, ok)) {
                     ok = false;
                     break;
                 }
                 store(kv);
-                load(kv ? j + 1 : j, kv ^ 1);
+                fetch(j + 1, kv);                                          // in place of the codes just used; none past the last block
                 fence_shared_async();
                 bar_arrive(shared_addr(&bars.full[at]));
                 if (++at == S::STAGES) {
@@ -713,7 +751,11 @@ k_attend_tile(AttnArgs a, AttnPlan pl, const __grid_constant__ CUtensorMap k_map
                     lap ^= 1;
                 }
             }
+#pragma unroll
+            for (int i = 0; i < N; ++i) pages[i] = ahead[i];
+            look_up(j + 3, ahead);
         }
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
     }
     if (!ok && lane == 0) bars.failed = 1;
     tmem_fence_before();

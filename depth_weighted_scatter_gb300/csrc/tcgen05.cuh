@@ -49,6 +49,20 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity) {
     return false;
 }
 
+// Whether the phase of this parity has come, without waiting: asked for some
+// time before the answer is needed, it takes the wait's latency off the path.
+__device__ __forceinline__ uint32_t bar_test(uint32_t bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return done;
+}
+
 // Generic writes to shared memory before reads by TMA or the tensor core.
 __device__ __forceinline__ void fence_shared_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
