@@ -14,24 +14,28 @@
 //                    store them in the same layout
 // While one tile is in its softmax the tensor core works on the other.
 //
-// Bound by the tensor core at head_dim 128 (two products of 128 x 128 x 128 a
-// tile and block, 512 cycles each, against 512 cycles of exponentials), by
-// tensor core and exponentials alike at 64.
-//
 // O is only rescaled when a row's maximum has grown by more than 2^8 since the
 // scale in use was set: P then stays below 2^8 and FP32 sums lose nothing.
-// The completion of S(j+1) also says that O += P V of block j is done, as they
-// are issued in that order: the softmax may then touch O.
+// At head_dim 128 P takes S's place in tensor memory, and the completion of
+// S(j+1) also says that O += P V of block j is done, as they are issued in that
+// order.  At 64 there is room for both, S(j+1) is made during block j's softmax,
+// and O and P have a barrier of their own.
 //
-// Measured on a GB300, 32 query and 8 key heads of 128, bf16: a prompt of 8192
-// tokens 404 us (1360 TFLOP/s of 1900 measured in short products, 1730 sustained:
-// the clock falls to about 1.5 GHz under this load); six ragged chunks of up to 500
-// tokens over up to 12000 keys 307 us (1120 TFLOP/s); 2500 tokens of 8 heads of 64
-// over 12500 keys in E4M3, two requests: 162 us (530 TFLOP/s).  A pair of blocks
-// takes about 2650 cycles against the products' 2048 at head_dim 128, and 2400
-// against 1024 at 64 (the softmax warps' dependent instructions).  Two threads a
-// row gave no gain (they share the exponentials' unit: 455 us for the prompt), nor
-// did walking several places of the grid in one CTA (423 against 417).
+// What bounds it.  At head_dim 128 the products: a block pair (both tiles) is
+// 2048 cycles of tensor core, but S takes both operands from shared memory, 8 KB
+// for each 64 cycles, all that it gives beside the copies, so about 2500; 2850 to
+// 2950 are measured, as the waits between the steps of a tile are not all covered
+// by the other's.  At 64 the softmax warps: 2300 cycles of dependent instructions
+// against 1024 of products and as many of exponentials.  A CTA's start and end
+// take some 12 us beside that (its queries, the first keys, the masked block, O).
+//
+// Measured on a GB300 (2.0 GHz), 32 query and 8 key heads of 128, bf16: a prompt of
+// 8192 tokens 397 us (1380 TFLOP/s of 1900 measured; whole blocks make 1.6 %
+// more products than are counted); six ragged chunks of up to 500 tokens over up to
+// 12000 keys 260 us (1320 TFLOP/s); 2500 tokens of 8 heads of 64 over 12500 keys in
+// E4M3, two requests: 158 us (546 TFLOP/s).  Two threads a row gave no gain (they
+// share the exponentials' unit: 471 us for the prompt against 473 at the time), nor
+// did going on with other places of the grid in one CTA (423 against 417).
 //
 // A wait that runs out (it never should) ends the CTA: its rows become NaN and
 // bevpool_attention_timeouts counts it.
