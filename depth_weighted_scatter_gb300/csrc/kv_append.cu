@@ -54,7 +54,7 @@ k_kv_append(AppendArgs g, int split) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, rg = lane / LPR;
     weights.load(f.q_weight, f.k_weight, f.D);
     if (threadIdx.x == 0) {
-        parts[0].set(0, f.q);
+        parts[0].set(0, f.q.p ? f.q : f.k);                // without queries: no steps, but an address
         parts[1].set(0, f.k);
         parts[2].set(0, g.v);
         parts[0].H = f.Hq, parts[0].end = steps_of<LPR>(f.Hq);

@@ -587,3 +587,41 @@ def test_attention_many_tiles(A, case):
                                                        + ref.tiny(dtype)).cpu(), f"out {b} {i} {h}")
                 within(lse[cu[b] + i, rows], want.cpu(), (d + 2.0 ** -18 + 2.0 ** -22 * want.abs()).cpu(), "lse")
     assert A.bevpool_attention_timeouts() == 0
+
+
+@pytest.mark.parametrize("page, D, dtype, cache, token_major", [(256, 128, BF16, "same", True), (256, 64, F16, "same", False),
+                                                                (16, 64, BF16, "same", True), (32, 128, F16, "same", True),
+                                                                (256, 128, F16, "e4m3", True)])
+def test_attention_page_sizes_and_layouts(A, page, D, dtype, cache, token_major):
+    """Many query rows over pages above and below a block, in either memory order, with holes among them."""
+    case = ([70, 33], [700, 290], 6, 2, D, True, 0, dtype, cache, page, token_major)
+    x = attend_inputs(case, seed=700)
+    poison(x)
+    check_attend(A, x)
+    x["block_table"][0, 1] = -1
+    check_attend(A, x)
+
+
+@pytest.mark.parametrize("q_len", [1, 40])
+@pytest.mark.parametrize("cache", ["same", "e4m3"])
+@pytest.mark.parametrize("power", [60, -60])
+def test_attention_query_magnitudes(A, q_len, cache, power):
+    """bf16 queries far from 1 give the same attention when the scale takes their magnitude back."""
+    case = ([q_len] * 2, [90, 200], 4, 1, 128, True, 0, BF16, cache, 16, False)
+    x = attend_inputs(case, seed=800)
+    x["q"] = x["q"] * 2.0 ** power
+    x["scale"] = 128 ** -0.5 * 2.0 ** -power
+    check_attend(A, x)
+
+
+def test_append_and_attention_of_one_request_among_empty_ones(A):
+    """Requests without tokens between others: their neighbours' rows are their own."""
+    q_len, kv_len = [0, 3, 0, 0, 40, 0], [7, 50, 0, 9, 40, 1]
+    case = (q_len, kv_len, 4, 2, 64, True, 0, F16, "same", 16, False)
+    x = attend_inputs(case, seed=900)
+    k, v = rand(901, 43, 2, 64, dtype=F16), rand(902, 43, 2, 64, dtype=F16)
+    A.kv_append(k, v, x["k_cache"], x["v_cache"], x["block_table"], x["kv_len"], x["cu_q"], positions_of(903, 43, 1), freqs(64))
+    tb = x["block_table"].cpu()
+    for t, (b, place) in {0: (1, 47), 2: (1, 49), 3: (4, 0), 42: (4, 39)}.items():
+        assert torch.equal(x["v_cache"][tb[b, place // 16], :, place % 16], v[t])
+    check_attend(A, x)
