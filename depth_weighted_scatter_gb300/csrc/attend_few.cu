@@ -101,7 +101,7 @@ k_attend_few(AttnArgs a, AttnPlan pl) {
     const Request r = request_of(a, b);
     if (r.q_rows == 0) return;
     int32_t base;
-    const int n_used = chunks_of(a, r, pl.chunk, pl.n_chunks, pl.align, &base);
+    const int n_used = chunks_of(a, r, pl.chunk, pl.n_chunks, &base);
     if (static_cast<int>(blockIdx.x) >= n_used) return;
     const int rows = r.q_rows * a.G;
 
@@ -370,7 +370,7 @@ k_attend_few(AttnArgs a, AttnPlan pl) {
         // row is then taken again element by element.
         if (r.q_rows > 1 && !__all_sync(0xffffffffu, fine))
             redo_row<T, E4M3, D>(a, r, b, hk, i, h, c0, c1, &mt, &lt, acc);
-        store_row<T, E>(a, pl, r, b, hk, i, h, row, static_cast<int>(blockIdx.x), n_used, mt, lt, acc);
+        store_row<T, E>(a, r, i, h, n_used > 1 ? part_row(a, pl, b, hk, static_cast<int>(blockIdx.x), row) : -1, mt, lt, acc);
     }
     grid_dep_allow();
 }

@@ -9,58 +9,93 @@ namespace bevpool {
 
 namespace {
 
-// W warps a query row: they take the chunks in turn, and the first joins their
-// sums.
-template <typename T, int D, int W>
+// W warps a query row: they take the parts in turn, and the first joins their
+// sums.  SHARED: rows are those of a tile pair that several CTAs shared.
+template <typename T, int D, int W, bool SHARED>
 __global__ void __launch_bounds__(kThreads)
 k_attend_join(AttnArgs a, AttnPlan pl) {
-    constexpr int E = D / 32, ROWS = kWarps / W;           // rows of a CTA
+    constexpr int E = D / 32, R = W == 1 ? 4 : 1;          // rows of a warp at a time, their loads in flight together
+    constexpr int ROWS = kWarps / W * R;                   // of a CTA
     __shared__ float sums[W > 1 ? kWarps : 1][D + 1];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = warp % W, hk = blockIdx.y, b = blockIdx.z;
-    const Request r = request_of(a, b);
-    int32_t base;
-    const int n = chunks_of(a, r, pl.chunk, pl.n_chunks, pl.align, &base);
-    const int rows = r.q_rows * a.G;
-    if (n == 1 || static_cast<int>(blockIdx.x) * ROWS >= rows) return;
-    grid_dep_wait();
-    for (int row0 = blockIdx.x * ROWS; row0 < rows; row0 += gridDim.x * ROWS) {
-        const int row = row0 + warp / W;
-        float m = -INFINITY, l = 0.0f, acc[E] = {};
-        if (row < rows) {
-            const int64_t at = part_row(a, pl, b, hk, 0, row);
-            for (int c = lane; c < n; c += 32) m = fmaxf(m, a.part_ml[(at + static_cast<int64_t>(c) * pl.rows) * 2]);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = warp % W;
+    int hk = blockIdx.y, b = blockIdx.z, n, row_end, first_row = 0;
+    // Part i of row x is at base + x + i * step, the first `extra` further on.
+    int64_t base, step, extra = 0;
+    Request r;
+    if constexpr (SHARED) {
+        grid_dep_wait();
+        const int2 cut = a.cut[blockIdx.y];
+        if (cut.x < 0) return;
+        const int tile = cut.x % pl.tiles;
+        hk = cut.x / pl.tiles % a.Hk;
+        b = cut.x / pl.tiles / a.Hk;
+        r = request_of(a, b);
+        n = cut.y - blockIdx.y + 1;
+        first_row = tile * kPairRows;
+        row_end = min(r.q_rows * a.G, first_row + kPairRows);
+        base = static_cast<int64_t>(blockIdx.y) * (2 * kPairRows) - first_row;
+        step = 2 * kPairRows;
+        extra = kPairRows;
+    } else {
+        r = request_of(a, b);
+        int32_t key0;
+        n = chunks_of(a, r, pl.chunk, pl.n_chunks, &key0);
+        row_end = r.q_rows * a.G;
+        if (n == 1 || static_cast<int>(blockIdx.x) * ROWS >= row_end) return;
+        grid_dep_wait();
+        base = part_row(a, pl, b, hk, 0, 0);
+        step = pl.rows;
+    }
+    for (int row0 = first_row + blockIdx.x * ROWS; row0 < row_end; row0 += gridDim.x * ROWS) {
+        const int row = row0 + warp / W * R;
+        float m[R], l[R] = {}, acc[R][E] = {};
+        const auto at = [&](int x, int i) {                // a row past the last reads the last one's
+            return base + min(row + x, row_end - 1) + i * step + (i == 0 ? extra : 0);
+        };
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-            const float from = m == -INFINITY ? 0.0f : m;
-#pragma unroll 4
-            for (int c = part; c < n; c += W) {
-                const int64_t p = at + static_cast<int64_t>(c) * pl.rows;
+        for (int x = 0; x < R; ++x) m[x] = lane < n ? a.part_ml[at(x, lane) * 2] : -INFINITY;
+        for (int i = lane + 32; i < n; i += 32)
+#pragma unroll
+            for (int x = 0; x < R; ++x) m[x] = fmaxf(m[x], a.part_ml[at(x, i) * 2]);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+            for (int x = 0; x < R; ++x) m[x] = fmaxf(m[x], __shfl_xor_sync(0xffffffffu, m[x], o));
+#pragma unroll(R == 1 ? 4 : 2)
+        for (int i = part; i < n; i += W) {
+#pragma unroll
+            for (int x = 0; x < R; ++x) {
+                const int64_t p = at(x, i);
                 const float2 ml = *reinterpret_cast<const float2 *>(a.part_ml + p * 2);
-                if (ml.y != 0.0f) {                        // else nothing was seen there, and no O written
-                    const float *o = a.part_o + p * D + lane * E;
-                    const float f = pow2(ml.x - from);
-                    l = fmaf(ml.y, f, l);
+                struct alignas(E * 4) Elements {
+                    float x[E];
+                };
+                const Elements o = *reinterpret_cast<const Elements *>(a.part_o + p * D + lane * E);
+                // no sum: nothing was seen there, and no O written
+                const float f = pow2(ml.x - (m[x] == -INFINITY ? 0.0f : m[x]));
+                if (ml.y != 0.0f) l[x] = fmaf(ml.y, f, l[x]);
 #pragma unroll
-                    for (int e = 0; e < E; ++e) acc[e] = fmaf(o[e], f, acc[e]);
-                }
+                for (int e = 0; e < E; ++e) acc[x][e] = ml.y != 0.0f ? fmaf(o.x[e], f, acc[x][e]) : acc[x][e];
             }
         }
         if constexpr (W > 1) {
 #pragma unroll
-            for (int e = 0; e < E; ++e) sums[warp][lane * E + e] = acc[e];
-            if (lane == 0) sums[warp][D] = l;
+            for (int e = 0; e < E; ++e) sums[warp][lane * E + e] = acc[0][e];
+            if (lane == 0) sums[warp][D] = l[0];
             __syncthreads();
             if (part == 0) {
 #pragma unroll
                 for (int w = 1; w < W; ++w) {
-                    l += sums[warp + w][D];
+                    l[0] += sums[warp + w][D];
 #pragma unroll
-                    for (int e = 0; e < E; ++e) acc[e] += sums[warp + w][lane * E + e];
+                    for (int e = 0; e < E; ++e) acc[0][e] += sums[warp + w][lane * E + e];
                 }
             }
         }
-        if (row < rows && part == 0)
-            store_row<T, E>(a, pl, r, b, hk, row / a.G, hk * a.G + row % a.G, row, 0, 1, m, l, acc);
+#pragma unroll
+        for (int x = 0; x < R; ++x)
+            if (row + x < row_end && part == 0)
+                store_row<T, E>(a, r, (row + x) / a.G, hk * a.G + (row + x) % a.G, -1, m[x], l[x], acc[x]);
         if constexpr (W > 1) __syncthreads();
     }
 }
@@ -68,23 +103,29 @@ k_attend_join(AttnArgs a, AttnPlan pl) {
 }  // namespace
 
 cudaError_t launch_attend_join(const AttnArgs &a, const AttnPlan &pl) {
-    auto run = [&](auto t, auto d, auto w) {
-        int64_t gx = div_up(pl.rows, kWarps / decltype(w)::value);
-        if (gx > 1024) gx = 1024;
-        const cudaError_t e =
-            launch_dependent(k_attend_join<decltype(t), decltype(d)::value, decltype(w)::value>,
-                             dim3(static_cast<unsigned>(gx), static_cast<unsigned>(a.Hk), static_cast<unsigned>(a.pg.n_seqs)),
-                             dim3(kThreads), 0, a.stream, a, pl);
+    auto launch = [&](auto kernel, dim3 grid) {
+        const cudaError_t e = launch_dependent(kernel, grid, dim3(kThreads), 0, a.stream, a, pl);
         if (e == cudaSuccess) count_launch();
         return e;
+    };
+    auto run = [&](auto t, auto d, auto w) {
+        constexpr int D = decltype(d)::value, W = decltype(w)::value, ROWS = kWarps / W * (W == 1 ? 4 : 1);
+        if (!pl.few)
+            return launch(k_attend_join<decltype(t), D, W, true>,
+                          dim3(kPairRows / ROWS, static_cast<unsigned>(pl.share)));
+        int64_t gx = div_up(pl.rows, ROWS);
+        if (gx > 1024) gx = 1024;
+        return launch(k_attend_join<decltype(t), D, W, false>,
+                      dim3(static_cast<unsigned>(gx), static_cast<unsigned>(a.Hk), static_cast<unsigned>(a.pg.n_seqs)));
     };
     // A warp a row where a row has few chunks (a CTA then takes eight rows), all
     // of a CTA's where it has many.  The whole call, with 76 chunks of 64 rows:
     // 137 us with a warp a row, 103 with eight; with 3 chunks of 40000 rows: 185
-    // and 232.
+    // and 232.  Shared tiles have as many parts as CTAs share one, and one more.
+    const int64_t n = pl.few ? pl.n_chunks : pl.share / (static_cast<int64_t>(pl.tiles) * a.Hk * a.pg.n_seqs) + 2;
     auto by_w = [&](auto t, auto d) {
-        if (pl.n_chunks <= 4) return run(t, d, std::integral_constant<int, 1>{});
-        if (pl.n_chunks <= 16) return run(t, d, std::integral_constant<int, 4>{});
+        if (n <= 4) return run(t, d, std::integral_constant<int, 1>{});
+        if (n <= 16) return run(t, d, std::integral_constant<int, 4>{});
         return run(t, d, std::integral_constant<int, 8>{});
     };
     auto by_d = [&](auto t) {

@@ -14,6 +14,11 @@
 //                    store them in the same layout
 // While one tile is in its softmax the tensor core works on the other.
 //
+// Where there are few pairs of row tiles they are shared out (AttnPlan::share): each
+// CTA works its part of all pairs' blocks, pieces of pairs at its ends leave their
+// sums, maxima and O to a second kernel.  A piece starts with every barrier set up
+// anew; warp 11 looks the next one up meanwhile.
+//
 // O is only rescaled when a row's maximum has grown by more than 2^8 since the
 // scale in use was set: P then stays below 2^8 and FP32 sums lose nothing.
 // At head_dim 128 P takes S's place in tensor memory, and the completion of
@@ -33,7 +38,8 @@
 // 8192 tokens 397 us (1380 TFLOP/s of 1900 measured; whole blocks make 1.6 %
 // more products than are counted); six ragged chunks of up to 500 tokens over up to
 // 12000 keys 260 us (1320 TFLOP/s); 2500 tokens of 8 heads of 64 over 12500 keys in
-// E4M3, two requests: 158 us (546 TFLOP/s).  Two threads a row gave no gain (they
+// E4M3, two requests: 131 us (654 TFLOP/s; chunks of equal length instead of shares:
+// 158).  A piece takes 10 us (5.5 at 64) beside its blocks.  Two threads a row gave no gain (they
 // share the exponentials' unit: 471 us for the prompt against 473 at the time), nor
 // did going on with other places of the grid in one CTA (423 against 417).
 //
@@ -61,7 +67,6 @@ struct TileShape {
     // one of loaders.  Registers a thread, by setmaxnreg; their sum is within
     // what the launch gives (168 a thread of 384, 128 of 512).
     static constexpr int LOADERS = E4M3 ? 4 : 1;                           // warps
-    static constexpr int FIRST_LOADER = E4M3 ? 12 : 10;
     static constexpr int THREADS = E4M3 ? 512 : 384;
     static constexpr int LAUNCH_REGS = E4M3 ? 128 : 168;
     static constexpr int SOFTMAX_REGS = E4M3 ? 184 : 208;
@@ -84,87 +89,190 @@ struct TileShape {
     static constexpr int SMEM = 1024 + 2 * Q_BYTES + STAGES * BLOCK_BYTES + RAW_BYTES;     // 1024: alignment
 };
 
+// What a CTA does at a time: a pair of row tiles over the blocks [p0, p1).
+struct TilePiece {
+    int32_t b, hk, row0;                   // b < 0: none
+    int32_t p0, p1;
+    int32_t part;                          // first row of its partial results; below 0: it has all of the pair's blocks
+};
+
+// Shared tiles.  All pairs in order lie on one axis, each kStart units (what its
+// start and end take, in blocks) and then its blocks; a CTA's share is [from, to).
+struct TileWalk {
+    int64_t from, to, total, at;           // at: where the next pair starts
+    int32_t place, ctas;                   // the next pair; CTAs with a share
+};
+constexpr int32_t kStart = 4, kLeast = 6;  // kLeast: units of a share, at least
+
 struct TileBars {                          // shared memory
     uint64_t full[8], empty[8];            // ring
     uint64_t q_full[2], s_full[2], p_full[2][2], s_read[2], o_full[2], turn[2], drain[2];
     uint32_t tmem, failed;
+    TilePiece piece[2];                    // the one at work and the next
+    TileWalk walk;
+    int64_t scan[16];
 };
 
-// What a row tile of this CTA sees: blocks [b0, b1) of the chunk.
+// What a row tile sees of the blocks [p0, p1): [b0, b1).
 struct TileRange {
     int32_t b0, b1;
 };
 
-__device__ __forceinline__ TileRange tile_range(const AttnArgs &a, const Request &r, int32_t row0, int32_t rows, int32_t c0,
-                                                int64_t c1) {
+__device__ __forceinline__ TileRange tile_range(const AttnArgs &a, const Request &r, int32_t row0, int32_t rows, int32_t p0,
+                                                int32_t p1) {
     if (row0 >= rows) return {0, 0};
     int32_t lo, hi, x;
     seen_keys(a, r, row0 / a.G, &lo, &x);
     seen_keys(a, r, (min(row0 + kTileRows, rows) - 1) / a.G, &x, &hi);
-    lo = max(lo, c0);
-    hi = static_cast<int32_t>(min(static_cast<int64_t>(hi), c1));
     if (hi <= lo) return {0, 0};
-    return {lo / kBlock, (hi - 1) / kBlock + 1};
+    const int32_t b0 = max(lo / kBlock, p0), b1 = min((hi - 1) / kBlock + 1, p1);
+    return b1 > b0 ? TileRange{b0, b1} : TileRange{0, 0};
 }
 
-template <typename T, bool E4M3, int D>
-__global__ void __launch_bounds__(TileShape<E4M3, D>::THREADS, 1)
-k_attend_tile(AttnArgs a, AttnPlan pl, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
-    using S = TileShape<E4M3, D>;
-    extern __shared__ uint8_t raw_smem[];
-    __shared__ TileBars bars;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+// What either tile of a pair sees.
+__device__ __forceinline__ TileRange pair_range(TileRange t0, TileRange t1) {
+    return {t0.b1 == 0 ? t1.b0 : t1.b1 == 0 ? t0.b0 : min(t0.b0, t1.b0), max(t0.b1, t1.b1)};
+}
 
-    // x: row tiles (the longest first) by key heads; y: chunks; z: requests.
-    const int hk = blockIdx.x % a.Hk, b = blockIdx.z, chunk = blockIdx.y;
-    const Request r = request_of(a, b);
+// The pair at a place on the axis; its blocks, or {0, -kStart} where it has no rows.
+__device__ __forceinline__ TileRange pair_at(const AttnArgs &a, const AttnPlan &pl, int32_t place, TilePiece *pc) {
+    pc->row0 = place % pl.tiles * kPairRows;
+    pc->hk = place / pl.tiles % a.Hk;
+    pc->b = place / pl.tiles / a.Hk;
+    const Request r = request_of(a, pc->b);
     const int32_t rows = r.q_rows * a.G;
-    const int32_t row0 = static_cast<int32_t>(gridDim.x / a.Hk - 1 - blockIdx.x / a.Hk) * (2 * kTileRows);
-    if (row0 >= rows) return;
-    int32_t base;
-    const int n_used = chunks_of(a, r, pl.chunk, pl.n_chunks, pl.align, &base);
-    if (chunk >= n_used) return;
-    const int32_t c0 = base + chunk * pl.chunk;
-    const int64_t c1 = static_cast<int64_t>(c0) + pl.chunk;
-    const TileRange t0 = tile_range(a, r, row0, rows, c0, c1), t1 = tile_range(a, r, row0 + kTileRows, rows, c0, c1);
-    const int32_t j0 = t0.b1 == 0 ? t1.b0 : t1.b1 == 0 ? t0.b0 : min(t0.b0, t1.b0);
-    const int32_t j1 = max(t0.b1, t1.b1);
-    const int32_t *table = a.pg.block_table + static_cast<int64_t>(b) * a.pg.table_pages;
+    if (pc->row0 >= rows) return {0, -kStart};
+    return pair_range(tile_range(a, r, pc->row0, rows, 0, INT32_MAX), tile_range(a, r, pc->row0 + kTileRows, rows, 0, INT32_MAX));
+}
 
-    const uint32_t smem = (shared_addr(raw_smem) + 1023) & ~1023u;
-    const uint32_t q_smem = smem, ring = smem + 2 * S::Q_BYTES;
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < S::STAGES; ++i) {
-            bar_init(shared_addr(&bars.full[i]), E4M3 ? S::LOADERS * 32 : 1);
-            bar_init(shared_addr(&bars.empty[i]), 2);
+// This CTA's share, by all of its threads (two places each).
+template <int THREADS>
+__device__ __forceinline__ void find_share(const AttnArgs &a, const AttnPlan &pl, TileBars &bars) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int32_t places = pl.tiles * a.Hk * a.pg.n_seqs;
+    int64_t w[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int32_t place = 2 * threadIdx.x + i;
+        w[i] = 0;
+        if (place < places) {
+            TilePiece pc;
+            const TileRange x = pair_at(a, pl, place, &pc);
+            w[i] = kStart + x.b1 - x.b0;
         }
-        for (int t = 0; t < 2; ++t) {
-            bar_init(shared_addr(&bars.q_full[t]), kTileRows);
-            bar_init(shared_addr(&bars.s_full[t]), 1);
-            bar_init(shared_addr(&bars.p_full[t][0]), kTileRows);
-            bar_init(shared_addr(&bars.p_full[t][1]), kTileRows);
-            bar_init(shared_addr(&bars.s_read[t]), kTileRows);
-            bar_init(shared_addr(&bars.o_full[t]), 1);
-            bar_init(shared_addr(&bars.turn[t]), 1);
-            bar_init(shared_addr(&bars.drain[t]), 1);
-        }
-        bars.failed = 0;
-        bar_init_fence();
     }
-    if (warp == 8) tmem_alloc<512>(shared_addr(&bars.tmem));
-    tmem_fence_before();
+    int64_t sum = w[0] + w[1];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t below = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += below;
+    }
+    if (lane == 31) bars.scan[warp] = sum;
     __syncthreads();
-    tmem_fence_after();
+    int64_t at = sum - w[0] - w[1], total = 0;
+#pragma unroll
+    for (int i = 0; i < THREADS / 32; ++i) {
+        if (i < warp) at += bars.scan[i];
+        total += bars.scan[i];
+    }
+    const int64_t most = total / kLeast;
+    const int32_t ctas = static_cast<int32_t>(most < 1 ? 1 : most < gridDim.x ? most : gridDim.x);
+    const int32_t me = min(static_cast<int32_t>(blockIdx.x), ctas);
+    const int64_t from = me * total / ctas, to = min(me + 1, ctas) * total / ctas;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        if (from < to && at <= from && from < at + w[i]) {
+            bars.walk.at = at;
+            bars.walk.place = 2 * threadIdx.x + i;
+        }
+        at += w[i];
+    }
+    if (threadIdx.x == 0) {
+        bars.walk.from = from;
+        bars.walk.to = to;
+        bars.walk.total = total;
+        bars.walk.ctas = ctas;
+        if (from >= to) bars.walk.at = to;                                 // no share
+        a.cut[blockIdx.x] = make_int2(-1, 0);
+    }
+}
+
+// The next piece of this CTA's share, by one thread.
+__device__ __forceinline__ TilePiece next_piece(const AttnArgs &a, const AttnPlan &pl, TileWalk &walk) {
+    TilePiece pc = {-1, 0, 0, 0, 0, -1};
+    while (walk.at < walk.to) {
+        const int32_t place = walk.place;
+        const TileRange x = pair_at(a, pl, place, &pc);
+        const int64_t at = walk.at, first = at + kStart;                   // of its first block
+        const int32_t n = x.b1 - x.b0;
+        // a request's later pairs have no rows either
+        walk.place = n >= 0 ? place + 1 : place - place % pl.tiles + (pc.row0 == 0 ? pl.tiles * (a.Hk - pc.hk) : pl.tiles);
+        if (n < 0) continue;
+        walk.at = first + n;
+        const int32_t from = static_cast<int32_t>(min(max(walk.from - first, static_cast<int64_t>(0)), static_cast<int64_t>(n)));
+        const int32_t to = static_cast<int32_t>(min(max(walk.to - first, static_cast<int64_t>(0)), static_cast<int64_t>(n)));
+        if (n == 0 ? at < walk.from : from >= to) continue;
+        pc.p0 = x.b0 + from;
+        pc.p1 = x.b0 + to;
+        if (from > 0 || to < n) {
+            pc.part = static_cast<int32_t>(blockIdx.x) * (2 * kPairRows);
+            if (from == 0) {                                               // others end it
+                pc.part += kPairRows;
+                const int64_t last = ((first + n) * walk.ctas - 1) / walk.total;           // whose share its last block is in
+                a.cut[blockIdx.x] = make_int2(place, static_cast<int32_t>(last));
+            }
+        }
+        return pc;
+    }
+    pc.b = -1;
+    return pc;
+}
+
+// Every barrier, set up; `again`: once more, with nothing left that arrives.
+template <int STAGES, int FULL>
+__device__ __forceinline__ void init_bars(TileBars &bars, bool again) {
+    const auto init = [&](uint64_t *bar, uint32_t n) {
+        if (again) bar_end(shared_addr(bar));
+        bar_init(shared_addr(bar), n);
+    };
+    for (int i = 0; i < STAGES; ++i) {
+        init(&bars.full[i], FULL);
+        init(&bars.empty[i], 2);
+    }
+    for (int t = 0; t < 2; ++t) {
+        init(&bars.q_full[t], kTileRows);
+        init(&bars.s_full[t], 1);
+        init(&bars.p_full[t][0], kTileRows);
+        init(&bars.p_full[t][1], kTileRows);
+        init(&bars.s_read[t], kTileRows);
+        init(&bars.o_full[t], 1);
+        init(&bars.turn[t], 1);
+        init(&bars.drain[t], 1);
+    }
+    bar_init_fence();
+}
+
+enum { kSoftmax, kProducts, kLoads };
+
+// A role's part of one piece; false where a wait ran out.
+template <typename T, bool E4M3, int D, int ROLE>
+__device__ __forceinline__ bool attend_piece(const AttnArgs &a, const AttnPlan &pl, const CUtensorMap &k_map,
+                                             const CUtensorMap &v_map, TileBars &bars, int piece, uint32_t smem) {
+    using S = TileShape<E4M3, D>;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const TilePiece &pc = bars.piece[piece];
+    const int hk = pc.hk, b = pc.b;
+    const Request r = request_of(a, b);
+    const int32_t rows = r.q_rows * a.G, row0 = pc.row0;
+    const TileRange t0 = tile_range(a, r, row0, rows, pc.p0, pc.p1), t1 = tile_range(a, r, row0 + kTileRows, rows, pc.p0, pc.p1);
+    const TileRange both = pair_range(t0, t1);
+    const int32_t j0 = both.b0, j1 = both.b1;
+    const int32_t *table = a.pg.block_table + static_cast<int64_t>(b) * a.pg.table_pages;
+    const uint32_t q_smem = smem, ring = smem + 2 * S::Q_BYTES;
     const uint32_t tmem = bars.tmem;
     bool ok = true;
-    if (warp < 8)
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(S::SOFTMAX_REGS));
-    else if (warp < 12)
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::PRODUCT_REGS));
-    else
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::LOADER_REGS));
 
-    if (warp < 8) {
+    if constexpr (ROLE == kSoftmax) {
         // ------------------------------------------------------------ softmax
         const int t = warp >> 2, tid = threadIdx.x & 127;
         const TileRange tr = t == 0 ? t0 : t1;
@@ -343,12 +451,12 @@ k_attend_tile(AttnArgs a, AttnPlan pl, const __grid_constant__ CUtensorMap k_map
             tmem_fence_after();
             const bool some = !(l == 0.0f);
             const float inv = some ? a.v_scale / l : 0.0f;
-            const int64_t part = n_used > 1 && used ? part_row(a, pl, b, hk, chunk, row) : 0;
+            const int64_t part = pc.part >= 0 ? pc.part + t * kTileRows + tid : -1;
             bool fine = l - l == 0.0f;
             // O leaves through shared memory (over the queries, read by now), so
             // that a warp's stores cover whole rows.
             const uint32_t stage = q_smem + t * S::Q_BYTES + (warp & 3) * 32 * (D * 2);
-            if (n_used == 1) {
+            if (part < 0) {
                 constexpr int CPR = D / 8;                                 // 16-byte pieces of a row
 #pragma unroll
                 for (int c = 0; c < D; c += 32) {
@@ -412,15 +520,14 @@ k_attend_tile(AttnArgs a, AttnPlan pl, const __grid_constant__ CUtensorMap k_map
                                          : "r"(stage + x * 64 + ((y ^ ((x >> 1) & 3)) << 4))
                                          : "memory");
                             if (warp0 + x < rows)
-                                *reinterpret_cast<uint4 *>(a.part_o + part_row(a, pl, b, hk, chunk, warp0 + x) * D + c +
-                                                           half * 16 + y * 4) = w;
+                                *reinterpret_cast<uint4 *>(a.part_o + (part - lane + x) * D + c + half * 16 + y * 4) = w;
                         }
                         __syncwarp();
                     }
                 }
             }
             if (used) {
-                if (n_used > 1)
+                if (part >= 0)
                     *reinterpret_cast<float2 *>(a.part_ml + part * 2) = make_float2(m, l);
                 else if (a.lse)
                     a.lse[token * a.Hq + h] = some ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
@@ -435,12 +542,13 @@ k_attend_tile(AttnArgs a, AttnPlan pl, const __grid_constant__ CUtensorMap k_map
                 again &= again - 1;
                 const int32_t rr = tile0 + (warp & 3) * 32 + x;
                 float acc[D / 32], m1, s1;
-                redo_row<T, E4M3, D>(a, r, b, hk, rr / a.G, hk * a.G + rr % a.G, c0,
-                                     static_cast<int32_t>(min(c1, static_cast<int64_t>(r.kv_len))), &m1, &s1, acc);
-                store_row<T, D / 32>(a, pl, r, b, hk, rr / a.G, hk * a.G + rr % a.G, rr, chunk, n_used, m1, s1, acc);
+                redo_row<T, E4M3, D>(a, r, b, hk, rr / a.G, hk * a.G + rr % a.G, pc.p0 * kBlock,
+                                     static_cast<int32_t>(min(pc.p1 * static_cast<int64_t>(kBlock), static_cast<int64_t>(r.kv_len))),
+                                     &m1, &s1, acc);
+                store_row<T, D / 32>(a, r, rr / a.G, hk * a.G + rr % a.G, part < 0 ? -1 : part - lane + x, m1, s1, acc);
             }
         }
-    } else if (warp < 10) {
+    } else if (ROLE == kProducts && warp < 10) {
         // ------------------------------------------------------------ products
         // A warp a tile: while one waits the other's products run.
         const int t = warp - 8;
@@ -611,8 +719,8 @@ k_attend_tile(AttnArgs a, AttnPlan pl, const __grid_constant__ CUtensorMap k_map
         if (elect_one()) mma_commit(shared_addr(&bars.drain[t]));
         __syncwarp();
         ok = bar_wait(shared_addr(&bars.drain[t]), 0) && ok;
-    } else if (warp < S::FIRST_LOADER || warp >= S::FIRST_LOADER + S::LOADERS) {
-        // warps without work
+    } else if (ROLE == kProducts && (E4M3 || warp == 11)) {
+        if (pl.share && warp == 11 && lane == 0) bars.piece[piece ^ 1] = next_piece(a, pl, bars.walk);
     } else if constexpr (!E4M3) {
         // ------------------------------------------------------------ TMA
         const int per = a.pg.page_size < kBlock ? kBlock / a.pg.page_size : 1;         // pages of a block
@@ -661,18 +769,20 @@ k_attend_tile(AttnArgs a, AttnPlan pl, const __grid_constant__ CUtensorMap k_map
                 }
             }
         }
-        // All copies landed before the CTA ends.
+        // All copies landed, and every place let go of, before the barriers are
+        // set up anew.
         for (int i = 0; i < S::STAGES && i < issued; ++i) {
             if (at == 0) lap ^= 1;
             at = at == 0 ? S::STAGES - 1 : at - 1;
             ok = bar_wait(shared_addr(&bars.full[at]), lap) && ok;
+            ok = ok && bar_wait(shared_addr(&bars.empty[at]), lap);
         }
     } else {
         // ------------------------------------------------------------ E4M3 codes
         constexpr int CPR = D / 16;                                        // 16-byte pieces of a row of codes
         constexpr int RPI = S::LOADERS * 32 / CPR;                         // rows in one step of all loader warps
         constexpr int N = kBlock / RPI;
-        const int tid = threadIdx.x - S::FIRST_LOADER * 32, c = tid % CPR, row_i = tid / CPR;
+        const int tid = threadIdx.x - 12 * 32, c = tid % CPR, row_i = tid / CPR;
         uint32_t at = 0, lap = 0;
         // Codes arrive by asynchronous copies two blocks ahead, each thread's own
         // pieces at its own place, so that it needs no other to widen them.
@@ -760,28 +870,103 @@ k_attend_tile(AttnArgs a, AttnPlan pl, const __grid_constant__ CUtensorMap k_map
             look_up(j + 3, ahead);
         }
         asm volatile("cp.async.wait_group 0;" ::: "memory");
+        for (int i = 0; i < S::STAGES && i < 2 * (j1 - j0) && ok; ++i) {   // every place let go of
+            if (at == 0) lap ^= 1;
+            at = at == 0 ? S::STAGES - 1 : at - 1;
+            ok = bar_wait(shared_addr(&bars.empty[at]), lap);
+        }
     }
-    if (!ok && lane == 0) bars.failed = 1;
+    return ok;
+}
+
+// All threads of the CTA, each role in its own code.
+__device__ __forceinline__ void sync_roles() {
+    tmem_fence_before();
+    asm volatile("bar.sync 0;" ::: "memory");
+    tmem_fence_after();
+}
+
+// A role's part of all of the CTA's pieces; true where a wait ran out.
+template <typename T, bool E4M3, int D, int ROLE>
+__device__ __forceinline__ bool attend_pieces(const AttnArgs &a, const AttnPlan &pl, const CUtensorMap &k_map,
+                                              const CUtensorMap &v_map, TileBars &bars, uint32_t smem) {
+    using S = TileShape<E4M3, D>;
+    bool failed = false;
+    for (int piece = 0; bars.piece[piece].b >= 0; piece ^= 1) {
+        if (!failed) {
+            const bool ok = attend_piece<T, E4M3, D, ROLE>(a, pl, k_map, v_map, bars, piece, smem);
+            if (!ok) bars.failed = 1;
+        } else if (ROLE == kSoftmax && threadIdx.x == 0 && pl.share) {
+            bars.piece[piece ^ 1] = next_piece(a, pl, bars.walk);
+        }
+        sync_roles();
+        failed = bars.failed != 0;
+        if (ROLE == kSoftmax && failed) {                                  // rows of NaN
+            const TilePiece &pc = bars.piece[piece];
+            const Request r = request_of(a, pc.b);
+            const int32_t row = pc.row0 + static_cast<int32_t>(threadIdx.x);
+            if (row < r.q_rows * a.G) {
+                const int64_t token = r.q0 + row / a.G;
+                const int32_t h = pc.hk * a.G + row % a.G;
+                T *op = static_cast<T *>(a.out.p) + token * a.out.token_stride + h * a.out.head_stride;
+                if (pc.part >= 0) {
+                    *reinterpret_cast<float2 *>(a.part_ml + (pc.part + static_cast<int64_t>(threadIdx.x)) * 2) = make_float2(NAN, NAN);
+                } else {
+                    for (int c = 0; c < D; ++c) op[c] = static_cast<T>(NAN);
+                    if (a.lse) a.lse[token * a.Hq + h] = NAN;
+                }
+            }
+        }
+        if (!pl.share) break;
+        if (ROLE == kSoftmax && threadIdx.x == 0 && !failed) init_bars<S::STAGES, E4M3 ? S::LOADERS * 32 : 1>(bars, true);
+        sync_roles();
+    }
+    return failed;
+}
+
+template <typename T, bool E4M3, int D>
+__global__ void __launch_bounds__(TileShape<E4M3, D>::THREADS, 1)
+k_attend_tile(AttnArgs a, AttnPlan pl, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
+    using S = TileShape<E4M3, D>;
+    extern __shared__ uint8_t raw_smem[];
+    __shared__ TileBars bars;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const uint32_t smem = (shared_addr(raw_smem) + 1023) & ~1023u;
+    if (pl.share) {
+        find_share<S::THREADS>(a, pl, bars);
+    } else {
+        // x: row tiles (the longest first) by key heads; z: requests.
+        const TilePiece pc = {static_cast<int32_t>(blockIdx.z), static_cast<int32_t>(blockIdx.x) % a.Hk,
+                              (pl.tiles - 1 - static_cast<int32_t>(blockIdx.x) / a.Hk) * kPairRows, 0, INT32_MAX, -1};
+        if (pc.row0 >= request_of(a, pc.b).q_rows * a.G) return;
+        if (threadIdx.x == 0) bars.piece[0] = pc;
+    }
+    if (threadIdx.x == 0) {
+        init_bars<S::STAGES, E4M3 ? S::LOADERS * 32 : 1>(bars, false);
+        bars.failed = 0;
+    }
+    if (warp == 8) tmem_alloc<512>(shared_addr(&bars.tmem));
     tmem_fence_before();
     __syncthreads();
     tmem_fence_after();
-    if (warp == 8) tmem_free<512>(tmem);
-    if (bars.failed) {                                                     // a wait ran out: rows of NaN, and counted
-        if (threadIdx.x == 0) atomicAdd(&g_attention_timeouts, 1ull);
-        const int32_t row = row0 + static_cast<int32_t>(threadIdx.x);
-        if (warp < 8 && row < rows) {
-            const int64_t token = r.q0 + row / a.G;
-            const int32_t h = hk * a.G + row % a.G;
-            T *op = static_cast<T *>(a.out.p) + token * a.out.token_stride + h * a.out.head_stride;
-            if (n_used > 1) {
-                const int64_t part = part_row(a, pl, b, hk, chunk, row);
-                *reinterpret_cast<float2 *>(a.part_ml + part * 2) = make_float2(NAN, NAN);
-            } else {
-                for (int c = 0; c < D; ++c) op[c] = static_cast<T>(NAN);
-                if (a.lse) a.lse[token * a.Hq + h] = NAN;
-            }
-        }
+    if (pl.share) {
+        if (warp == 11 && lane == 0) bars.piece[0] = next_piece(a, pl, bars.walk);
+        __syncthreads();
     }
+    // Each role has its own registers, so its own loop.
+    bool failed = false;
+    if (warp < 8) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(S::SOFTMAX_REGS));
+        failed = attend_pieces<T, E4M3, D, kSoftmax>(a, pl, k_map, v_map, bars, smem);
+    } else if (warp < 12) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::PRODUCT_REGS));
+        failed = attend_pieces<T, E4M3, D, kProducts>(a, pl, k_map, v_map, bars, smem);
+    } else if constexpr (E4M3) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::LOADER_REGS));
+        failed = attend_pieces<T, E4M3, D, kLoads>(a, pl, k_map, v_map, bars, smem);
+    }
+    if (warp == 8) tmem_free<512>(bars.tmem);
+    if (failed && threadIdx.x == 0) atomicAdd(&g_attention_timeouts, 1ull);
     grid_dep_allow();
 }
 
@@ -846,8 +1031,8 @@ cudaError_t launch_attend_tile(const AttnArgs &a, const AttnPlan &pl) {
         using S = TileShape<E, D>;
         const cudaError_t e = allow_smem<&k_attend_tile<decltype(t), E, D>>(S::SMEM);
         if (e != cudaSuccess) return e;
-        k_attend_tile<decltype(t), E, D><<<dim3(static_cast<unsigned>(div_up(pl.rows, 2 * kTileRows) * a.Hk), static_cast<unsigned>(pl.n_chunks),
-                      static_cast<unsigned>(a.pg.n_seqs)),
+        k_attend_tile<decltype(t), E, D><<<pl.share ? dim3(static_cast<unsigned>(pl.share))
+                          : dim3(static_cast<unsigned>(pl.tiles * a.Hk), 1, static_cast<unsigned>(a.pg.n_seqs)),
                  S::THREADS, S::SMEM, a.stream>>>(a, pl, k_map, v_map);
         count_launch();
         return cudaGetLastError();

@@ -21,35 +21,32 @@ int64_t few_ctas(int64_t keys, int64_t pairs, int32_t n_seqs, int32_t D) {
     return 152 * 2 * (w < 1 ? 1 : w > 6 ? 6 : w);
 }
 
-// What the plan of the few-rows kernel cuts keys by, and of the tiled one.
-constexpr int32_t kFewAlign = 64, kTileAlign = 128;
+constexpr int32_t kSms = 152;
 
-// Most chunks that a tiled call is cut into.
-constexpr int64_t kTileChunks = 32;
-
-// Keys from the first that a request's rows see, rounded down to align, to the last.
-int64_t keys_of(int32_t max_q_len, int32_t max_kv_len, int32_t window, int32_t align) {
+// Keys from the first that a request's rows see, rounded down to kFewAlign, to the last.
+int64_t keys_of(int32_t max_q_len, int32_t max_kv_len, int32_t window) {
     int64_t keys = max_kv_len;
-    if (window > 0 && static_cast<int64_t>(window) + max_q_len + align < keys)
-        keys = static_cast<int64_t>(window) + max_q_len + align;
+    if (window > 0 && static_cast<int64_t>(window) + max_q_len + kFewAlign < keys)
+        keys = static_cast<int64_t>(window) + max_q_len + kFewAlign;
     return keys < 1 ? 1 : keys;
 }
 
-// Few CTAs (less than the GPU's SMs) leave SMs idle, so the keys are cut then:
-// the cost of n chunks is its waves of CTAs times the keys of one plus what a
-// CTA costs besides, in keys (its start, and its partial results).  Four waves
-// are even enough uncut.
-int64_t tile_chunks(int64_t tiles, int64_t keys) {
-    if (tiles >= 4 * 152) return 1;
-    int64_t best = 1, least = div_up(tiles, 152) * (keys + 512);
-    for (int64_t n = 2; n <= kTileChunks && n * 512 <= keys; ++n) {
-        const int64_t cost = div_up(tiles * n, 152) * (div_up(keys, n) + 1200);
-        if (cost < least) {
-            least = cost;
-            best = n;
-        }
-    }
-    return best;
+// Whether a call's tile pairs are shared out among one CTA an SM, each with the
+// same number of blocks, rather than a CTA each: where there are few of them a
+// wave that is not full, or a long one in the last, costs more than the pieces
+// that are cut (2 x 2500 rows of 8 heads of 64 over 12500 keys, 160 pairs: 158 us
+// with chunks of equal length, 130 shared).  Not where all keys are few, and not
+// where the pairs of a key head would read its keys at times so far apart that
+// they have left L2 meanwhile: shared, they are keys * pairs a head / 152 apart,
+// over all heads; a CTA each, they walk together (six chunks of up to 500 tokens
+// over 226 MB of cache, 71 MB apart: 1.2 GB from DRAM and 300 us shared, 260 us
+// not).  With SMs to spare that counts for less.
+int32_t tile_share(int64_t tiles, int64_t heads, int64_t keys, int64_t D) {
+    constexpr int64_t kApart = 48 << 20;
+    if (tiles >= 4 * kSms || keys < 1024) return 0;
+    const int64_t cache = heads * keys * D * 4;                            // of 16 bits, at most
+    const bool near = tiles <= heads || cache / kSms * heads <= kApart;
+    return near || tiles <= kSms * 3 / 4 ? kSms : 0;
 }
 
 }  // namespace
@@ -59,33 +56,36 @@ AttnPlan attention_plan(const AttnSizes &z) {
     const int32_t q_len = z.max_q_len < z.T ? z.max_q_len : z.T;
     pl.rows = q_len * (z.Hq / z.Hk);
     pl.few = pl.rows <= 16;
-    pl.align = pl.few ? kFewAlign : kTileAlign;
-    const int64_t keys = keys_of(q_len, z.max_kv_len, z.window, pl.align), pairs = static_cast<int64_t>(z.n_seqs) * z.Hk;
-    int64_t n = 1;
-    if (pl.few && pairs > 0)
-        n = (few_ctas(keys, pairs, z.n_seqs, z.D) + pairs / 2) / pairs;
-    else
-        n = tile_chunks(div_up(pl.rows, 256) * pairs, keys);
-    int64_t chunk = div_up(div_up(keys, n < 1 ? 1 : n), pl.align) * pl.align;
-    if (chunk > keys) chunk = div_up(keys, pl.align) * pl.align;
-    pl.chunk = static_cast<int32_t>(chunk);
-    pl.n_chunks = static_cast<int32_t>(div_up(keys, chunk));
+    const int64_t keys = keys_of(q_len, z.max_kv_len, z.window), pairs = static_cast<int64_t>(z.n_seqs) * z.Hk;
+    pl.n_chunks = 1;
+    if (pl.few) {
+        const int64_t n = pairs > 0 ? (few_ctas(keys, pairs, z.n_seqs, z.D) + pairs / 2) / pairs : 1;
+        int64_t chunk = div_up(div_up(keys, n < 1 ? 1 : n), kFewAlign) * kFewAlign;
+        if (chunk > keys) chunk = div_up(keys, kFewAlign) * kFewAlign;
+        pl.chunk = static_cast<int32_t>(chunk);
+        pl.n_chunks = static_cast<int32_t>(div_up(keys, chunk));
+    } else {
+        pl.tiles = static_cast<int32_t>(div_up(pl.rows, kPairRows));
+        pl.share = tile_share(pl.tiles * pairs, pairs, keys, z.D);
+    }
+    if (pl.n_chunks > 1) pl.parts = static_cast<int64_t>(z.n_seqs) * z.Hk * pl.n_chunks * pl.rows;
+    if (pl.share) pl.parts = static_cast<int64_t>(pl.share) * 2 * kPairRows;
     return pl;
 }
 
 size_t attention_workspace_bytes(const AttnSizes &z) {
     const AttnPlan pl = attention_plan(z);
-    if (pl.n_chunks <= 1) return 0;
-    return static_cast<size_t>(z.n_seqs) * z.Hk * pl.n_chunks * pl.rows * (z.D + 2) * sizeof(float);
+    return static_cast<size_t>(pl.parts) * (z.D + 2) * sizeof(float) + static_cast<size_t>(pl.share) * sizeof(int2);
 }
 
 cudaError_t launch_paged_attention(const AttnArgs &args, void *workspace) {
     AttnArgs a = args;
     const AttnPlan pl = attention_plan({a.pg.n_seqs, a.T, a.Hq, a.Hk, a.D, a.max_q_len, a.max_kv_len, a.window});
     a.part_o = static_cast<float *>(workspace);
-    a.part_ml = a.part_o + static_cast<int64_t>(a.pg.n_seqs) * a.Hk * pl.n_chunks * pl.rows * a.D;
+    a.part_ml = a.part_o + pl.parts * a.D;
+    a.cut = reinterpret_cast<int2 *>(a.part_ml + pl.parts * 2);
     const cudaError_t e = pl.few ? launch_attend_few(a, pl) : launch_attend_tile(a, pl);
-    if (e != cudaSuccess || pl.n_chunks == 1) return e;
+    if (e != cudaSuccess || pl.parts == 0) return e;
     return launch_attend_join(a, pl);
 }
 

@@ -18,8 +18,9 @@ struct AttnArgs {
     float v_scale;
     int32_t causal, window;
     float *lse;
-    float *part_o;                    // [n_seqs][Hk][n_chunks][rows][D], of n_chunks > 1
-    float *part_ml;                   // [n_seqs][Hk][n_chunks][rows][2]: maximum (base 2), sum
+    float *part_o;                    // partial results: [parts][D]; what a part is says the plan
+    float *part_ml;                   // [parts][2]: maximum (base 2), sum
+    int2 *cut;                        // shared tiles: of each CTA the tile that it begins and another ends, and that one; -1
     cudaStream_t stream;
 };
 
@@ -30,16 +31,23 @@ struct AttnSizes {
 // How one call is laid out, from its sizes alone.
 struct AttnPlan {
     int32_t few;              // 1: at most 16 query rows a request and key head
-    int32_t align;            // the first chunk starts at a multiple of this many keys, and has a multiple of it
     int32_t rows;             // query rows a request and key head, at most
+    // few rows: parts are [n_seqs][Hk][n_chunks][rows]
     int32_t chunk;            // keys of one CTA
     int32_t n_chunks;         // CTAs along the keys; above 1 their results are joined by a second kernel
+    // many rows
+    int32_t tiles;            // pairs of row tiles a request and key head
+    int32_t share;            // CTAs that share all tiles' blocks of keys evenly, or 0: a CTA a tile pair.  Parts are
+                              // [share][2][kPairRows]: of the tile that began before the CTA's share, of the one that goes on
+    int64_t parts;            // rows of partial results
 };
+constexpr int32_t kFewAlign = 64;      // few rows: the first chunk starts at a multiple of this many keys, and has a multiple
+constexpr int32_t kPairRows = 256;     // rows of a pair of row tiles
 AttnPlan attention_plan(const AttnSizes &z);
 cudaError_t launch_attend_few(const AttnArgs &a, const AttnPlan &pl);      // attend_few.cu
 cudaError_t launch_attend_tile(const AttnArgs &a, const AttnPlan &pl);     // attend_tile.cu
 cudaError_t attention_timeouts(int64_t *count);
-cudaError_t launch_attend_join(const AttnArgs &a, const AttnPlan &pl);     // attend_join.cu
+cudaError_t launch_attend_join(const AttnArgs &a, const AttnPlan &pl);     // attend_join.cu: where there are parts
 
 size_t attention_workspace_bytes(const AttnSizes &z);
 cudaError_t launch_paged_attention(const AttnArgs &a, void *workspace);
@@ -76,11 +84,11 @@ __device__ __forceinline__ void seen_keys(const AttnArgs &a, const Request &r, i
 // Where the keys of a request's chunks start, and how many chunks it has (one
 // at least: it writes the rows that see nothing).
 __device__ __forceinline__ int32_t chunks_of(const AttnArgs &a, const Request &r, int32_t chunk, int32_t n_chunks,
-                                             int32_t align, int32_t *base) {
+                                             int32_t *base) {
     int32_t lo, hi, x;
     seen_keys(a, r, 0, &lo, &x);
     seen_keys(a, r, max(r.q_rows - 1, 0), &x, &hi);
-    *base = min(lo, hi) / align * align;
+    *base = min(lo, hi) / kFewAlign * kFewAlign;
     const int64_t n = (static_cast<int64_t>(hi) - *base + chunk - 1) / chunk;
     return static_cast<int32_t>(min(max(n, static_cast<int64_t>(1)), static_cast<int64_t>(n_chunks)));
 }
@@ -188,14 +196,13 @@ __device__ __forceinline__ int64_t part_row(const AttnArgs &a, const AttnPlan &p
     return ((static_cast<int64_t>(b) * a.Hk + hk) * pl.n_chunks + chunk) * pl.rows + row;
 }
 
-// The end of a row, held by a warp (lane l: elements l*E ..): to out and lse
-// where the request has one chunk, else to the chunk's partial results.
+// The end of a row, held by a warp (lane l: elements l*E ..): to out and lse, or
+// to the partial results' row `at`, if that is not below 0.
 template <typename T, int E>
-__device__ __forceinline__ void store_row(const AttnArgs &a, const AttnPlan &pl, const Request &r, int b, int hk, int i,
-                                          int h, int row, int chunk, int n_used, float m, float l, const float *acc) {
+__device__ __forceinline__ void store_row(const AttnArgs &a, const Request &r, int i, int h, int64_t at, float m, float l,
+                                          const float *acc) {
     const int lane = threadIdx.x & 31;
-    if (n_used > 1) {
-        const int64_t at = part_row(a, pl, b, hk, chunk, row);
+    if (at >= 0) {
         float *o = a.part_o + at * (32 * E) + lane * E;
 #pragma unroll
         for (int e = 0; e < E; ++e) o[e] = acc[e];

@@ -23,6 +23,7 @@ __device__ __forceinline__ bool elect_one() {
 __device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count) {
     asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
 }
+__device__ __forceinline__ void bar_end(uint32_t bar) { asm volatile("mbarrier.inval.shared::cta.b64 [%0];" ::"r"(bar) : "memory"); }
 __device__ __forceinline__ void bar_init_fence() {
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
 }
@@ -135,7 +136,7 @@ __device__ __forceinline__ uint64_t operand_desc(uint32_t addr, uint32_t lead, u
 
 // kind::f16 with FP32 accumulation, M = 128; format 0 fp16, 1 bf16; b_rows_k:
 // the B operand's memory rows run along the product's inner axis.
-constexpr uint32_t mma_desc(int format, int n, bool b_rows_k) {
+__host__ __device__ constexpr uint32_t mma_desc(int format, int n, bool b_rows_k) {
     return (1u << 4) | (static_cast<uint32_t>(format) << 7) | (static_cast<uint32_t>(format) << 10) |
            (static_cast<uint32_t>(b_rows_k) << 16) | (static_cast<uint32_t>(n >> 3) << 17) | ((128u >> 4) << 24);
 }

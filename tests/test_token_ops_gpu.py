@@ -625,3 +625,60 @@ def test_append_and_attention_of_one_request_among_empty_ones(A):
     for t, (b, place) in {0: (1, 47), 2: (1, 49), 3: (4, 0), 42: (4, 39)}.items():
         assert torch.equal(x["v_cache"][tb[b, place // 16], :, place % 16], v[t])
     check_attend(A, x)
+
+
+# Calls whose row tiles are shared out among CTAs: pieces of tiles, whole tiles and tiles that see nothing in one CTA.
+SHARED = [
+    # q_len, kv_len, Hq, Hk, D, causal, window, dtype, cache, page, token_major
+    ([300], [5000], 8, 2, 128, True, 0, BF16, "same", 16, False),                       # few tiles cut many times
+    ([64], [20000], 4, 1, 64, False, 0, F16, "e4m3", 64, True),                         # one tile
+    ([257, 0, 1, 900, 33], [1100, 1300, 1, 900, 4000], 8, 4, 64, True, 0, F16, "same", 32, True),
+    ([257, 0, 1, 900, 33], [1100, 1300, 1, 900, 4000], 8, 4, 128, False, 0, BF16, "e4m3", 16, False),
+    ([700, 1300], [3000, 1300], 16, 8, 64, True, 500, BF16, "same", 128, False),        # windows
+    ([400] * 9, [1500, 0, 1025, 1, 90, 1400, 128, 129, 1279], 6, 3, 128, False, 0, F16, "same", 16, True),  # requests without keys
+    ([1] * 40 + [600], [2000] * 41, 16, 4, 64, True, 0, BF16, "e4m3", 16, False),       # rows far below the longest
+    ([50, 60], [1200, 1100], 12, 3, 128, True, 40, F16, "e4m3", 256, True),
+    ([1500, 20], [1200, 1100], 8, 8, 64, True, 0, F16, "same", 16, False),              # more new tokens than keys
+]
+
+
+@pytest.mark.parametrize("case", SHARED, ids=[str(i) for i in range(len(SHARED))])
+def test_attention_shared_tiles(A, case):
+    x = attend_inputs(case, seed=1000 + SHARED.index(case))
+    poison(x)
+    check_attend(A, x)
+
+
+def test_attention_shared_tiles_repeat(A):
+    """The same call gives the same bits, also beside another one on another stream."""
+    x = attend_inputs(SHARED[2], seed=1100)
+    y = attend_inputs(SHARED[0], seed=1101)
+
+    def run(x):
+        return attend(A, x)[0]
+
+    first = run(x)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        for _ in range(3):
+            run(y)
+    again = [run(x) for _ in range(3)]
+    torch.cuda.synchronize()
+    for o in again:
+        assert torch.equal(first, o)
+
+
+def test_attention_shared_tiles_non_finite(A):
+    """Infinities and NaN among keys that some rows of a shared tile see and others do not."""
+    case = ([200], [3000], 4, 2, 64, True, 0, BF16, "same", 16, False)
+    x = attend_inputs(case, seed=1200)
+    for j, value in ((2900, float("inf")), (2950, float("nan"))):
+        x["v_cache"][int(x["block_table"][0, j // 16]), :, j % 16] = value
+    out, lse = attend(A, x)
+    want, want_lse, tol, lse_tol, done = ref.attention(scale=64 ** -0.5, **x)
+    assert torch.equal(out.isnan().cpu(), want.isnan()) and torch.equal(out.isinf().cpu(), want.isinf())
+    fine = want.isfinite().all(-1).all(-1)
+    assert int(fine.sum()) == 100
+    within(out[fine.cuda()], want[fine], tol[fine], "out")
+    within(lse, want_lse, lse_tol, "lse")
