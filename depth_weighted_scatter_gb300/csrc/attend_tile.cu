@@ -35,9 +35,9 @@
 // take some 12 us beside that (its queries, the first keys, the masked block, O).
 //
 // Measured on a GB300 (2.0 GHz), 32 query and 8 key heads of 128, bf16: a prompt of
-// 8192 tokens 397 us (1380 TFLOP/s of 1900 measured; whole blocks make 1.6 %
+// 8192 tokens 388 us (1415 TFLOP/s of 1900 measured; whole blocks make 1.6 %
 // more products than are counted); six ragged chunks of up to 500 tokens over up to
-// 12000 keys 260 us (1320 TFLOP/s); 2500 tokens of 8 heads of 64 over 12500 keys in
+// 12000 keys 258 us (1330 TFLOP/s); 2500 tokens of 8 heads of 64 over 12500 keys in
 // E4M3, two requests: 131 us (654 TFLOP/s; chunks of equal length instead of shares:
 // 158).  A piece takes 10 us (5.5 at 64) beside its blocks.  Two threads a row gave no gain (they
 // share the exponentials' unit: 471 us for the prompt against 473 at the time), nor
@@ -289,26 +289,23 @@ __device__ __forceinline__ bool attend_piece(const AttnArgs &a, const AttnPlan &
             seen_keys(a, r, i, &lo, &hi);
         }
         if (tr.b1 > tr.b0) {
-            // The warp's 32 rows of queries, 16 bytes a lane and all of them in
-            // flight; where a row starts is known to its own lane.
+            // The warp's 32 rows of queries, copied 16 bytes a lane; where a row
+            // starts is known to its own lane.  (Through registers a prompt of 8192
+            // tokens took 402 us for 388.)
             constexpr int CPR = D / 8, RPI = 32 / CPR, N = 32 / RPI;       // 16-byte pieces of a row; rows a load
             const int64_t at = token * a.q.token_stride + h * a.q.head_stride;
             const int c = lane % CPR;
-            uint4 w[N];
 #pragma unroll
             for (int i = 0; i < N; ++i) {
-                const int x = i * RPI + lane / CPR;
-                const int64_t at_x = __shfl_sync(0xffffffffu, at, x);
-                w[i] = make_uint4(0, 0, 0, 0);
-                if (warp0 + x < rows) w[i] = *reinterpret_cast<const uint4 *>(static_cast<const T *>(a.q.p) + at_x + c * 8);
-            }
-#pragma unroll
-            for (int i = 0; i < N; ++i) {
-                const int x = (warp & 3) * 32 + i * RPI + lane / CPR;
+                const int y = i * RPI + lane / CPR, x = (warp & 3) * 32 + y;
+                const int64_t at_x = __shfl_sync(0xffffffffu, at, y);
+                const bool on = warp0 + y < rows;
                 const uint32_t d = q_smem + t * S::Q_BYTES + (c >> 3) * (kTileRows * 128) + x * 128 + (((c & 7) ^ (x & 7)) << 4);
-                asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(d), "r"(w[i].x), "r"(w[i].y), "r"(w[i].z), "r"(w[i].w)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d),
+                             "l"(static_cast<const T *>(a.q.p) + (on ? at_x : 0) + c * 8), "r"(on ? 16 : 0)
                              : "memory");
             }
+            asm volatile("cp.async.wait_all;" ::: "memory");
             fence_shared_async();
             bar_arrive(shared_addr(&bars.q_full[t]));
         }
