@@ -101,7 +101,7 @@ k_attend_few(AttnArgs a, AttnPlan pl) {
     const Request r = request_of(a, b);
     if (r.q_rows == 0) return;
     int32_t base;
-    const int n_used = chunks_of(a, r, pl.chunk, pl.n_chunks, &base);
+    const int n_used = chunks_of(a, r, pl, &base);
     if (static_cast<int>(blockIdx.x) >= n_used) return;
     const int rows = r.q_rows * a.G;
 

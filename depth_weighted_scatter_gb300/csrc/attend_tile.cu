@@ -193,7 +193,6 @@ __device__ __forceinline__ void find_share(const AttnArgs &a, const AttnPlan &pl
         bars.walk.total = total;
         bars.walk.ctas = ctas;
         if (from >= to) bars.walk.at = to;                                 // no share
-        a.cut[blockIdx.x] = make_int2(-1, 0);
     }
 }
 
@@ -219,8 +218,11 @@ __device__ __forceinline__ TilePiece next_piece(const AttnArgs &a, const AttnPla
             if (from == 0) {                                               // others end it
                 pc.part += kPairRows;
                 const int64_t last = ((first + n) * walk.ctas - 1) / walk.total;           // whose share its last block is in
-                a.cut[blockIdx.x] = make_int2(place, static_cast<int32_t>(last));
+                a.cut[place] = make_int2(blockIdx.x, static_cast<int32_t>(last));
             }
+        } else {
+            pc.part = -1;
+            a.cut[place] = make_int2(-1, 0);
         }
         return pc;
     }
@@ -255,7 +257,7 @@ __device__ __forceinline__ void init_bars(TileBars &bars, bool again) {
 enum { kSoftmax, kProducts, kLoads };
 
 // A role's part of one piece; false where a wait ran out.
-template <typename T, bool E4M3, int D, int ROLE>
+template <typename T, bool E4M3, int D, bool SHARED, int ROLE>
 __device__ __forceinline__ bool attend_piece(const AttnArgs &a, const AttnPlan &pl, const CUtensorMap &k_map,
                                              const CUtensorMap &v_map, TileBars &bars, int piece, uint32_t smem) {
     using S = TileShape<E4M3, D>;
@@ -717,7 +719,7 @@ __device__ __forceinline__ bool attend_piece(const AttnArgs &a, const AttnPlan &
         __syncwarp();
         ok = bar_wait(shared_addr(&bars.drain[t]), 0) && ok;
     } else if (ROLE == kProducts && (E4M3 || warp == 11)) {
-        if (pl.share && warp == 11 && lane == 0) bars.piece[piece ^ 1] = next_piece(a, pl, bars.walk);
+        if (SHARED && warp == 11 && lane == 0) bars.piece[piece ^ 1] = next_piece(a, pl, bars.walk);
     } else if constexpr (!E4M3) {
         // ------------------------------------------------------------ TMA
         const int per = a.pg.page_size < kBlock ? kBlock / a.pg.page_size : 1;         // pages of a block
@@ -766,13 +768,13 @@ __device__ __forceinline__ bool attend_piece(const AttnArgs &a, const AttnPlan &
                 }
             }
         }
-        // All copies landed, and every place let go of, before the barriers are
-        // set up anew.
+        // All copies landed before the CTA ends, and every place let go of before
+        // the barriers are set up anew.
         for (int i = 0; i < S::STAGES && i < issued; ++i) {
             if (at == 0) lap ^= 1;
             at = at == 0 ? S::STAGES - 1 : at - 1;
             ok = bar_wait(shared_addr(&bars.full[at]), lap) && ok;
-            ok = ok && bar_wait(shared_addr(&bars.empty[at]), lap);
+            if (SHARED) ok = ok && bar_wait(shared_addr(&bars.empty[at]), lap);
         }
     } else {
         // ------------------------------------------------------------ E4M3 codes
@@ -867,7 +869,7 @@ __device__ __forceinline__ bool attend_piece(const AttnArgs &a, const AttnPlan &
             look_up(j + 3, ahead);
         }
         asm volatile("cp.async.wait_group 0;" ::: "memory");
-        for (int i = 0; i < S::STAGES && i < 2 * (j1 - j0) && ok; ++i) {   // every place let go of
+        for (int i = 0; SHARED && i < S::STAGES && i < 2 * (j1 - j0) && ok; ++i) {     // every place let go of
             if (at == 0) lap ^= 1;
             at = at == 0 ? S::STAGES - 1 : at - 1;
             ok = bar_wait(shared_addr(&bars.empty[at]), lap);
@@ -884,16 +886,16 @@ __device__ __forceinline__ void sync_roles() {
 }
 
 // A role's part of all of the CTA's pieces; true where a wait ran out.
-template <typename T, bool E4M3, int D, int ROLE>
+template <typename T, bool E4M3, int D, bool SHARED, int ROLE>
 __device__ __forceinline__ bool attend_pieces(const AttnArgs &a, const AttnPlan &pl, const CUtensorMap &k_map,
                                               const CUtensorMap &v_map, TileBars &bars, uint32_t smem) {
     using S = TileShape<E4M3, D>;
     bool failed = false;
-    for (int piece = 0; bars.piece[piece].b >= 0; piece ^= 1) {
-        if (!failed) {
-            const bool ok = attend_piece<T, E4M3, D, ROLE>(a, pl, k_map, v_map, bars, piece, smem);
+    for (int piece = 0; !SHARED || bars.piece[piece].b >= 0; piece ^= 1) {
+        if (!SHARED || !failed) {
+            const bool ok = attend_piece<T, E4M3, D, SHARED, ROLE>(a, pl, k_map, v_map, bars, piece, smem);
             if (!ok) bars.failed = 1;
-        } else if (ROLE == kSoftmax && threadIdx.x == 0 && pl.share) {
+        } else if (ROLE == kSoftmax && threadIdx.x == 0) {
             bars.piece[piece ^ 1] = next_piece(a, pl, bars.walk);
         }
         sync_roles();
@@ -914,14 +916,14 @@ __device__ __forceinline__ bool attend_pieces(const AttnArgs &a, const AttnPlan 
                 }
             }
         }
-        if (!pl.share) break;
+        if (!SHARED) break;
         if (ROLE == kSoftmax && threadIdx.x == 0 && !failed) init_bars<S::STAGES, E4M3 ? S::LOADERS * 32 : 1>(bars, true);
         sync_roles();
     }
     return failed;
 }
 
-template <typename T, bool E4M3, int D>
+template <typename T, bool E4M3, int D, bool SHARED>
 __global__ void __launch_bounds__(TileShape<E4M3, D>::THREADS, 1)
 k_attend_tile(AttnArgs a, AttnPlan pl, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
     using S = TileShape<E4M3, D>;
@@ -929,13 +931,22 @@ k_attend_tile(AttnArgs a, AttnPlan pl, const __grid_constant__ CUtensorMap k_map
     __shared__ TileBars bars;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint32_t smem = (shared_addr(raw_smem) + 1023) & ~1023u;
-    if (pl.share) {
+    if (SHARED) {
         find_share<S::THREADS>(a, pl, bars);
     } else {
-        // x: row tiles (the longest first) by key heads; z: requests.
-        const TilePiece pc = {static_cast<int32_t>(blockIdx.z), static_cast<int32_t>(blockIdx.x) % a.Hk,
-                              (pl.tiles - 1 - static_cast<int32_t>(blockIdx.x) / a.Hk) * kPairRows, 0, INT32_MAX, -1};
-        if (pc.row0 >= request_of(a, pc.b).q_rows * a.G) return;
+        // x: row tiles (the longest first) by key heads; y: chunks; z: requests.
+        TilePiece pc = {static_cast<int32_t>(blockIdx.z), static_cast<int32_t>(blockIdx.x) % a.Hk,
+                        (pl.tiles - 1 - static_cast<int32_t>(blockIdx.x) / a.Hk) * kPairRows, 0, INT32_MAX, -1};
+        const Request r = request_of(a, pc.b);
+        if (pc.row0 >= r.q_rows * a.G) return;
+        if (pl.n_chunks > 1) {
+            int32_t base;
+            const int n = chunks_of(a, r, pl, &base), chunk = blockIdx.y;
+            if (chunk >= n) return;
+            pc.p0 = base / kBlock + chunk * (pl.chunk / kBlock);
+            pc.p1 = pc.p0 + pl.chunk / kBlock;
+            if (n > 1) pc.part = static_cast<int32_t>(part_row(a, pl, pc.b, pc.hk, chunk, pc.row0));
+        }
         if (threadIdx.x == 0) bars.piece[0] = pc;
     }
     if (threadIdx.x == 0) {
@@ -946,7 +957,7 @@ k_attend_tile(AttnArgs a, AttnPlan pl, const __grid_constant__ CUtensorMap k_map
     tmem_fence_before();
     __syncthreads();
     tmem_fence_after();
-    if (pl.share) {
+    if (SHARED) {
         if (warp == 11 && lane == 0) bars.piece[0] = next_piece(a, pl, bars.walk);
         __syncthreads();
     }
@@ -954,13 +965,13 @@ k_attend_tile(AttnArgs a, AttnPlan pl, const __grid_constant__ CUtensorMap k_map
     bool failed = false;
     if (warp < 8) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(S::SOFTMAX_REGS));
-        failed = attend_pieces<T, E4M3, D, kSoftmax>(a, pl, k_map, v_map, bars, smem);
+        failed = attend_pieces<T, E4M3, D, SHARED, kSoftmax>(a, pl, k_map, v_map, bars, smem);
     } else if (warp < 12) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::PRODUCT_REGS));
-        failed = attend_pieces<T, E4M3, D, kProducts>(a, pl, k_map, v_map, bars, smem);
+        failed = attend_pieces<T, E4M3, D, SHARED, kProducts>(a, pl, k_map, v_map, bars, smem);
     } else if constexpr (E4M3) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::LOADER_REGS));
-        failed = attend_pieces<T, E4M3, D, kLoads>(a, pl, k_map, v_map, bars, smem);
+        failed = attend_pieces<T, E4M3, D, SHARED, kLoads>(a, pl, k_map, v_map, bars, smem);
     }
     if (warp == 8) tmem_free<512>(bars.tmem);
     if (failed && threadIdx.x == 0) atomicAdd(&g_attention_timeouts, 1ull);
@@ -1022,17 +1033,21 @@ cudaError_t attention_timeouts(int64_t *count) {
 cudaError_t launch_attend_tile(const AttnArgs &a, const AttnPlan &pl) {
     CUtensorMap k_map = {}, v_map = {};
     if (!a.cache_e4m3 && (!cache_map(a, a.k_cache, false, &k_map) || !cache_map(a, a.v_cache, true, &v_map))) return cudaErrorInvalidValue;
-    auto run = [&](auto t, auto e4m3, auto d) {
-        constexpr bool E = decltype(e4m3)::value;
+    auto launch = [&](auto t, auto e4m3, auto d, auto shared, dim3 grid) {
+        constexpr bool E = decltype(e4m3)::value, SHARED = decltype(shared)::value;
         constexpr int D = decltype(d)::value;
         using S = TileShape<E, D>;
-        const cudaError_t e = allow_smem<&k_attend_tile<decltype(t), E, D>>(S::SMEM);
+        const cudaError_t e = allow_smem<&k_attend_tile<decltype(t), E, D, SHARED>>(S::SMEM);
         if (e != cudaSuccess) return e;
-        k_attend_tile<decltype(t), E, D><<<pl.share ? dim3(static_cast<unsigned>(pl.share))
-                          : dim3(static_cast<unsigned>(pl.tiles * a.Hk), 1, static_cast<unsigned>(a.pg.n_seqs)),
-                 S::THREADS, S::SMEM, a.stream>>>(a, pl, k_map, v_map);
+        k_attend_tile<decltype(t), E, D, SHARED><<<grid, S::THREADS, S::SMEM, a.stream>>>(a, pl, k_map, v_map);
         count_launch();
         return cudaGetLastError();
+    };
+    auto run = [&](auto t, auto e4m3, auto d) {
+        if (pl.share) return launch(t, e4m3, d, std::true_type{}, dim3(static_cast<unsigned>(pl.share)));
+        return launch(t, e4m3, d, std::false_type{},
+                      dim3(static_cast<unsigned>(pl.tiles * a.Hk), static_cast<unsigned>(pl.n_chunks),
+                           static_cast<unsigned>(a.pg.n_seqs)));
     };
     auto by_d = [&](auto t, auto e4m3) {
         return a.D == 64 ? run(t, e4m3, std::integral_constant<int, 64>{})

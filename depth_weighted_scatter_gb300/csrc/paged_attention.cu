@@ -1,5 +1,6 @@
 // paged_attention.cu -- attention of new tokens over the paged cache: how a
 // call is laid out, and its launches.
+#include <algorithm>
 #include <cmath>
 
 #include "paged_attention.cuh"
@@ -23,30 +24,56 @@ int64_t few_ctas(int64_t keys, int64_t pairs, int32_t n_seqs, int32_t D) {
 
 constexpr int32_t kSms = 152;
 
-// Keys from the first that a request's rows see, rounded down to kFewAlign, to the last.
-int64_t keys_of(int32_t max_q_len, int32_t max_kv_len, int32_t window) {
+// What the plan of the few-rows kernel cuts keys by, and of the tiled one.
+constexpr int32_t kFewAlign = 64, kTileAlign = 128;
+
+// Most chunks that a tiled call is cut into.
+constexpr int64_t kTileChunks = 32;
+
+// Keys of a CTA's share of a tiled call, at least.
+constexpr int64_t kLeastShare = 6 * 128;
+
+// Keys from the first that a request's rows see, rounded down to align, to the last.
+int64_t keys_of(int32_t max_q_len, int32_t max_kv_len, int32_t window, int32_t align) {
     int64_t keys = max_kv_len;
-    if (window > 0 && static_cast<int64_t>(window) + max_q_len + kFewAlign < keys)
-        keys = static_cast<int64_t>(window) + max_q_len + kFewAlign;
+    if (window > 0 && static_cast<int64_t>(window) + max_q_len + align < keys)
+        keys = static_cast<int64_t>(window) + max_q_len + align;
     return keys < 1 ? 1 : keys;
 }
 
-// Whether a call's tile pairs are shared out among one CTA an SM, each with the
-// same number of blocks, rather than a CTA each: where there are few of them a
-// wave that is not full, or a long one in the last, costs more than the pieces
-// that are cut (2 x 2500 rows of 8 heads of 64 over 12500 keys, 160 pairs: 158 us
-// with chunks of equal length, 130 shared).  Not where all keys are few, and not
-// where the pairs of a key head would read its keys at times so far apart that
-// they have left L2 meanwhile: shared, they are keys * pairs a head / 152 apart,
-// over all heads; a CTA each, they walk together (six chunks of up to 500 tokens
-// over 226 MB of cache, 71 MB apart: 1.2 GB from DRAM and 300 us shared, 260 us
-// not).  With SMs to spare that counts for less.
-int32_t tile_share(int64_t tiles, int64_t heads, int64_t keys, int64_t D) {
+// Few CTAs (less than the GPU's SMs) leave SMs idle, so the keys are cut then:
+// the cost of n chunks is its waves of CTAs times the keys of one plus what a
+// CTA costs besides, in keys (its start, and its partial results).  Four waves
+// are even enough uncut.
+//
+// Waves that are not full, or a last one as long as the others, can cost more
+// than that, so the pairs' blocks may be shared out evenly among one CTA an SM
+// instead (2 x 2500 rows of 8 heads of 64 over 12500 keys, 160 pairs: 158 us in
+// three chunks, 131 shared): each CTA then has pieces of two pairs and a pair's
+// share of whole ones.  Not where the pairs of a key head would read its keys at
+// times so far apart that they have left L2 meanwhile: shared, keys * pairs a
+// head / 152 of them lie between, over all heads; chunks walk together (six
+// chunks of up to 500 tokens over 226 MB of cache, 71 MB apart: 1.2 GB from DRAM
+// and 300 us shared, 258 us as one chunk).  A pair starts at 700 keys, a CTA at
+// 1500 and the join besides: 2 x 1000 tokens of 8 heads of 64 over 8000 keys are
+// 62.5 us in two chunks, 51.2 shared; 64 tokens over 20000 keys 18.7 in 32, 24.8
+// shared, as a share is not less than kLeastShare.
+int64_t tile_chunks(int64_t tiles, int64_t heads, int64_t keys, int64_t D, bool *share) {
+    *share = false;
+    if (tiles >= 4 * kSms) return 1;
+    int64_t best = 1, least = div_up(tiles, kSms) * (keys + 512);
+    for (int64_t n = 2; n <= kTileChunks && n * 512 <= keys; ++n) {
+        const int64_t cost = div_up(tiles * n, kSms) * (div_up(keys, n) + 1200);
+        if (cost < least) {
+            least = cost;
+            best = n;
+        }
+    }
     constexpr int64_t kApart = 48 << 20;
-    if (tiles >= 4 * kSms || keys < 1024) return 0;
     const int64_t cache = heads * keys * D * 4;                            // of 16 bits, at most
-    const bool near = tiles <= heads || cache / kSms * heads <= kApart;
-    return near || tiles <= kSms * 3 / 4 ? kSms : 0;
+    if (tiles <= heads || cache / kSms * heads <= kApart)
+        *share = std::max(tiles * (keys + 700) / kSms, kLeastShare) + 1500 < least;
+    return *share ? 1 : best;
 }
 
 }  // namespace
@@ -56,18 +83,21 @@ AttnPlan attention_plan(const AttnSizes &z) {
     const int32_t q_len = z.max_q_len < z.T ? z.max_q_len : z.T;
     pl.rows = q_len * (z.Hq / z.Hk);
     pl.few = pl.rows <= 16;
-    const int64_t keys = keys_of(q_len, z.max_kv_len, z.window), pairs = static_cast<int64_t>(z.n_seqs) * z.Hk;
-    pl.n_chunks = 1;
+    pl.align = pl.few ? kFewAlign : kTileAlign;
+    const int64_t keys = keys_of(q_len, z.max_kv_len, z.window, pl.align), pairs = static_cast<int64_t>(z.n_seqs) * z.Hk;
+    int64_t n = 1;
     if (pl.few) {
-        const int64_t n = pairs > 0 ? (few_ctas(keys, pairs, z.n_seqs, z.D) + pairs / 2) / pairs : 1;
-        int64_t chunk = div_up(div_up(keys, n < 1 ? 1 : n), kFewAlign) * kFewAlign;
-        if (chunk > keys) chunk = div_up(keys, kFewAlign) * kFewAlign;
-        pl.chunk = static_cast<int32_t>(chunk);
-        pl.n_chunks = static_cast<int32_t>(div_up(keys, chunk));
+        if (pairs > 0) n = (few_ctas(keys, pairs, z.n_seqs, z.D) + pairs / 2) / pairs;
     } else {
+        bool share;
         pl.tiles = static_cast<int32_t>(div_up(pl.rows, kPairRows));
-        pl.share = tile_share(pl.tiles * pairs, pairs, keys, z.D);
+        n = tile_chunks(pl.tiles * pairs, pairs, keys, z.D, &share);
+        if (share) pl.share = kSms;
     }
+    int64_t chunk = div_up(div_up(keys, n < 1 ? 1 : n), pl.align) * pl.align;
+    if (chunk > keys) chunk = div_up(keys, pl.align) * pl.align;
+    pl.chunk = static_cast<int32_t>(chunk);
+    pl.n_chunks = static_cast<int32_t>(div_up(keys, chunk));
     if (pl.n_chunks > 1) pl.parts = static_cast<int64_t>(z.n_seqs) * z.Hk * pl.n_chunks * pl.rows;
     if (pl.share) pl.parts = static_cast<int64_t>(pl.share) * 2 * kPairRows;
     return pl;
@@ -75,7 +105,7 @@ AttnPlan attention_plan(const AttnSizes &z) {
 
 size_t attention_workspace_bytes(const AttnSizes &z) {
     const AttnPlan pl = attention_plan(z);
-    return static_cast<size_t>(pl.parts) * (z.D + 2) * sizeof(float) + static_cast<size_t>(pl.share) * sizeof(int2);
+    return static_cast<size_t>(pl.parts) * (z.D + 2) * sizeof(float) + (pl.share ? static_cast<size_t>(pl.tiles) * z.Hk * z.n_seqs * sizeof(int2) : 0);
 }
 
 cudaError_t launch_paged_attention(const AttnArgs &args, void *workspace) {

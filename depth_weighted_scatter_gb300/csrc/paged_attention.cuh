@@ -20,7 +20,7 @@ struct AttnArgs {
     float *lse;
     float *part_o;                    // partial results: [parts][D]; what a part is says the plan
     float *part_ml;                   // [parts][2]: maximum (base 2), sum
-    int2 *cut;                        // shared tiles: of each CTA the tile that it begins and another ends, and that one; -1
+    int2 *cut;                        // shared tiles, [n_seqs][Hk][tiles]: first and last CTA that have a part; -1: one alone
     cudaStream_t stream;
 };
 
@@ -31,17 +31,16 @@ struct AttnSizes {
 // How one call is laid out, from its sizes alone.
 struct AttnPlan {
     int32_t few;              // 1: at most 16 query rows a request and key head
+    int32_t align;            // the first chunk starts at a multiple of this many keys, and has a multiple of it
     int32_t rows;             // query rows a request and key head, at most
-    // few rows: parts are [n_seqs][Hk][n_chunks][rows]
     int32_t chunk;            // keys of one CTA
-    int32_t n_chunks;         // CTAs along the keys; above 1 their results are joined by a second kernel
-    // many rows
-    int32_t tiles;            // pairs of row tiles a request and key head
-    int32_t share;            // CTAs that share all tiles' blocks of keys evenly, or 0: a CTA a tile pair.  Parts are
-                              // [share][2][kPairRows]: of the tile that began before the CTA's share, of the one that goes on
+    int32_t n_chunks;         // CTAs along the keys; above 1 their results are joined by a second kernel: parts are
+                              // [n_seqs][Hk][n_chunks][rows]
+    int32_t tiles;            // many rows: pairs of row tiles a request and key head
+    int32_t share;            // many rows: CTAs that share all pairs' blocks of keys evenly, or 0.  Parts are then
+                              // [share][2][kPairRows]: of the pair that began before the CTA's share, of the one that goes on
     int64_t parts;            // rows of partial results
 };
-constexpr int32_t kFewAlign = 64;      // few rows: the first chunk starts at a multiple of this many keys, and has a multiple
 constexpr int32_t kPairRows = 256;     // rows of a pair of row tiles
 AttnPlan attention_plan(const AttnSizes &z);
 cudaError_t launch_attend_few(const AttnArgs &a, const AttnPlan &pl);      // attend_few.cu
@@ -83,14 +82,13 @@ __device__ __forceinline__ void seen_keys(const AttnArgs &a, const Request &r, i
 
 // Where the keys of a request's chunks start, and how many chunks it has (one
 // at least: it writes the rows that see nothing).
-__device__ __forceinline__ int32_t chunks_of(const AttnArgs &a, const Request &r, int32_t chunk, int32_t n_chunks,
-                                             int32_t *base) {
+__device__ __forceinline__ int32_t chunks_of(const AttnArgs &a, const Request &r, const AttnPlan &pl, int32_t *base) {
     int32_t lo, hi, x;
     seen_keys(a, r, 0, &lo, &x);
     seen_keys(a, r, max(r.q_rows - 1, 0), &x, &hi);
-    *base = min(lo, hi) / kFewAlign * kFewAlign;
-    const int64_t n = (static_cast<int64_t>(hi) - *base + chunk - 1) / chunk;
-    return static_cast<int32_t>(min(max(n, static_cast<int64_t>(1)), static_cast<int64_t>(n_chunks)));
+    *base = min(lo, hi) / pl.align * pl.align;
+    const int64_t n = (static_cast<int64_t>(hi) - *base + pl.chunk - 1) / pl.chunk;
+    return static_cast<int32_t>(min(max(n, static_cast<int64_t>(1)), static_cast<int64_t>(pl.n_chunks)));
 }
 
 // 2^x, 2^-inf = 0; results below 2^-126 are zero.

@@ -627,8 +627,8 @@ def test_append_and_attention_of_one_request_among_empty_ones(A):
     check_attend(A, x)
 
 
-# Calls whose row tiles are shared out among CTAs: pieces of tiles, whole tiles and tiles that see nothing in one CTA.
-SHARED = [
+# Long calls of few row tiles, their keys cut into chunks.
+CHUNKED = [
     # q_len, kv_len, Hq, Hk, D, causal, window, dtype, cache, page, token_major
     ([300], [5000], 8, 2, 128, True, 0, BF16, "same", 16, False),                       # few tiles cut many times
     ([64], [20000], 4, 1, 64, False, 0, F16, "e4m3", 64, True),                         # one tile
@@ -642,9 +642,37 @@ SHARED = [
 ]
 
 
+@pytest.mark.parametrize("case", CHUNKED, ids=[str(i) for i in range(len(CHUNKED))])
+def test_attention_chunked_tiles(A, case):
+    x = attend_inputs(case, seed=1000 + CHUNKED.index(case))
+    poison(x)
+    check_attend(A, x)
+
+
+# Calls whose row tiles are shared out among CTAs: pieces of tiles, whole tiles and tiles that see nothing in one CTA.
+SHARED = [
+    ([1030, 0, 1, 300, 40], [3000, 7, 1, 300, 2990], 8, 8, 64, True, 0, F16, "same", 32, True),
+    ([1030, 0, 1, 300, 40], [3300, 7, 1, 300, 2990], 8, 8, 128, False, 0, BF16, "e4m3", 16, False),
+    ([300, 300, 300, 5, 5], [3500, 3400, 0, 128, 3500], 32, 8, 128, True, 0, BF16, "same", 16, True),    # one without keys
+    ([2100, 10], [5000, 4900], 10, 10, 64, True, 0, BF16, "e4m3", 64, False),
+    ([700, 1300], [4000, 3500], 32, 16, 64, True, 2200, BF16, "same", 128, False),                      # windows
+    ([40] * 100, [7000] + [300] * 99, 4, 1, 64, True, 0, F16, "e4m3", 16, False),                       # one far longer
+    ([1100] * 4, [3500, 900, 1099, 600], 10, 10, 64, True, 0, F16, "same", 256, True),                  # more tokens than keys
+]
+
+
+def shares(A, case):
+    """Whether the call's workspace is that of shared tiles."""
+    q_len, kv_len, Hq, Hk, D, _, window = case[:7]
+    size = A.bevpool_paged_attention_workspace_size(len(q_len), sum(q_len), Hq, Hk, D, max(q_len), max(kv_len), window)
+    tiles = -(-max(q_len) * (Hq // Hk) // 256) * Hk * len(q_len)
+    return size == 152 * 512 * (D + 2) * 4 + tiles * 8
+
+
 @pytest.mark.parametrize("case", SHARED, ids=[str(i) for i in range(len(SHARED))])
 def test_attention_shared_tiles(A, case):
-    x = attend_inputs(case, seed=1000 + SHARED.index(case))
+    assert shares(A, case)
+    x = attend_inputs(case, seed=1300 + SHARED.index(case))
     poison(x)
     check_attend(A, x)
 
@@ -652,7 +680,7 @@ def test_attention_shared_tiles(A, case):
 def test_attention_shared_tiles_repeat(A):
     """The same call gives the same bits, also beside another one on another stream."""
     x = attend_inputs(SHARED[2], seed=1100)
-    y = attend_inputs(SHARED[0], seed=1101)
+    y = attend_inputs(SHARED[3], seed=1101)
 
     def run(x):
         return attend(A, x)[0]
@@ -671,14 +699,15 @@ def test_attention_shared_tiles_repeat(A):
 
 def test_attention_shared_tiles_non_finite(A):
     """Infinities and NaN among keys that some rows of a shared tile see and others do not."""
-    case = ([200], [3000], 4, 2, 64, True, 0, BF16, "same", 16, False)
+    case = SHARED[0]
+    assert shares(A, case)
     x = attend_inputs(case, seed=1200)
-    for j, value in ((2900, float("inf")), (2950, float("nan"))):
-        x["v_cache"][int(x["block_table"][0, j // 16]), :, j % 16] = value
+    for j, value in ((2500, float("inf")), (2900, float("nan"))):
+        x["v_cache"][int(x["block_table"][0, j // 32]), :, j % 32] = value
     out, lse = attend(A, x)
     want, want_lse, tol, lse_tol, done = ref.attention(scale=64 ** -0.5, **x)
     assert torch.equal(out.isnan().cpu(), want.isnan()) and torch.equal(out.isinf().cpu(), want.isinf())
     fine = want.isfinite().all(-1).all(-1)
-    assert int(fine.sum()) == 100
+    assert int(fine.sum()) == 530 + 1 + 300 + 40
     within(out[fine.cuda()], want[fine], tol[fine], "out")
-    within(lse, want_lse, lse_tol, "lse")
+    within(lse[done.cuda()], want_lse[done], lse_tol[done], "lse")
