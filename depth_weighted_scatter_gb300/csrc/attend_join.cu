@@ -3,7 +3,8 @@
 // o = sum o_c 2^(m_c - m) / l, in a fixed order.
 // Bound by the read of the partial results and, where they are few, by its latency:
 // with one row of a warp at a time 3 x 700 tokens over 1500 keys took 24.7 us in
-// all for 22.6, two requests over 131072 keys 92.4 for 90.5.
+// all, with four 22.6.  (Where a request has few rows that leaves warps idle: 64
+// single tokens 234 and 239 us.)
 #include "paged_attention.cuh"
 
 namespace bevpool {
@@ -11,12 +12,13 @@ namespace bevpool {
 namespace {
 
 // W warps a query row: they take the parts in turn, and the first joins their
-// sums.  SHARED: rows are those of a tile pair that several CTAs shared.
-template <typename T, int D, int W, bool SHARED>
+// sums.  A warp takes R rows at a time, their loads in flight together.  SHARED:
+// rows are those of a tile pair that several CTAs shared.
+template <typename T, int D, int W, int R, bool SHARED>
 __global__ void __launch_bounds__(kThreads)
 k_attend_join(AttnArgs a, AttnPlan pl) {
-    constexpr int E = D / 32, R = W == 1 ? 4 : 1;          // rows of a warp at a time, their loads in flight together
-    constexpr int ROWS = kWarps / W * R;                   // of a CTA
+    constexpr int E = D / 32, ROWS = kWarps / W * R;       // rows of a CTA
+    static_assert(W == 1 || R == 1, "rows of several warps are one at a time");
     struct alignas(E * 4) Elements {
         float x[E];
     };
@@ -109,15 +111,20 @@ cudaError_t launch_attend_join(const AttnArgs &a, const AttnPlan &pl) {
         if (e == cudaSuccess) count_launch();
         return e;
     };
-    auto run = [&](auto t, auto d, auto w) {
-        constexpr int D = decltype(d)::value, W = decltype(w)::value, ROWS = kWarps / W * (W == 1 ? 4 : 1);
+    auto by_rows = [&](auto t, auto d, auto w, auto r) {
+        constexpr int D = decltype(d)::value, W = decltype(w)::value, R = decltype(r)::value, ROWS = kWarps / W * R;
         if (pl.share)
-            return launch(k_attend_join<decltype(t), D, W, true>,
+            return launch(k_attend_join<decltype(t), D, W, R, true>,
                           dim3(kPairRows / ROWS, static_cast<unsigned>(pl.tiles * a.Hk * a.pg.n_seqs)));
         int64_t gx = div_up(pl.rows, ROWS);
         if (gx > 1024) gx = 1024;
-        return launch(k_attend_join<decltype(t), D, W, false>,
+        return launch(k_attend_join<decltype(t), D, W, R, false>,
                       dim3(static_cast<unsigned>(gx), static_cast<unsigned>(a.Hk), static_cast<unsigned>(a.pg.n_seqs)));
+    };
+    auto run = [&](auto t, auto d, auto w) {
+        if constexpr (decltype(w)::value == 1)
+            if (!pl.few) return by_rows(t, d, w, std::integral_constant<int, 4>{});
+        return by_rows(t, d, w, std::integral_constant<int, 1>{});
     };
     // A warp a row where a row has few chunks (a CTA then takes eight rows), all
     // of a CTA's where it has many.  The whole call, with 76 chunks of 64 rows:

@@ -14,7 +14,7 @@
 //                    store them in the same layout
 // While one tile is in its softmax the tensor core works on the other.
 //
-// Where there are few pairs of row tiles they are shared out (AttnPlan::share): each
+// Where there are few pairs of row tiles they may be shared out (AttnPlan::share): each
 // CTA works its part of all pairs' blocks, pieces of pairs at its ends leave their
 // sums, maxima and O to a second kernel.  A piece starts with every barrier set up
 // anew; warp 11 looks the next one up meanwhile.
@@ -32,16 +32,17 @@
 // 2950 are measured, as the waits between the steps of a tile are not all covered
 // by the other's.  At 64 the softmax warps: 2300 cycles of dependent instructions
 // against 1024 of products and as many of exponentials.  A CTA's start and end
-// take some 12 us beside that (its queries, the first keys, the masked block, O).
+// take 7 us beside that, a piece of a share 10 (at 64: 5.5): its queries, the first
+// keys, the masked block, O.
 //
 // Measured on a GB300 (2.0 GHz), 32 query and 8 key heads of 128, bf16: a prompt of
-// 8192 tokens 388 us (1415 TFLOP/s of 1900 measured; whole blocks make 1.6 %
+// 8192 tokens 380 us (1445 TFLOP/s of 1900 measured; whole blocks make 1.6 %
 // more products than are counted); six ragged chunks of up to 500 tokens over up to
 // 12000 keys 258 us (1330 TFLOP/s); 2500 tokens of 8 heads of 64 over 12500 keys in
 // E4M3, two requests: 131 us (654 TFLOP/s; chunks of equal length instead of shares:
-// 158).  A piece takes 10 us (5.5 at 64) beside its blocks.  Two threads a row gave no gain (they
-// share the exponentials' unit: 471 us for the prompt against 473 at the time), nor
-// did going on with other places of the grid in one CTA (423 against 417).
+// 158).  Two threads a row gave no gain (they share the exponentials' unit: 471 us
+// for the prompt against 473 at the time), nor did going on with other places of the
+// grid in one CTA (423 against 417).
 //
 // A wait that runs out (it never should) ends the CTA: its rows become NaN and
 // bevpool_attention_timeouts counts it.
@@ -262,7 +263,7 @@ __device__ __forceinline__ bool attend_piece(const AttnArgs &a, const AttnPlan &
                                              const CUtensorMap &v_map, TileBars &bars, int piece, uint32_t smem) {
     using S = TileShape<E4M3, D>;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const TilePiece &pc = bars.piece[piece];
+    const TilePiece pc = bars.piece[piece];
     const int hk = pc.hk, b = pc.b;
     const Request r = request_of(a, b);
     const int32_t rows = r.q_rows * a.G, row0 = pc.row0;

@@ -105,7 +105,8 @@ AttnPlan attention_plan(const AttnSizes &z) {
 
 size_t attention_workspace_bytes(const AttnSizes &z) {
     const AttnPlan pl = attention_plan(z);
-    return static_cast<size_t>(pl.parts) * (z.D + 2) * sizeof(float) + (pl.share ? static_cast<size_t>(pl.tiles) * z.Hk * z.n_seqs * sizeof(int2) : 0);
+    const size_t cuts = pl.share ? static_cast<size_t>(pl.tiles) * z.Hk * z.n_seqs : 0;
+    return static_cast<size_t>(pl.parts) * (z.D + 2) * sizeof(float) + cuts * sizeof(int2);
 }
 
 cudaError_t launch_paged_attention(const AttnArgs &args, void *workspace) {
