@@ -57,8 +57,11 @@ int64_t keys_of(int32_t max_q_len, int32_t max_kv_len, int32_t window, int32_t a
 // and 300 us shared, 258 us as one chunk).  A pair starts at 700 keys, a CTA at
 // 1500 and the join besides: 2 x 1000 tokens of 8 heads of 64 over 8000 keys are
 // 62.5 us in two chunks, 51.2 shared; 64 tokens over 20000 keys 18.7 in 32, 24.8
-// shared, as a share is not less than kLeastShare.
-int64_t tile_chunks(int64_t tiles, int64_t heads, int64_t keys, int64_t D, bool *share) {
+// shared, as a share is not less than kLeastShare.  Not for a causal prompt either:
+// its tiles are not alike, and with the longest first no wave is left half full
+// (4096 tokens: 144 us shared, 118 not; 5000 that all see each other, 8 heads of
+// 64: 83 shared, 108 not).
+int64_t tile_chunks(int64_t tiles, int64_t heads, int64_t keys, int64_t D, bool alike, bool *share) {
     *share = false;
     if (tiles >= 4 * kSms) return 1;
     int64_t best = 1, least = div_up(tiles, kSms) * (keys + 512);
@@ -71,7 +74,7 @@ int64_t tile_chunks(int64_t tiles, int64_t heads, int64_t keys, int64_t D, bool 
     }
     constexpr int64_t kApart = 48 << 20;
     const int64_t cache = heads * keys * D * 4;                            // of 16 bits, at most
-    if (tiles <= heads || cache / kSms * heads <= kApart)
+    if (alike && (tiles <= heads || cache / kSms * heads <= kApart))
         *share = std::max(tiles * (keys + 700) / kSms, kLeastShare) + 1500 < least;
     return *share ? 1 : best;
 }
@@ -91,7 +94,7 @@ AttnPlan attention_plan(const AttnSizes &z) {
     } else {
         bool share;
         pl.tiles = static_cast<int32_t>(div_up(pl.rows, kPairRows));
-        n = tile_chunks(pl.tiles * pairs, pairs, keys, z.D, &share);
+        n = tile_chunks(pl.tiles * pairs, pairs, keys, z.D, !z.causal || 2 * static_cast<int64_t>(q_len) <= keys, &share);
         if (share) pl.share = kSms;
     }
     int64_t chunk = div_up(div_up(keys, n < 1 ? 1 : n), pl.align) * pl.align;
@@ -103,15 +106,19 @@ AttnPlan attention_plan(const AttnSizes &z) {
     return pl;
 }
 
-size_t attention_workspace_bytes(const AttnSizes &z) {
-    const AttnPlan pl = attention_plan(z);
-    const size_t cuts = pl.share ? static_cast<size_t>(pl.tiles) * z.Hk * z.n_seqs : 0;
-    return static_cast<size_t>(pl.parts) * (z.D + 2) * sizeof(float) + cuts * sizeof(int2);
+size_t attention_workspace_bytes(AttnSizes z) {
+    size_t most = 0;
+    for (z.causal = 0; z.causal < 2; ++z.causal) {
+        const AttnPlan pl = attention_plan(z);
+        const size_t cuts = pl.share ? static_cast<size_t>(pl.tiles) * z.Hk * z.n_seqs : 0;
+        most = std::max(most, static_cast<size_t>(pl.parts) * (z.D + 2) * sizeof(float) + cuts * sizeof(int2));
+    }
+    return most;
 }
 
 cudaError_t launch_paged_attention(const AttnArgs &args, void *workspace) {
     AttnArgs a = args;
-    const AttnPlan pl = attention_plan({a.pg.n_seqs, a.T, a.Hq, a.Hk, a.D, a.max_q_len, a.max_kv_len, a.window});
+    const AttnPlan pl = attention_plan({a.pg.n_seqs, a.T, a.Hq, a.Hk, a.D, a.max_q_len, a.max_kv_len, a.window, a.causal});
     a.part_o = static_cast<float *>(workspace);
     a.part_ml = a.part_o + pl.parts * a.D;
     a.cut = reinterpret_cast<int2 *>(a.part_ml + pl.parts * 2);

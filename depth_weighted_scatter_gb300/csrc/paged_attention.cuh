@@ -25,7 +25,7 @@ struct AttnArgs {
 };
 
 struct AttnSizes {
-    int32_t n_seqs, T, Hq, Hk, D, max_q_len, max_kv_len, window;
+    int32_t n_seqs, T, Hq, Hk, D, max_q_len, max_kv_len, window, causal;
 };
 
 // How one call is laid out, from its sizes alone.
@@ -48,7 +48,7 @@ cudaError_t launch_attend_tile(const AttnArgs &a, const AttnPlan &pl);     // at
 cudaError_t attention_timeouts(int64_t *count);
 cudaError_t launch_attend_join(const AttnArgs &a, const AttnPlan &pl);     // attend_join.cu: where there are parts
 
-size_t attention_workspace_bytes(const AttnSizes &z);
+size_t attention_workspace_bytes(AttnSizes z);     // causal or not
 cudaError_t launch_paged_attention(const AttnArgs &a, void *workspace);
 
 // ---------------------------------------------------------------- device

@@ -261,7 +261,7 @@ size_t bevpool_paged_attention_workspace_size(int32_t n_seqs, int32_t n_tokens, 
         window < 0)
         return 0;
     if (n_seqs == 0 || n_tokens == 0 || max_q_len == 0) return 0;
-    return attention_workspace_bytes({n_seqs, n_tokens, n_q_heads, n_k_heads, head_dim, max_q_len, max_kv_len, window});
+    return attention_workspace_bytes({n_seqs, n_tokens, n_q_heads, n_k_heads, head_dim, max_q_len, max_kv_len, window, 0});
 }
 
 bevpool_status bevpool_paged_attention(
@@ -288,7 +288,7 @@ bevpool_status bevpool_paged_attention(
         return BEVPOOL_ERR_INVALID_ARG;
     if (window < 0 || (window > 0 && !causal)) return BEVPOOL_ERR_INVALID_ARG;
     const size_t need =
-        attention_workspace_bytes({n_seqs, n_tokens, n_q_heads, n_k_heads, head_dim, max_q_len, max_kv_len, window});
+        attention_workspace_bytes({n_seqs, n_tokens, n_q_heads, n_k_heads, head_dim, max_q_len, max_kv_len, window, 0});
     if (need > 0 && (!workspace || !aligned(workspace, 256) || workspace_bytes < need)) return BEVPOOL_ERR_WORKSPACE;
     a.dtype = dtype;
     a.cache_e4m3 = e4m3;

@@ -711,3 +711,13 @@ def test_attention_shared_tiles_non_finite(A):
     assert int(fine.sum()) == 530 + 1 + 300 + 40
     within(out[fine.cuda()], want[fine], tol[fine], "out")
     within(lse[done.cuda()], want_lse[done], lse_tol[done], "lse")
+
+
+@pytest.mark.parametrize("causal", [True, False])
+def test_attention_whole_prompts(A, causal):
+    """The same sizes, causal and not: tiles of all lengths and tiles that are alike are laid out differently."""
+    case = ([2100], [2100], 20, 20, 64, causal, 0, BF16, "same", 16, False)
+    assert shares(A, case)
+    x = attend_inputs(case, seed=1400)
+    poison(x)
+    check_attend(A, x)
