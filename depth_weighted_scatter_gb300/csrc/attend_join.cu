@@ -13,7 +13,10 @@ namespace {
 
 // W warps a query row: they take the parts in turn, and the first joins their
 // sums.  A warp takes R rows at a time, their loads in flight together.  SHARED:
-// rows are those of a tile pair that several CTAs shared.
+// rows are those of a tile pair that several CTAs shared.  Every CTA waits for the
+// attention kernel, also one that has nothing to join: where no request has more
+// than one chunk that kernel alone writes the results, and what comes next in the
+// stream is ordered after this kernel.
 template <typename T, int D, int W, int R, bool SHARED>
 __global__ void __launch_bounds__(kThreads)
 k_attend_join(AttnArgs a, AttnPlan pl) {
@@ -34,8 +37,8 @@ k_attend_join(AttnArgs a, AttnPlan pl) {
         r = request_of(a, b);
         first_row = blockIdx.y % pl.tiles * kPairRows;
         row_end = min(r.q_rows * a.G, first_row + kPairRows);
-        if (first_row >= row_end) return;
         grid_dep_wait();
+        if (first_row >= row_end) return;
         const int2 cut = a.cut[blockIdx.y];
         if (cut.x < 0) return;
         n = cut.y - cut.x + 1;
@@ -47,8 +50,8 @@ k_attend_join(AttnArgs a, AttnPlan pl) {
         int32_t key0;
         n = chunks_of(a, r, pl, &key0);
         row_end = r.q_rows * a.G;
-        if (n == 1 || static_cast<int>(blockIdx.x) * ROWS >= row_end) return;
         grid_dep_wait();
+        if (n == 1 || static_cast<int>(blockIdx.x) * ROWS >= row_end) return;
         base = part_row(a, pl, b, hk, 0, 0);
         step = pl.rows;
     }

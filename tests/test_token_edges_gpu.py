@@ -1,0 +1,49 @@
+"""The token operators where a call is easy to get wrong: host bounds far above
+the lengths on the device, heads that do not fill a step, weights far below the
+largest.  Definitions and bounds: tests/token_ref.py."""
+import pytest
+
+import token_ref as ref
+from test_token_ops_gpu import attend_inputs, within
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+F16, BF16 = torch.float16, torch.bfloat16
+
+
+@pytest.fixture(scope="module")
+def A():
+    if not torch.cuda.is_available():
+        pytest.fail("GPU tests need a CUDA device")
+    from depth_weighted_scatter_gb300 import attention
+
+    return attention
+
+
+# ------------------------------------------------------------------ bounds far above the lengths
+
+@pytest.mark.parametrize("case, most", [
+    # every request's keys lie in one chunk although the bound makes many: few rows, chunked tiles, shared tiles
+    (([1, 1, 1], [60, 5, 33], 8, 2, 128, True, 0, BF16, "same", 16, False), 60000),
+    (([2], [64], 4, 1, 64, True, 0, F16, "e4m3", 64, False), 131072),
+    (([70, 33], [100, 90], 6, 2, 128, True, 0, BF16, "same", 16, True), 30000),
+    (([1100, 1], [128, 0], 8, 8, 64, False, 0, F16, "same", 32, False), 8000),
+], ids=["few", "few_e4m3", "chunked", "shared"])
+def test_attention_is_done_when_the_next_kernel_reads_it(A, case, most):
+    """What comes next in the stream sees the results, call after call."""
+    x = attend_inputs(case, seed=2000)
+    x["max_kv_len"] = most
+    pages = -(-most // case[9])                             # the table has room for the bound; past the lengths there is no page
+    x["block_table"] = torch.nn.functional.pad(x["block_table"], (0, pages - x["block_table"].shape[1]), value=-1).contiguous()
+    assert A.bevpool_paged_attention_workspace_size(len(case[0]), sum(case[0]), *case[2:5], max(case[0]), most, 0) > 0
+    args = (x.pop("q"), x.pop("k_cache"), x.pop("v_cache"), x.pop("block_table"), x.pop("kv_len"), x.pop("cu_q"))
+    want, _, tol, _, _ = ref.attention(*args, scale=case[4] ** -0.5, **x)
+    out, seen = torch.empty_like(args[0]), []
+    for _ in range(200):
+        out.fill_(float("nan"))
+        A.paged_attention(*args, out=out, **x)
+        seen.append(out.clone())
+    within(seen[0], want, tol, "out")
+    assert all(torch.equal(s, seen[0]) for s in seen)
