@@ -102,7 +102,9 @@ def _stream_of(stream):
 
 # Each helper takes `stream` (a torch stream or a cudaStream_t; None: torch's
 # current one).  Another stream is made torch's current stream for the call, so
-# that what the helper allocates belongs to the stream that uses it.
+# that what the helper allocates belongs to the stream that uses it.  A
+# `workspace` is a contiguous tensor on the current device, 256-byte aligned, of
+# the bytes that the C entry point's ..._workspace_size names, or more.
 
 def qk_norm_rope(q, k, positions, inv_freq, *, sections=None, q_weight=None, k_weight=None, eps: float = 1e-6,
                  interleaved: bool = False, q_out=None, k_out=None, stream=None):
@@ -150,7 +152,7 @@ def paged_attention(q, k_cache, v_cache, block_table, kv_len, cu_q, *, max_q_len
     what `out` held."""
     if stream is not None:
         with _stream_of(stream):
-            return _ops.paged_attention(q, k_cache, v_cache, block_table, kv_len, cu_q, max_q_len, max_kv_len, scale, causal,
-                                        window, k_scale, v_scale, out, return_lse, workspace)
-    return _ops.paged_attention(q, k_cache, v_cache, block_table, kv_len, cu_q, max_q_len, max_kv_len, scale, causal, window,
-                                k_scale, v_scale, out, return_lse, workspace)
+            return _ops.paged_attention(q, workspace, k_cache, v_cache, block_table, kv_len, cu_q, max_q_len, max_kv_len, scale,
+                                        causal, window, k_scale, v_scale, out, return_lse)
+    return _ops.paged_attention(q, workspace, k_cache, v_cache, block_table, kv_len, cu_q, max_q_len, max_kv_len, scale, causal,
+                                window, k_scale, v_scale, out, return_lse)

@@ -119,6 +119,15 @@ at::Tensor fresh(at::IntArrayRef sizes, at::ScalarType type, const c10::Device &
     return at::empty(sizes, at::TensorOptions().dtype(type).device(device));
 }
 
+// A caller's workspace (undefined: none): the kernels write all of its bytes, so
+// it has to own them, where they run.
+void workspace_ok(const at::Tensor &ws) {
+    if (!ws.defined()) return;
+    if (!ws.is_contiguous()) refuse("workspace: a contiguous tensor is wanted");
+    if (!ws.is_cuda() || ws.device().index() != c10::cuda::current_device())
+        refuse("workspace: a tensor on the current CUDA device is wanted");
+}
+
 struct Positions {
     const int32_t *p;
     int32_t axes, sections[4], rotary_dim, interleaved;
@@ -233,6 +242,7 @@ PyObject *qk_norm_rope_backward(Args a) {
     const at::Tensor gq = a.tensor("dq_out"), gk = a.tensor("dk_out"), q = a.tensor("q"), k = a.tensor("k"),
                      qw = a.maybe("q_weight"), kw = a.maybe("k_weight");
     at::Tensor dq = a.maybe("dq"), dk = a.maybe("dk"), ws = a.maybe("workspace"), dqw, dkw;
+    workspace_ok(ws);
     const float eps = a.f32();
     const Like l = like("q", q);
     const Rows qr = rows("q", q, l, l.H), kr = rows("k", k, l, -1);
@@ -287,9 +297,11 @@ PyObject *kv_append(Args a) {
     return THPVariable_Wrap(qo);
 }
 
-// q, k_cache.., max_q_len, max_kv_len, scale (None: head_dim ** -0.5), causal, window, k_scale, v_scale, out, lse?, workspace
+// q, workspace, k_cache.., max_q_len, max_kv_len, scale (None: head_dim ** -0.5), causal, window, k_scale, v_scale, out, lse?
 PyObject *paged_attention(Args a) {
     const at::Tensor q = a.tensor("q");
+    at::Tensor ws = a.maybe("workspace");
+    workspace_ok(ws);
     const Like l = like("q", q);
     const Rows qr = rows("q", q, l, l.H);
     const Cache c = cache(a, l, -1);
@@ -305,7 +317,6 @@ PyObject *paged_attention(Args a) {
     const float ks = a.f32(), vs = a.f32();
     at::Tensor out = a.maybe("out"), lse;
     const bool want_lse = a.flag();
-    at::Tensor ws = a.maybe("workspace");
     if (!out.defined()) out = fresh(q.sizes(), l.type, l.device);
     const Rows o = rows("out", out, l, l.H);
     if (want_lse) lse = fresh({l.T, l.H}, at::kFloat, l.device);

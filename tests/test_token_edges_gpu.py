@@ -47,3 +47,29 @@ def test_attention_is_done_when_the_next_kernel_reads_it(A, case, most):
         seen.append(out.clone())
     within(seen[0], want, tol, "out")
     assert all(torch.equal(s, seen[0]) for s in seen)
+
+
+# ------------------------------------------------------------------ the caller's workspace
+
+def test_workspace_of_the_caller(A):
+    """One of the size that is named serves; views that do not own their bytes, and other devices, are refused."""
+    from depth_weighted_scatter_gb300.bevpool import BevpoolError
+
+    x = attend_inputs(([1], [3000], 8, 2, 128, True, 0, BF16, "same", 16, False), seed=2100)
+    args = (x.pop("q"), x.pop("k_cache"), x.pop("v_cache"), x.pop("block_table"), x.pop("kv_len"), x.pop("cu_q"))
+    size = A.bevpool_paged_attention_workspace_size(1, 1, 8, 2, 128, 1, 3000, 0)
+    own = torch.empty(size, dtype=torch.uint8, device="cuda")
+    assert torch.equal(A.paged_attention(*args, workspace=own, **x), A.paged_attention(*args, **x))
+    q, pos = args[0].expand(5, 8, 128), torch.arange(5, dtype=torch.int32, device="cuda")
+    f, w = torch.ones(64, device="cuda"), torch.ones(128, device="cuda")
+    need = A.bevpool_qk_norm_rope_backward_workspace_size(5, 8, 8, 128)
+    own = torch.empty(need, dtype=torch.uint8, device="cuda")
+    got = A.qk_norm_rope_backward(q, q, q, q, pos, f, q_weight=w, workspace=own)
+    want = A.qk_norm_rope_backward(q, q, q, q, pos, f, q_weight=w)
+    assert all(torch.equal(a, b) for a, b in zip(got[:3], want))
+    wide = torch.empty(2, size, dtype=torch.uint8, device="cuda")
+    for bad in (torch.empty(size, dtype=torch.uint8), wide[:1, :1].expand(1, size), wide[:, :size // 2], own[:1].expand(need)):
+        with pytest.raises(BevpoolError, match="workspace"):
+            A.paged_attention(*args, workspace=bad, **x)
+        with pytest.raises(BevpoolError, match="workspace"):
+            A.qk_norm_rope_backward(q, q, q, q, pos, f, q_weight=w, workspace=bad)
