@@ -162,7 +162,9 @@ k_norm_rope_back(NormRopeBackArgs a, int split) {
                         sq += __shfl_xor_sync(0xffffffffu, sq, k);
                         dot += __shfl_xor_sync(0xffffffffu, dot, k);
                     }
-                    const float rs = rsqrtf(fmaf(sq, inv_d, f.eps));
+                    // a lane without a row has read zeros: with eps = 0 their
+                    // rsqrt is infinite, and 0 * inf would reach the sums
+                    const float rs = rows > 0 ? rsqrtf(fmaf(sq, inv_d, f.eps)) : 0.0f;
                     const float c = -dot * inv_d * rs * rs;
                     const uint64_t r2 = pair(rs, rs), c2 = pair(c, c);
 #pragma unroll

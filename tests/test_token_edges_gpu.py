@@ -4,7 +4,7 @@ largest.  Definitions and bounds: tests/token_ref.py."""
 import pytest
 
 import token_ref as ref
-from test_token_ops_gpu import attend_inputs, within
+from test_token_ops_gpu import attend_inputs, norm_rope_inputs, rand, within
 
 pytestmark = pytest.mark.gpu
 
@@ -73,3 +73,35 @@ def test_workspace_of_the_caller(A):
             A.paged_attention(*args, workspace=bad, **x)
         with pytest.raises(BevpoolError, match="workspace"):
             A.qk_norm_rope_backward(q, q, q, q, pos, f, q_weight=w, workspace=bad)
+
+
+# ------------------------------------------------------------------ heads that do not fill a step
+
+@pytest.mark.parametrize("eps", [0.0, 1e-30])
+@pytest.mark.parametrize("case", [
+    # T, Hq, Hk, D, R, axes, interleaved, dtype: a step holds 32 / (lanes of a row) heads
+    (5, 3, 1, 128, 128, 1, False, BF16),
+    (700, 7, 1, 128, 96, 2, True, F16),
+    (5, 7, 2, 64, 64, 3, True, F16),
+    (3000, 5, 1, 64, 32, 1, False, BF16),
+    (9, 9, 3, 32, 32, 1, False, F16),
+    (9, 4, 2, 80, 80, 1, True, BF16),                       # heads fill the steps, lanes the rows do not
+    (4, 3, 1, 256, 256, 1, False, F16),
+], ids=str)
+def test_norm_rope_backward_without_eps(A, case, eps):
+    """Places of a step without a head add nothing to the weights' gradients: no real row is zero, so eps = 0 is as
+    good as any."""
+    T, Hq, Hk, D, R, axes, il, dtype = case
+    x = norm_rope_inputs(case, seed=70)
+    x["eps"] = eps
+    dy = dict(q=rand(71, T, Hq, D, dtype=dtype), k=rand(72, T, Hk, D, dtype=dtype))
+    args = {k: v for k, v in x.items() if k not in ("q", "k", "positions", "inv_freq")}
+    got = A.qk_norm_rope_backward(dy["q"], dy["k"], x["q"], x["k"], x["positions"], x["inv_freq"], **args)
+    out = A.qk_norm_rope(x["q"], x["k"], x["positions"], x["inv_freq"], **args)
+    cos, sin = ref.cos_sin(x["positions"], x["inv_freq"], x["sections"])
+    for i, name in enumerate("qk"):
+        want, mag = ref.norm_rope(x[name], x[name + "_weight"], cos, sin, il, eps)
+        within(out[i], want, ref.U[dtype] * want.abs() + 2.0 ** -18 * mag + ref.tiny(dtype), name)
+        dx, mag, dw, dw_mag = ref.norm_rope_back(dy[name], x[name], x[name + "_weight"], cos, sin, il, eps)
+        within(got[i], dx, ref.U[dtype] * dx.abs() + 2.0 ** -16 * mag + ref.tiny(dtype), "d" + name)
+        within(got[2 + i], dw, 2.0 ** -16 * dw_mag, "d" + name + "_weight")
