@@ -4,7 +4,7 @@ largest.  Definitions and bounds: tests/token_ref.py."""
 import pytest
 
 import token_ref as ref
-from test_token_ops_gpu import attend_inputs, norm_rope_inputs, rand, within
+from test_token_ops_gpu import attend, attend_inputs, norm_rope_inputs, rand, within
 
 pytestmark = pytest.mark.gpu
 
@@ -105,3 +105,88 @@ def test_norm_rope_backward_without_eps(A, case, eps):
         dx, mag, dw, dw_mag = ref.norm_rope_back(dy[name], x[name], x[name + "_weight"], cos, sin, il, eps)
         within(got[i], dx, ref.U[dtype] * dx.abs() + 2.0 ** -16 * mag + ref.tiny(dtype), "d" + name)
         within(got[2 + i], dw, 2.0 ** -16 * dw_mag, "d" + name + "_weight")
+
+
+# ------------------------------------------------------------------ weights far below the largest
+
+def check_rows(x, out, lse, b, i, h):
+    """Token i of request b, the query heads of key head h, in FP64 on the GPU (no holes in the table).  The bound is
+    token_ref's but for three terms.  fp16 weights carry a factor of 2^7 at least: what subnormal ones lose is 2^-25 of
+    2^7 times the largest, 2^-32 of it each.  The sums of n keys are FP32 chains of n / 64 + 16 additions, and products of
+    16 keys added up n / 16 times, possibly with truncation: (n / 16) * 2^-23 and 2^-18 cover both."""
+    cu, kv_len, page, D = x["cu_q"].tolist(), x["kv_len"].tolist(), x["k_cache"].shape[2], x["q"].shape[2]
+    G, dtype = x["q"].shape[1] // x["k_cache"].shape[1], x["q"].dtype
+    n, m = cu[b + 1] - cu[b], kv_len[b]
+    pos = m - n + i
+    hi, lo = (pos + 1 if x["causal"] else m), (max(0, pos - x["window"] + 1) if x["window"] else 0)
+    pg = x["block_table"][b, :-(-m // page)].long()
+
+    def keys(c, scale):
+        c = c.view(torch.uint8)[pg, h].view(c.dtype) if c.element_size() == 1 else c[pg, h]
+        return c.float().reshape(-1, D)[lo:hi].double() * scale
+
+    k, v = keys(x["k_cache"], x.get("k_scale", 1.0)), keys(x["v_cache"], x.get("v_scale", 1.0))
+    rows = slice(h * G, (h + 1) * G)
+    q = x["q"][cu[b] + i, rows].double()
+    scale = x.get("scale", D ** -0.5)
+    z = q @ k.T * scale
+    d = (D + 8) * 2.0 ** -23 * scale * (q.abs() @ k.abs().T).max(-1).values
+    want = torch.logsumexp(z, -1)
+    p = torch.exp(z - want[:, None])
+    o, mag = p @ v, p @ v.abs()
+    sub = 2.0 ** -32 * v.abs().sum(0)[None] * p.max(-1, keepdim=True).values if dtype == F16 else 0.0
+    sums = (hi - lo) / 16 * 2.0 ** -23 + 2.0 ** -18
+    u = ref.U[dtype]
+    within(out[cu[b] + i, rows], o.cpu(), ((u + 2 * d[:, None] + sums) * mag + sub + u * o.abs() + ref.tiny(dtype)).cpu(),
+           f"out {b} {i} {h}")
+    within(lse[cu[b] + i, rows], want.cpu(), (d + sums + 2.0 ** -22 * want.abs()).cpu(), f"lse {b} {i} {h}")
+
+
+@pytest.mark.parametrize("tail", ["alike", "spread"])
+@pytest.mark.parametrize("case", [
+    # q_len, kv_len, Hq, Hk, D, causal, window, dtype, cache, page, token_major
+    ([1], [20000], 4, 1, 64, True, 0, F16, "same", 16, False),          # few rows
+    ([2, 1], [20000, 9000], 4, 2, 128, True, 0, F16, "e4m3", 64, False),
+    ([600] * 8, [5000] * 8, 16, 8, 64, True, 0, F16, "same", 32, False),       # tiles
+    ([1300] * 2, [4000] * 2, 16, 16, 128, True, 0, F16, "same", 64, False),
+    ([70], [20000], 4, 1, 64, True, 0, F16, "same", 16, False),         # chunked
+    ([70], [20000], 4, 1, 128, False, 0, F16, "e4m3", 64, False),
+    ([2100, 10], [5000, 4900], 10, 10, 64, True, 0, F16, "e4m3", 64, False),   # shared
+    ([1100] * 2, [6000] * 2, 10, 10, 128, False, 0, F16, "same", 64, False),
+], ids=[str(i) for i in range(8)])
+def test_attention_weights_far_below_the_largest(A, case, tail):
+    """The first key takes nearly all of a row's weight and its value is zero: the result is what the others add up to.
+    They weigh about 2^-21 each, all alike, or about 2^-26, spread."""
+    x = attend_inputs(case, seed=2200)
+    kv_len, page, e4m3 = case[1], case[9], case[8] == "e4m3"
+    x["scale"] = 0.125
+    x["q"][..., 0] = 4.0                                    # a key's first element says what it weighs
+    ks, vs = (1 / 12.0, 1 / 32.0) if e4m3 else (1.0, 1.0)
+    if e4m3:
+        x.update(k_scale=ks, v_scale=vs)
+    heights = dict(alike=28.84, spread=36.0)[tail] / ks
+
+    def put(name, fn):
+        c = x[name].float()
+        fn(c)
+        x[name].copy_(c.to(x[name].dtype))
+
+    def keys(c):
+        c.mul_(0.0 if tail == "alike" else 0.3)
+        c[..., 0] = 0.0
+        for b in range(len(kv_len)):
+            c[int(x["block_table"][b, 0]), :, 0] = 0.0
+            c[int(x["block_table"][b, 0]), :, 0, 0] = heights
+
+    def values(c):
+        c.abs_().mul_(0.25).add_(6.0 / vs)
+        for b in range(len(kv_len)):
+            c[int(x["block_table"][b, 0]), :, 0] = 0.0
+
+    put("k_cache", keys)
+    put("v_cache", values)
+    out, lse = attend(A, x)
+    for b, n in enumerate(case[0]):
+        for i in sorted({0, n // 3, n - 1}):
+            check_rows(x, out, lse, b, i, (i + b) % case[3])
+    assert out[:case[0][0]].abs().amax(-1).amin() > 2.0 ** -13          # sums that fp16 holds to all of its bits
