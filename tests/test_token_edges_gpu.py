@@ -1,10 +1,11 @@
 """The token operators where a call is easy to get wrong: host bounds far above
 the lengths on the device, heads that do not fill a step, weights far below the
 largest.  Definitions and bounds: tests/token_ref.py."""
+import numpy as np
 import pytest
 
 import token_ref as ref
-from test_token_ops_gpu import attend, attend_inputs, norm_rope_inputs, rand, within
+from test_token_ops_gpu import MANY, attend, attend_inputs, norm_rope_inputs, poison, rand, within
 
 pytestmark = pytest.mark.gpu
 
@@ -190,3 +191,17 @@ def test_attention_weights_far_below_the_largest(A, case, tail):
         for i in sorted({0, n // 3, n - 1}):
             check_rows(x, out, lse, b, i, (i + b) % case[3])
     assert out[:case[0][0]].abs().amax(-1).amin() > 2.0 ** -13          # sums that fp16 holds to all of its bits
+
+
+@pytest.mark.parametrize("case", MANY, ids=[str(i) for i in range(len(MANY))])
+def test_attention_many_tiles_small_contributions(A, case):
+    """The largest calls held to what their own weights can lose: an allowance for subnormal fp16 weights is of the
+    largest weight, which is a small part of a sum over thousands of keys."""
+    x = attend_inputs(case, seed=2300)
+    poison(x)
+    out, lse = attend(A, x)
+    rng = np.random.default_rng(11)
+    for b, n in enumerate(case[0]):
+        for i in sorted({0, n - 1, *rng.integers(0, n, 3).tolist()}):
+            for h in {0, int(rng.integers(0, case[3]))}:
+                check_rows(x, out, lse, b, i, h)
