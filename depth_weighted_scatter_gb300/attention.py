@@ -105,6 +105,10 @@ def _stream_of(stream):
 # that what the helper allocates belongs to the stream that uses it.  A
 # `workspace` is a contiguous tensor on the current device, 256-byte aligned, of
 # the bytes that the C entry point's ..._workspace_size names, or more.
+#
+# The helpers do not take part in autograd: a tensor that requires gradients (with
+# grad mode on) or carries a forward-mode tangent is refused.  Training calls
+# qk_norm_rope_backward.
 
 def qk_norm_rope(q, k, positions, inv_freq, *, sections=None, q_weight=None, k_weight=None, eps: float = 1e-6,
                  interleaved: bool = False, q_out=None, k_out=None, stream=None):

@@ -8,6 +8,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
+#include <ATen/core/grad_mode.h>
 #include <ATen/ops/empty.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
@@ -40,13 +41,13 @@ public:
     at::Tensor tensor(const char *name) {
         PyObject *o = next();
         if (!THPVariable_Check(o)) refuse(std::string(name) + ": a tensor is wanted");
-        return THPVariable_Unpack(o);
+        return plain(name, THPVariable_Unpack(o));
     }
     at::Tensor maybe(const char *name) {   // None: undefined
         PyObject *o = next();
         if (o == Py_None) return at::Tensor();
         if (!THPVariable_Check(o)) refuse(std::string(name) + ": a tensor or None is wanted");
-        return THPVariable_Unpack(o);
+        return plain(name, THPVariable_Unpack(o));
     }
     int32_t i32(const char *name) {
         const long long v = PyLong_AsLongLong(next());
@@ -66,6 +67,15 @@ public:
     }
 
 private:
+    // The helpers record no gradients, so a tensor that would lose its own is refused.
+    const at::Tensor &plain(const char *name, const at::Tensor &t) const {
+        if ((grad_ && t.requires_grad()) || t._fw_grad(0).defined())
+            refuse(std::string(name) + ": gradients are not recorded through this call; make it under torch.no_grad() or on "
+                                       "detached tensors (qk_norm_rope_backward computes those of qk_norm_rope)");
+        return t;
+    }
+
+    const bool grad_ = at::GradMode::is_enabled();
     PyObject *const *a_;
     Py_ssize_t i_ = 0;
 };

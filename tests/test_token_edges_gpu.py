@@ -205,3 +205,30 @@ def test_attention_many_tiles_small_contributions(A, case):
         for i in sorted({0, n - 1, *rng.integers(0, n, 3).tolist()}):
             for h in {0, int(rng.integers(0, case[3]))}:
                 check_rows(x, out, lse, b, i, h)
+
+
+# ------------------------------------------------------------------ tensors that require gradients
+
+def test_gradients_are_not_dropped(A):
+    """With grad mode on a tensor that requires gradients is refused, whatever its place; without, it is taken."""
+    from depth_weighted_scatter_gb300.bevpool import BevpoolError
+
+    q, k = rand(1, 3, 4, 64, dtype=F16), rand(2, 3, 2, 64, dtype=F16)
+    pos, f, w = torch.arange(3, dtype=torch.int32, device="cuda"), torch.ones(32, device="cuda"), torch.ones(64, device="cuda")
+    c = rand(3, 4, 2, 16, 64, dtype=F16)
+    table, n = torch.zeros(1, 1, dtype=torch.int32, device="cuda"), torch.full((1,), 3, dtype=torch.int32, device="cuda")
+    cu = torch.tensor([0, 3], dtype=torch.int32, device="cuda")
+    want = A.qk_norm_rope(q, k, pos, f, q_weight=w)
+    at = dict(max_q_len=3, max_kv_len=3)
+    attended = A.paged_attention(q, c, c, table, n, cu, **at)
+    for name, args in (("q", (q.clone().requires_grad_(), k, pos, f)), ("inv_freq", (q, k, pos, f.clone().requires_grad_()))):
+        with pytest.raises(BevpoolError, match=name + ": gradients"):
+            A.qk_norm_rope(*args, q_weight=w)
+        with torch.no_grad():
+            got = A.qk_norm_rope(*args, q_weight=w)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]) and not got[0].requires_grad
+    g = c.clone().requires_grad_()
+    with pytest.raises(BevpoolError, match="v_cache: gradients"):
+        A.paged_attention(q, c, g, table, n, cu, **at)
+    with torch.no_grad():
+        assert torch.equal(A.paged_attention(q, c, g, table, n, cu, **at), attended)
