@@ -7,8 +7,8 @@
 // slice of its rows when there are few tokens, and finds the token's request
 // with one 32-wide search of cu_q.
 //
-// Measured on a GB300: 65536 tokens of 8 + 8 + 8 heads of 64, fp16 to E4M3: 63 us
-// (3.9 TB/s of 6.7 measured copy; 69 % of the issue slots, as a token has but six
+// Measured on a GB300: 65536 tokens of 8 + 8 + 8 heads of 64, fp16 to E4M3: 65 us
+// (3.8 TB/s of 6.7 measured copy; 69 % of the issue slots, as a token has but six
 // steps to share its angles and its place); 64 single tokens of 32 + 8 + 8 heads
 // of 128, bf16: 8.2 us a call, bound by the launch.
 #include "rotary.cuh"
@@ -39,6 +39,14 @@ __device__ __forceinline__ int64_t slot_of(const PagedArgs &pg, int64_t t, int l
     const int32_t page = pg.block_table[static_cast<int64_t>(b) * pg.table_pages + (place >> pg.page_shift)];
     if (page < 0 || page >= pg.n_pages) return -1;
     return page * pg.page_stride + (place & (pg.page_size - 1)) * pg.slot_stride;
+}
+
+// x / scale of two values, rounded once but for 2^-46 of it.  (Times the rounded
+// inverse an exact value halfway between two codes goes the wrong way for some
+// scales: half of them for 63 / 4096.  The second product costs 65536 tokens of 24 heads
+// of 64 1.4 us of 65.)
+__device__ __forceinline__ uint64_t quotient(uint64_t x, const AppendArgs::Inverse &inv) {
+    return fma2(x, pair(inv.hi, inv.hi), mul2(x, pair(inv.lo, inv.lo)));
 }
 
 constexpr int kAppendDepth = 8;                        // steps in flight a warp
@@ -90,7 +98,7 @@ k_kv_append(AppendArgs g, int split) {
             }
             const bool norm = (part == 0 ? f.q_weight : f.k_weight) != nullptr;
             const int H = part == 0 ? f.Hq : f.Hk;
-            const float inv = part == 1 ? g.k_inv : g.v_inv;
+            const AppendArgs::Inverse &inv = part == 1 ? g.k_inv : g.v_inv;
             const int h = (first - begin) * Stream::RPS + rg;
             // steps in which this lane has a row to keep
             int rows_left = p.live && (part == 0 || slot >= 0) ? (H - h + Stream::RPS - 1) / Stream::RPS : 0;
@@ -109,7 +117,7 @@ k_kv_append(AppendArgs g, int split) {
                 }
                 if (E4M3 && part > 0) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) y[i] = mul2(y[i], pair(inv, inv));
+                    for (int i = 0; i < 4; ++i) y[i] = quotient(y[i], inv);
                 }
                 if (rows_left-- > 0) {
                     if (E4M3 && part > 0)

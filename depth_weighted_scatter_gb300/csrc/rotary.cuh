@@ -77,7 +77,9 @@ struct AppendArgs {
     int cache_e4m3;
     void *k_cache, *v_cache;
     PagedArgs pg;
-    float k_inv, v_inv;           // 1 / scale
+    struct Inverse {              // 1 / scale, in two parts of one sign
+        float hi, lo;
+    } k_inv, v_inv;
 };
 cudaError_t launch_kv_append(const AppendArgs &a);
 

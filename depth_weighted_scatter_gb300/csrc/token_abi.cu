@@ -60,6 +60,16 @@ bool weight_ok(const float *w) { return aligned(w, 4); }
 
 bool scale_ok(float s) { return std::isfinite(s) && s > 0.0f && std::isfinite(1.0f / s); }
 
+// 1 / s as hi + lo, s > 0.  hi is rounded towards zero and lo is never zero (2^-60 of
+// hi where hi is exact), so that an infinite value times either has its sign.
+AppendArgs::Inverse inverse(float s) {
+    const double inv = 1.0 / static_cast<double>(s);
+    float hi = static_cast<float>(inv);
+    if (hi > inv) hi = std::nextafter(hi, 0.0f);
+    const float lo = static_cast<float>(std::fmax(inv - hi, hi * 0x1p-60));
+    return {hi, std::fmax(lo, 0x1p-149f)};
+}
+
 // The cache arguments, into *g.  eb: bytes of an element.
 bevpool_status cache_ok(const void *k_cache, const void *v_cache, int64_t page_stride, int64_t slot_stride,
                         int64_t head_stride, int32_t n_pages, int32_t page_size, const int32_t *block_table,
@@ -234,8 +244,10 @@ bevpool_status bevpool_kv_append(
     g.cache_e4m3 = e4m3;
     g.k_cache = k_cache;
     g.v_cache = v_cache;
-    g.k_inv = 1.0f / k_scale;
-    g.v_inv = 1.0f / v_scale;
+    if (e4m3) {
+        g.k_inv = inverse(k_scale);
+        g.v_inv = inverse(v_scale);
+    }
     return cuda_status(launch_kv_append(g));
 }
 

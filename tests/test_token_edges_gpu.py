@@ -5,7 +5,7 @@ import numpy as np
 import pytest
 
 import token_ref as ref
-from test_token_ops_gpu import MANY, attend, attend_inputs, norm_rope_inputs, poison, rand, within
+from test_token_ops_gpu import MANY, attend, attend_inputs, cu_of, freqs, i32, make_pages, norm_rope_inputs, poison, rand, within
 
 pytestmark = pytest.mark.gpu
 
@@ -232,3 +232,44 @@ def test_gradients_are_not_dropped(A):
         A.paged_attention(q, c, g, table, n, cu, **at)
     with torch.no_grad():
         assert torch.equal(A.paged_attention(q, c, g, table, n, cu, **at), attended)
+
+
+# ------------------------------------------------------------------ E4M3 codes of exact values
+
+def e4m3_of(x):
+    """Codes' values of FP64 numbers: nearest, even where halfway, saturating; from the format's definition."""
+    a = x.abs().clamp(max=448.0)
+    step = torch.exp2(torch.floor(torch.log2(a.clamp(min=2.0 ** -6))) - 3)              # of the code's binade
+    return torch.copysign(torch.round(a / step) * step, x)                              # torch.round: halves to even
+
+
+@pytest.mark.parametrize("k_scale, v_scale", [(63 / 4096, 7 / 4096), (15 / 4096, 61 / 4096), (1 / 64, 2.0), (3e-3, 0.1)])
+@pytest.mark.parametrize("il, D, R", [(False, 64, 64), (True, 128, 128), (False, 80, 64)])
+def test_append_e4m3_rounds_the_quotient(A, k_scale, v_scale, il, D, R):
+    """Keys without norm at position 0 and values are exact, so their codes are those of value / scale, rounded once: a
+    value halfway between two codes goes to the even one."""
+    T, page = 64, 32
+    halves = torch.tensor([(1 + (2 * i + 1) / 16) * 2.0 ** e for i in range(8) for e in range(-6, 8)], dtype=torch.float64)
+    kc, vc, table = make_pages(1, [T], page, 2, D, F16, "e4m3")
+    x = []
+    for seed, scale in ((1, k_scale), (2, v_scale)):
+        s = float(torch.tensor(scale, dtype=torch.float32))
+        v = rand(seed, T, 2, D, dtype=F16).double().cpu()
+        exact = torch.where(torch.rand(T, 2, D, generator=torch.Generator().manual_seed(seed)) < 0.8,
+                            (halves * s)[torch.randint(0, len(halves), (T, 2, D), generator=torch.Generator().manual_seed(seed))], v)
+        h = exact.half()
+        h[0, 0, :4] = torch.tensor([float("inf"), -float("inf"), 65504.0, -0.0], dtype=F16)
+        x.append(h.cuda())
+    A.kv_append(*x, kc, vc, table, i32([T]), cu_of([T]), torch.zeros(T, dtype=torch.int32, device="cuda"), freqs(R),
+                interleaved=il, k_scale=k_scale, v_scale=v_scale)
+    pg = table[0].long().cpu()
+    ties = 0
+    for name, got, h, scale in (("k", kc, x[0], k_scale), ("v", vc, x[1], v_scale)):
+        q = h.float().cpu() / torch.tensor(scale, dtype=torch.float32)                  # one rounding
+        want = e4m3_of(q.double())
+        got = got.float().cpu()[pg].transpose(1, 2).reshape(-1, 2, D)[:T].double()
+        if name == "k":                                     # an infinity's partner: inf * 0
+            want, got = want[1:], got[1:]
+        assert torch.equal(got, want), name
+        ties += int(torch.isin(q.double(), halves).sum())
+    assert ties > 0 or k_scale == 3e-3
