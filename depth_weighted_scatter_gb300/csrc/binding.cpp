@@ -188,7 +188,9 @@ struct Cache {
 Cache cache(Args &a, const Like &l, int64_t heads) {
     const at::Tensor k = a.tensor("k_cache"), v = a.tensor("v_cache"), t = a.tensor("block_table"), n = a.tensor("kv_len"),
                      cu = a.tensor("cu_q");
-    if (k.dim() != 4 || k.sizes() != v.sizes() || k.strides() != v.strides() || k.scalar_type() != v.scalar_type())
+    bool alike = k.dim() == 4 && k.sizes() == v.sizes() && k.scalar_type() == v.scalar_type();
+    for (int64_t i = 0; alike && i < 4; ++i) alike = k.size(i) == 1 || k.stride(i) == v.stride(i);
+    if (!alike)
         refuse("caches: two [n_pages, n_k_heads, page_size, head_dim] tensors of one type and layout are wanted");
     Cache c;
     switch (k.scalar_type()) {

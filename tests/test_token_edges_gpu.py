@@ -273,3 +273,26 @@ def test_append_e4m3_rounds_the_quotient(A, k_scale, v_scale, il, D, R):
         assert torch.equal(got, want), name
         ties += int(torch.isin(q.double(), halves).sum())
     assert ties > 0 or k_scale == 3e-3
+
+
+# ------------------------------------------------------------------ caches of one page or one head
+
+@pytest.mark.parametrize("n_pages, Hk, q_len", [(1, 1, 3), (1, 2, 40), (5, 1, 3), (5, 1, 40)])
+def test_caches_that_differ_in_the_stride_of_an_axis_of_one_entry(A, n_pages, Hk, q_len):
+    """Two caches lie alike where they do along every axis of more than one entry."""
+    page, D, n = 64, 64, 60 if n_pages == 1 else 300
+    kc, vc = rand(1, n_pages, Hk, page, D, dtype=F16), rand(2, n_pages, Hk, page, D, dtype=F16)
+    strides = (vc.stride(0) if n_pages > 1 else 8, vc.stride(1) if Hk > 1 else 40, D, 1)
+    v2 = vc.as_strided(vc.shape, strides)                   # the same elements
+    assert torch.equal(v2, vc) and v2.stride() != kc.stride()
+    q, k = rand(3, q_len, 2 * Hk, D, dtype=F16), rand(4, q_len, Hk, D, dtype=F16)
+    table = torch.arange(n_pages, dtype=torch.int32, device="cuda")[None]
+    at = (table, i32([n]), cu_of([q_len]))
+    want = A.paged_attention(q, kc, vc, *at, max_q_len=q_len, max_kv_len=n)
+    assert torch.equal(A.paged_attention(q, kc, v2, *at, max_q_len=q_len, max_kv_len=n), want)
+    assert torch.equal(A.paged_attention(q, kc.as_strided(kc.shape, strides), vc, *at, max_q_len=q_len, max_kv_len=n), want)
+    pos = torch.arange(q_len, dtype=torch.int32, device="cuda")
+    k1, v1 = kc.clone(), vc.clone()
+    A.kv_append(k, k, k1, v1, *at, pos, freqs(D))
+    A.kv_append(k, k, kc, v2, *at, pos, freqs(D))
+    assert torch.equal(kc, k1) and torch.equal(vc, v1)
