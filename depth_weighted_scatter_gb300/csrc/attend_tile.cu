@@ -1037,7 +1037,8 @@ bool cache_map(const AttnArgs &a, const void *cache, bool columns, CUtensorMap *
 
 cudaError_t attention_timeouts(int64_t *count) {
     unsigned long long n = 0;
-    const cudaError_t e = cudaMemcpyFromSymbol(&n, g_attention_timeouts, sizeof(n));
+    cudaError_t e = cudaDeviceSynchronize();               // a copy alone leaves out streams that do not wait for the default one
+    if (e == cudaSuccess) e = cudaMemcpyFromSymbol(&n, g_attention_timeouts, sizeof(n));
     if (e == cudaSuccess) *count = static_cast<int64_t>(n);
     return e;
 }

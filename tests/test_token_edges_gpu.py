@@ -296,3 +296,19 @@ def test_caches_that_differ_in_the_stride_of_an_axis_of_one_entry(A, n_pages, Hk
     A.kv_append(k, k, k1, v1, *at, pos, freqs(D))
     A.kv_append(k, k, kc, v2, *at, pos, freqs(D))
     assert torch.equal(kc, k1) and torch.equal(vc, v1)
+
+
+# ------------------------------------------------------------------ the count of waits that ran out
+
+def test_timeouts_are_counted_to_the_end(A):
+    """The count is that of all work enqueued so far, on streams that do not wait for the default one too."""
+    x = attend_inputs(([300], [700], 4, 2, 128, True, 0, BF16, "same", 16, False), seed=2500)
+    attend(A, x)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(200_000_000)                      # about a tenth of a second
+        attend(A, x)
+    assert not side.query()
+    assert A.bevpool_attention_timeouts() == 0
+    assert side.query()
