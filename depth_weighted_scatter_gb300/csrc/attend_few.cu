@@ -23,10 +23,11 @@
 // of the largest.
 //
 // Measured on a GB300, 32 query and 8 key heads of 128: 64 requests of up to 8192
-// keys, bf16: 234 us (6.5 TB/s, 97 % of measured copy); two requests of up to
-// 131072 keys in E4M3: 93 us (4.5 TB/s, 67 %: the widening keeps the integer units
-// at half their rate); one request of 777 keys, 8 heads of 64: 8.3 us on the GPU,
-// 10 us a call.
+// keys, bf16: 233 us (6.6 TB/s, 98 % of measured copy); two requests of up to
+// 131072 keys in E4M3: 91 us (4.6 TB/s, 68 %: no unit is saturated (ALU 44 %, issue
+// slots 36 %), eight warps an SM do not cover the way from the copies through the
+// conversions to the products); one request of 777 keys, 8 heads of 64: 8.3 us on
+// the GPU, 10 to 12 a call.
 #include "paged_attention.cuh"
 
 namespace bevpool {

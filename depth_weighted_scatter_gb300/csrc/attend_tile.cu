@@ -42,9 +42,9 @@
 // keys, the masked block, O.
 //
 // Measured on a GB300 (2.0 GHz), 32 query and 8 key heads of 128, bf16: a prompt of
-// 8192 tokens 380 us (1445 TFLOP/s of 1900 measured; whole blocks make 1.6 %
-// more products than are counted); six ragged chunks of up to 500 tokens over up to
-// 12000 keys 258 us (1330 TFLOP/s); 2500 tokens of 8 heads of 64 over 12500 keys in
+// 8192 tokens 380 to 400 us (1445 to 1375 TFLOP/s of 1900 measured; whole blocks make
+// 1.6 % more products than are counted); six ragged chunks of up to 500 tokens over up
+// to 12000 keys 258 to 269 us (1330 to 1270 TFLOP/s); 2500 tokens of 8 heads of 64 over 12500 keys in
 // E4M3, two requests: 131 us (654 TFLOP/s; chunks of equal length instead of shares:
 // 158).  Two threads a row gave no gain (they share the exponentials' unit: 471 us
 // for the prompt against 473 at the time), nor did going on with other places of the

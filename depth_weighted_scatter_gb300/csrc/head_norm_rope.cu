@@ -13,10 +13,12 @@
 // a ring of asynchronous copies that runs on over tensors and tokens (plain
 // loads, some in registers ahead, left the memory idle at each token's start:
 // backward 115 us against 86 below).  What is left over the bytes is
-// instructions: about 130 a step of 512 bytes, 60 % of the issue slots.
+// instructions: about 130 a step of 512 bytes, 60 % of the issue slots; and the start of
+// a CTA: the frequencies as turns, in FP64, come before its first copies and hold the
+// FP64 unit for 4600 cycles an SM (forward, heads of 128; backward 3100).
 //
 // Measured on a GB300, q and k of one fused projection: forward of 20001 tokens,
-// 40 heads of 128, bf16: 79 us (5.2 TB/s of 6.7 measured copy); backward of
+// 40 heads of 128, bf16: 80 us (5.2 TB/s of 6.7 measured copy); backward of
 // 32768 tokens, 18 heads of 128, bf16: 86 us in the kernel (5.2 TB/s).
 #include "rotary.cuh"
 
