@@ -14,7 +14,8 @@ Head tensors are [tokens, heads, head_dim], fp16 or bf16, with any token and
 head strides that are multiples of 8 elements (a slice of a fused projection
 is taken as it is).  A cache is [n_pages, n_k_heads, page_size, head_dim] (or
 a permuted view of [n_pages, page_size, n_k_heads, head_dim] memory), of the
-heads' type, or E4M3 codes (torch.float8_e4m3fn or uint8).
+heads' type, or E4M3 codes (torch.float8_e4m3fn or uint8); its strides are
+multiples of 16 bytes, so E4M3 rows start 16 elements apart or a multiple of it.
 """
 from __future__ import annotations
 
