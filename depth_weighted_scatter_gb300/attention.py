@@ -21,7 +21,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
-from typing import Optional
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -51,6 +51,8 @@ _lib.bevpool_paged_attention_workspace_size.restype = _sz
 _lib.bevpool_paged_attention.argtypes = ([_dt, _dt] + _rows + [_vp, _vp] + _pages + [_i32] * 6
                                          + [_f32, _i32, _i32, _f32, _f32] + _rows + [_vp, _vp, _sz, _vp])
 _lib.bevpool_paged_attention.restype = ctypes.c_int
+_lib.bevpool_plan_pages.argtypes = [_vp] * 7 + [_i32] * 5 + [_vp] * 10
+_lib.bevpool_plan_pages.restype = ctypes.c_int
 _lib.bevpool_attention_timeouts.argtypes = [_vp]
 _lib.bevpool_attention_timeouts.restype = ctypes.c_int
 
@@ -81,6 +83,10 @@ def bevpool_paged_attention_workspace_size(n_seqs: int, n_tokens: int, n_q_heads
 
 def bevpool_paged_attention(*args) -> int:
     return _lib.bevpool_paged_attention(*args)
+
+
+def bevpool_plan_pages(*args) -> int:
+    return _lib.bevpool_plan_pages(*args)
 
 
 def bevpool_attention_timeouts() -> int:
@@ -161,3 +167,32 @@ def paged_attention(q, k_cache, v_cache, block_table, kv_len, cu_q, *, max_q_len
                                         causal, window, k_scale, v_scale, out, return_lse)
     return _ops.paged_attention(q, workspace, k_cache, v_cache, block_table, kv_len, cu_q, max_q_len, max_kv_len, scale, causal,
                                 window, k_scale, v_scale, out, return_lse)
+
+
+class PagePlan(NamedTuple):
+    """What plan_pages returns; kv_len, first, block_table, free_pages and n_free are the next call's state."""
+
+    cu_q: torch.Tensor          # int32 [n_seqs + 1]
+    positions: torch.Tensor     # int32 [n_tokens]
+    slots: torch.Tensor         # int64 [n_tokens]
+    kv_len: torch.Tensor        # int32 [n_seqs]
+    first: torch.Tensor         # int32 [n_seqs]
+    block_table: torch.Tensor   # int32 [n_seqs, pages]
+    free_pages: torch.Tensor    # int32 [n_pool]
+    n_free: torch.Tensor        # int32 [1]
+    missing: torch.Tensor       # int32 [1]: 0 unless the batch does not fit
+
+
+def plan_pages(q_len, kv_len, first, block_table, free_pages, n_free, *, page_size: int, n_tokens: int, drop=None,
+               out: Optional[PagePlan] = None, stream=None) -> PagePlan:
+    """bevpool_plan_pages: pages given back and handed out for q_len new tokens a
+    request, on the device: cu_q, kv_len and block_table as kv_append and
+    paged_attention take them, each new token's position and slot.  All tensors
+    int32 (slots int64); n_tokens is a host bound of the new tokens; drop: oldest
+    pages that a request gives back first, negative: it ends.  With missing != 0
+    nothing has changed.  `out`: an earlier plan's tensors to write to, none of
+    which this call reads."""
+    if stream is not None:
+        with _stream_of(stream):
+            return PagePlan._make(_ops.plan_pages(q_len, kv_len, first, drop, block_table, free_pages, n_free, page_size, n_tokens, out))
+    return PagePlan._make(_ops.plan_pages(q_len, kv_len, first, drop, block_table, free_pages, n_free, page_size, n_tokens, out))

@@ -345,6 +345,74 @@ PyObject *paged_attention(Args a) {
     return Py_BuildValue("NN", THPVariable_Wrap(out), THPVariable_Wrap(lse));
 }
 
+// Byte ranges of a call's tensors.
+struct Span {
+    const char *from, *to;
+    Span(const at::Tensor &t) : from(static_cast<const char *>(t.data_ptr())), to(from + t.nbytes()) {}
+    bool meets(const Span &o) const { return from < o.to && o.from < to; }
+};
+
+// q_len, kv_len, first, drop, block_table, free_pages, n_free, page_size, n_tokens, out (None or its nine tensors)
+PyObject *plan_pages(Args a) {
+    const at::Tensor q = a.tensor("q_len"), kv = a.tensor("kv_len"), first = a.tensor("first"), drop = a.maybe("drop"),
+                     table = a.tensor("block_table"), pool = a.tensor("free_pages"), n_free = a.tensor("n_free");
+    const int32_t page = a.i32("page_size"), n_tokens = a.i32("n_tokens");
+    PyObject *given = a.next();
+    if (table.dim() != 2) refuse("block_table: [n_seqs, pages] is wanted");
+    if (!table.is_cuda() || table.device().index() != c10::cuda::current_device())
+        refuse("block_table: tensors must be on the current CUDA device");
+    if (n_tokens < 0) refuse("n_tokens: a count is wanted");
+    const int64_t B = table.size(0), W = table.size(1), P = pool.numel();
+    if (B > INT32_MAX || W > INT32_MAX || P > INT32_MAX) refuse("block_table, free_pages: too large");
+    const c10::Device device = table.device();
+    const auto ints = [&](const char *name, const at::Tensor &t, int64_t n) {
+        return static_cast<const int32_t *>(vector(name, t, n, at::kInt, device));
+    };
+    const int32_t *in[] = {ints("q_len", q, B),           ints("kv_len", kv, B), ints("first", first, B), ints("drop", drop, B),
+                           ints("block_table", table, B * W), ints("free_pages", pool, P), ints("n_free", n_free, 1)};
+    // outputs, in the order of the result
+    constexpr int N = 9, SLOTS = 2;
+    static const char *const names[N] = {"cu_q", "positions", "slots", "kv_len", "first", "block_table", "free_pages", "n_free", "missing"};
+    const int64_t sizes[N] = {B + 1, n_tokens, n_tokens, B, B, B * W, P, 1, 1};
+    at::Tensor out[N];
+    void *p[N];
+    if (given == Py_None) {
+        for (int i = 0; i < N; ++i) {
+            const auto type = i == SLOTS ? at::kLong : at::kInt;
+            out[i] = i == 5 ? fresh({B, W}, type, device) : fresh({sizes[i]}, type, device);
+            p[i] = out[i].data_ptr();
+        }
+    } else {
+        PyObject *seq = PySequence_Fast(given, "out: the tensors of a plan are wanted");
+        if (!seq) throw python_error();
+        const bool fits = PySequence_Fast_GET_SIZE(seq) == N;
+        for (int i = 0; fits && i < N; ++i) {
+            PyObject *o = PySequence_Fast_GET_ITEM(seq, i);
+            if (THPVariable_Check(o)) out[i] = THPVariable_Unpack(o);
+        }
+        Py_DECREF(seq);
+        for (int i = 0; i < N; ++i) {
+            if (!out[i].defined()) refuse("out: the nine tensors of a plan are wanted");
+            p[i] = vector(names[i], out[i], sizes[i], i == SLOTS ? at::kLong : at::kInt, device);
+            const Span x(out[i]);
+            for (int j = 0; j < i; ++j)
+                if (x.meets(out[j])) refuse(std::string("out: ") + names[i] + " and " + names[j] + " overlap");
+            for (const at::Tensor &t : {q, kv, first, drop, table, pool, n_free})
+                if (t.defined() && x.meets(t)) refuse(std::string("out: ") + names[i] + " overlaps an input");
+        }
+        if (out[5].sizes() != table.sizes()) refuse("out: block_table has another shape");
+    }
+    const auto i32 = [&](int i) { return static_cast<int32_t *>(p[i]); };
+    done(bevpool_plan_pages(in[0], in[1], in[2], in[3], in[4], in[5], in[6], static_cast<int32_t>(B), static_cast<int32_t>(W),
+                            static_cast<int32_t>(P), n_tokens, page, i32(0), i32(1), static_cast<int64_t *>(p[2]), i32(3),
+                            i32(4), i32(5), i32(6), i32(7), i32(8), c10::cuda::getCurrentCUDAStream(device.index()).stream()),
+         "bevpool_plan_pages");
+    PyObject *res = PyTuple_New(N);
+    if (!res) throw python_error();
+    for (int i = 0; i < N; ++i) PyTuple_SET_ITEM(res, i, THPVariable_Wrap(out[i]));
+    return res;
+}
+
 // A method of the module: C++ exceptions become Python's.
 template <PyObject *(*Fn)(Args), int N>
 PyObject *method(PyObject *, PyObject *const *args, Py_ssize_t n) {
@@ -378,6 +446,7 @@ PyMethodDef g_methods[] = {entry<qk_norm_rope, 11>("qk_norm_rope"),
                            entry<qk_norm_rope_backward, 14>("qk_norm_rope_backward"),
                            entry<kv_append, 18>("kv_append"),
                            entry<paged_attention, 16>("paged_attention"),
+                           entry<plan_pages, 10>("plan_pages"),
                            {"set_error", set_error, METH_O, nullptr},
                            {nullptr, nullptr, 0, nullptr}};
 

@@ -4,6 +4,7 @@
 #include <cmath>
 
 #include "paged_attention.cuh"
+#include "plan_pages.cuh"
 
 using namespace bevpool;
 
@@ -70,13 +71,21 @@ AppendArgs::Inverse inverse(float s) {
     return {hi, std::fmax(lo, 0x1p-149f)};
 }
 
+bool page_size_ok(int32_t n) { return n >= 16 && n <= 256 && (n & (n - 1)) == 0; }
+
+int32_t page_shift(int32_t page_size) {
+    int32_t s = 0;
+    while ((1 << s) < page_size) ++s;
+    return s;
+}
+
 // The cache arguments, into *g.  eb: bytes of an element.
 bevpool_status cache_ok(const void *k_cache, const void *v_cache, int64_t page_stride, int64_t slot_stride,
                         int64_t head_stride, int32_t n_pages, int32_t page_size, const int32_t *block_table,
                         int32_t table_pages, const int32_t *kv_len, const int32_t *cu_q, int32_t n_seqs, int32_t Hk,
                         int32_t D, int eb, PagedArgs *g) {
     if (page_size < 1 || n_pages < 1 || table_pages < 1 || n_seqs < 0) return BEVPOOL_ERR_INVALID_ARG;
-    if (page_size < 16 || page_size > 256 || (page_size & (page_size - 1)) != 0) return BEVPOOL_ERR_UNSUPPORTED;
+    if (!page_size_ok(page_size)) return BEVPOOL_ERR_UNSUPPORTED;
     const int64_t unit = 16 / eb;
     for (const int64_t s : {page_stride, slot_stride, head_stride})
         if (s < 0 || s >= kMaxStride / 2 || s % unit != 0) return BEVPOOL_ERR_INVALID_ARG;
@@ -92,8 +101,7 @@ bevpool_status cache_ok(const void *k_cache, const void *v_cache, int64_t page_s
     g->head_stride = head_stride;
     g->n_pages = n_pages;
     g->page_size = page_size;
-    g->page_shift = 0;
-    while ((1 << g->page_shift) < page_size) ++g->page_shift;
+    g->page_shift = page_shift(page_size);
     g->table_pages = table_pages;
     g->n_seqs = n_seqs;
     g->block_table = block_table;
@@ -200,6 +208,29 @@ bevpool_status bevpool_qk_norm_rope_backward(
     a.dk_weight = dk_weight;
     a.partial = static_cast<float *>(workspace);
     return cuda_status(launch_norm_rope_back(a));
+}
+
+bevpool_status bevpool_plan_pages(
+    const int32_t *q_len, const int32_t *kv_len, const int32_t *first, const int32_t *drop, const int32_t *block_table,
+    const int32_t *free_pages, const int32_t *n_free, int32_t n_seqs, int32_t table_pages, int32_t n_pool,
+    int32_t n_tokens, int32_t page_size, int32_t *cu_q, int32_t *positions, int64_t *slots, int32_t *kv_len_out,
+    int32_t *first_out, int32_t *block_table_out, int32_t *free_out, int32_t *n_free_out, int32_t *missing,
+    void *stream) {
+    if (n_seqs < 0 || table_pages < 1 || n_pool < 1 || n_tokens < 0 || page_size < 1) return BEVPOOL_ERR_INVALID_ARG;
+    if (!page_size_ok(page_size) || n_seqs > kMaxPlanSeqs) return BEVPOOL_ERR_UNSUPPORTED;
+    if ((static_cast<int64_t>(table_pages) + 1) * page_size > INT32_MAX) return BEVPOOL_ERR_INVALID_ARG;
+    const void *always[] = {free_pages, n_free, cu_q, free_out, n_free_out, missing};
+    const void *requests[] = {q_len, kv_len, first, block_table, kv_len_out, first_out, block_table_out};
+    for (const void *p : always)
+        if (!p || !aligned(p, 4)) return BEVPOOL_ERR_INVALID_ARG;
+    for (const void *p : requests)
+        if ((n_seqs > 0 && !p) || !aligned(p, 4)) return BEVPOOL_ERR_INVALID_ARG;
+    if (!aligned(drop, 4) || !aligned(positions, 4) || !aligned(slots, 8)) return BEVPOOL_ERR_INVALID_ARG;
+    if (n_tokens > 0 && (!positions || !slots)) return BEVPOOL_ERR_INVALID_ARG;
+    PlanArgs a = {q_len,  kv_len,    first, drop,       block_table, free_pages,      n_free,   n_seqs,     table_pages, n_pool,
+                  n_tokens, page_shift(page_size), cu_q, positions, slots, kv_len_out, first_out, block_table_out, free_out, n_free_out,
+                  missing, static_cast<cudaStream_t>(stream)};
+    return cuda_status(launch_plan_pages(a));
 }
 
 bevpool_status bevpool_kv_append(

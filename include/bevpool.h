@@ -476,6 +476,48 @@ BEVPOOL_API bevpool_status bevpool_qk_norm_rope_backward(
     float *dk_weight, void *workspace, size_t workspace_bytes, void *stream);
 
 /*
+ * A batch's pages and places from its lengths, on the device: requests that
+ * end or let go of their oldest pages give them back, new tokens get pages, and
+ * what the append and the attention read is written out.  One launch.
+ *
+ * Request b holds kv_len[b] tokens on the pages block_table[b][0 ..], the first
+ * of them at position first[b], and brings q_len[b] new ones (negative lengths
+ * count as 0).  drop (NULL: none) says how many of its oldest pages it gives
+ * back before that (more than it has: all); a negative entry ends the request:
+ * all its pages go back and its row starts anew at position 0.
+ *
+ * The free pages are a stack, free_pages[0 .. n_free): pages given back are laid
+ * on top in the requests' order, then the requests in order take their new pages
+ * from the top.  Outputs:
+ *   cu_q             int32 [n_seqs + 1], the sums of q_len;
+ *   positions        int32 [n_tokens]: first_out + place of each new token;
+ *   slots            int64 [n_tokens]: page * page_size + place % page_size;
+ *   kv_len_out, first_out, block_table_out  lengths with the new tokens,
+ *                    positions of the first tokens kept, tables (-1 past a
+ *                    request's pages);
+ *   free_out, n_free_out  the stack that is left (-1 past it);
+ *   missing          int32 [1]: 0; or how many pages there were too few; or -1
+ *                    where something else does not fit: a table's row, n_tokens
+ *                    rows for the new tokens, or free_out for the pages.
+ * Rows from cu_q[n_seqs] on get position 0 and slot -1.  Where missing is not 0
+ * nothing changes: lengths, tables and free pages are handed on as they were,
+ * cu_q is 0 throughout, and the rows are those of a batch without new tokens.
+ *   q_len, kv_len, first, drop  device int32 [n_seqs];
+ *   block_table      device int32 [n_seqs][table_pages], as its output;
+ *   free_pages       device int32 [n_pool], as its output;  n_free: device int32 [1];
+ *   n_seqs           0 .. 16384;  page_size: a power of two in [16, 256];
+ *   n_tokens         host bound of the new tokens.
+ * Outputs must not overlap inputs or each other.  Page numbers are passed on,
+ * not looked at.
+ */
+BEVPOOL_API bevpool_status bevpool_plan_pages(
+    const int32_t *q_len, const int32_t *kv_len, const int32_t *first, const int32_t *drop, const int32_t *block_table,
+    const int32_t *free_pages, const int32_t *n_free, int32_t n_seqs, int32_t table_pages, int32_t n_pool,
+    int32_t n_tokens, int32_t page_size, int32_t *cu_q, int32_t *positions, int64_t *slots, int32_t *kv_len_out,
+    int32_t *first_out, int32_t *block_table_out, int32_t *free_out, int32_t *n_free_out, int32_t *missing,
+    void *stream);
+
+/*
  * Append the keys and values of new tokens to a paged cache, with the keys'
  * norm and rotation on the way; optionally the same for the queries of the
  * tokens (q NULL: none), all in one launch.
