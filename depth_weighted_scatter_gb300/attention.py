@@ -35,6 +35,7 @@ _dt = ctypes.c_int
 _rows = [_vp, _i64, _i64]
 _rotary = [_vp, _i32, _vp, _i32, _vp, _i32]                 # positions, n_axes, sections, rotary_dim, inv_freq, interleaved
 _pages = [_i64, _i64, _i64, _i32, _i32, _vp, _i32, _vp, _vp, _i32]
+_scaled_pages = _pages[:3] + [_vp, _vp] + _pages[3:]        # with k_scales, v_scales
 
 _lib.bevpool_qk_norm_rope.argtypes = ([_dt] + _rows * 2 + [_i32] * 4 + [_vp, _vp, _f32] + _rotary + _rows * 2 + [_vp])
 _lib.bevpool_qk_norm_rope.restype = ctypes.c_int
@@ -46,6 +47,9 @@ _lib.bevpool_qk_norm_rope_backward.restype = ctypes.c_int
 _lib.bevpool_kv_append.argtypes = ([_dt, _dt] + _rows * 3 + [_i32] * 4 + [_vp, _vp, _f32] + _rotary + _rows
                                    + [_vp, _vp] + _pages + [_f32, _f32, _vp])
 _lib.bevpool_kv_append.restype = ctypes.c_int
+_lib.bevpool_kv_append_scaled.argtypes = ([_dt] + _rows * 3 + [_i32] * 4 + [_vp, _vp, _f32] + _rotary + _rows + [_vp, _vp]
+                                          + _scaled_pages + [_vp])
+_lib.bevpool_kv_append_scaled.restype = ctypes.c_int
 _lib.bevpool_paged_attention_workspace_size.argtypes = [_i32] * 8
 _lib.bevpool_paged_attention_workspace_size.restype = _sz
 _lib.bevpool_paged_attention.argtypes = ([_dt, _dt] + _rows + [_vp, _vp] + _pages + [_i32] * 6
@@ -73,6 +77,10 @@ def bevpool_qk_norm_rope_backward(*args) -> int:
 
 def bevpool_kv_append(*args) -> int:
     return _lib.bevpool_kv_append(*args)
+
+
+def bevpool_kv_append_scaled(*args) -> int:
+    return _lib.bevpool_kv_append_scaled(*args)
 
 
 def bevpool_paged_attention_workspace_size(n_seqs: int, n_tokens: int, n_q_heads: int, n_k_heads: int, head_dim: int,
@@ -151,6 +159,21 @@ def kv_append(k, v, k_cache, v_cache, block_table, kv_len, cu_q, positions, inv_
                                   cu_q, eps, positions, inv_freq, sections, interleaved)
     return _ops.kv_append(k, v, q, k_weight, q_weight, q_out, k_scale, v_scale, k_cache, v_cache, block_table, kv_len, cu_q,
                           eps, positions, inv_freq, sections, interleaved)
+
+
+def kv_append_scaled(k, v, k_cache, v_cache, k_scales, v_scales, block_table, kv_len, cu_q, positions, inv_freq, *,
+                     sections=None, k_weight=None, eps: float = 1e-6, interleaved: bool = False, q=None, q_weight=None,
+                     q_out=None, stream=None):
+    """bevpool_kv_append_scaled: kv_append to a cache of E4M3 codes with a scale
+    for each page and key head (k_scales, v_scales: float32 [n_pages,
+    n_k_heads]), worked out from what a page gets.  Returns q_out (None without
+    q)."""
+    if stream is not None:
+        with _stream_of(stream):
+            return _ops.kv_append_scaled(k, v, q, k_weight, q_weight, q_out, k_scales, v_scales, k_cache, v_cache, block_table,
+                                         kv_len, cu_q, eps, positions, inv_freq, sections, interleaved)
+    return _ops.kv_append_scaled(k, v, q, k_weight, q_weight, q_out, k_scales, v_scales, k_cache, v_cache, block_table, kv_len,
+                                 cu_q, eps, positions, inv_freq, sections, interleaved)
 
 
 def paged_attention(q, k_cache, v_cache, block_table, kv_len, cu_q, *, max_q_len: int, max_kv_len: int,

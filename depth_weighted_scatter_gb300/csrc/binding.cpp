@@ -309,6 +309,47 @@ PyObject *kv_append(Args a) {
     return THPVariable_Wrap(qo);
 }
 
+// k_scales, v_scales: checked against the cache that they belong to.
+struct PageScales {
+    at::Tensor k, v;
+    explicit PageScales(Args &a) : k(a.tensor("k_scales")), v(a.tensor("v_scales")) {}
+    float *of(const char *name, const at::Tensor &t, const Cache &c, const Like &l) const {
+        if (c.code != BEVPOOL_E4M3) refuse("caches: E4M3 codes are wanted", BEVPOOL_ERR_UNSUPPORTED);
+        if (t.dim() != 2 || t.size(0) != c.n_pages || t.size(1) != c.heads) refuse(std::string(name) + ": [n_pages, n_k_heads] is wanted");
+        return static_cast<float *>(vector(name, t, static_cast<int64_t>(c.n_pages) * c.heads, at::kFloat, l.device));
+    }
+};
+
+// k, v, q, k_weight, q_weight, q_out, k_scales, v_scales, k_cache.. , eps, positions..
+PyObject *kv_append_scaled(Args a) {
+    const at::Tensor k = a.tensor("k"), v = a.tensor("v"), q = a.maybe("q"), kw = a.maybe("k_weight"), qw = a.maybe("q_weight");
+    at::Tensor qo = a.maybe("q_out");
+    const PageScales s(a);
+    const Like l = like("k", k);
+    const Rows kr = rows("k", k, l, l.H), vr = rows("v", v, l, l.H);
+    const Cache c = cache(a, l, l.H);
+    const float eps = a.f32();
+    const Positions p = positions(a, l);
+    const float *w0 = weight("q_weight", qw, l), *w1 = weight("k_weight", kw, l);
+    float *ks = s.of("k_scales", s.k, c, l), *vs = s.of("v_scales", s.v, c, l);
+    Rows qr = {nullptr, 0, 0}, qor = {nullptr, 0, 0};
+    int64_t Hq = 0;
+    if (q.defined()) {
+        qr = rows("q", q, l, -1);
+        Hq = q.size(1);
+        if (!qo.defined()) qo = fresh(q.sizes(), l.type, l.device);
+        qor = rows("q_out", qo, l, Hq);
+    } else if (qo.defined()) {
+        refuse("q_out without q");
+    }
+    done(bevpool_kv_append_scaled(l.code, kr.p, kr.ts, kr.hs, vr.p, vr.ts, vr.hs, qr.p, qr.ts, qr.hs, l.T, Hq, l.H, l.D, w0, w1, eps,
+                                  p.p, p.axes, p.sections, p.rotary_dim, p.inv_freq, p.interleaved, qor.p, qor.ts, qor.hs, c.k, c.v,
+                                  c.ps, c.ss, c.hs, ks, vs, c.n_pages, c.page, c.table, c.table_pages, c.kv_len, c.cu_q, c.n_seqs,
+                                  l.stream),
+         "bevpool_kv_append_scaled");
+    return THPVariable_Wrap(qo);
+}
+
 // q, workspace, k_cache.., max_q_len, max_kv_len, scale (None: head_dim ** -0.5), causal, window, k_scale, v_scale, out, lse?
 PyObject *paged_attention(Args a) {
     const at::Tensor q = a.tensor("q");
@@ -445,6 +486,7 @@ PyMethodDef entry(const char *name) {
 PyMethodDef g_methods[] = {entry<qk_norm_rope, 11>("qk_norm_rope"),
                            entry<qk_norm_rope_backward, 14>("qk_norm_rope_backward"),
                            entry<kv_append, 18>("kv_append"),
+                           entry<kv_append_scaled, 18>("kv_append_scaled"),
                            entry<paged_attention, 16>("paged_attention"),
                            entry<plan_pages, 10>("plan_pages"),
                            {"set_error", set_error, METH_O, nullptr},

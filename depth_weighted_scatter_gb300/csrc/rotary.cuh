@@ -83,6 +83,13 @@ struct AppendArgs {
 };
 cudaError_t launch_kv_append(const AppendArgs &a);
 
+// Append to a cache with scales of its own (kv_append_scaled.cu).
+struct ScaledAppendArgs {
+    AppendArgs g;                 // an E4M3 cache; k_inv, v_inv unused
+    float *k_scales, *v_scales;   // [n_pages][Hk]
+};
+cudaError_t launch_append_scaled(const ScaledAppendArgs &a);
+
 // ---------------------------------------------------------------- device
 
 // Two 16-bit elements as two FP32 values in one register pair, and back.

@@ -110,6 +110,41 @@ bevpool_status cache_ok(const void *k_cache, const void *v_cache, int64_t page_s
     return BEVPOOL_OK;
 }
 
+// What both appends take, into *g; the cache's elements have eb bytes.
+bevpool_status append_args(bevpool_dtype dtype, int eb, const HeadRows &k, const HeadRows &v, const HeadRows &q, int32_t T, int32_t Hq,
+                           int32_t Hk, int32_t D, const float *q_weight, const float *k_weight, float eps, const int32_t *positions,
+                           int32_t n_axes, const int32_t *sections, int32_t rotary_dim, const float *inv_freq, int32_t interleaved,
+                           const HeadRowsOut &q_out, void *k_cache, void *v_cache, int64_t page_stride, int64_t slot_stride,
+                           int64_t head_stride, int32_t n_pages, int32_t page_size, const int32_t *block_table, int32_t table_pages,
+                           const int32_t *kv_len, const int32_t *cu_q, int32_t n_seqs, void *stream, AppendArgs *g) {
+    const bevpool_status st = cache_ok(k_cache, v_cache, page_stride, slot_stride, head_stride, n_pages, page_size, block_table,
+                                       table_pages, kv_len, cu_q, n_seqs, Hk, D, eb, &g->pg);
+    if (st != BEVPOOL_OK) return st;
+    if (!rows_ok(k.p, k.token_stride, k.head_stride) || !rows_ok(v.p, v.token_stride, v.head_stride) || !weight_ok(q_weight) ||
+        !weight_ok(k_weight) || !eps_ok(eps) ||
+        !rotary_ok(positions, n_axes, sections, rotary_dim, inv_freq, interleaved, D, &g->f.rot))
+        return BEVPOOL_ERR_INVALID_ARG;
+    if (q.p && (!rows_ok(q.p, q.token_stride, q.head_stride) || !rows_ok(q_out.p, q_out.token_stride, q_out.head_stride)))
+        return BEVPOOL_ERR_INVALID_ARG;
+    g->f.dtype = dtype;
+    g->f.q = q;
+    g->f.k = k;
+    g->f.q_out = q_out;
+    g->f.T = T;
+    g->f.Hq = q.p ? Hq : 0;
+    g->f.Hk = Hk;
+    g->f.D = D;
+    g->f.q_weight = q_weight;
+    g->f.k_weight = k_weight;
+    g->f.eps = eps;
+    g->f.stream = static_cast<cudaStream_t>(stream);
+    g->v = v;
+    g->cache_e4m3 = eb == 1;
+    g->k_cache = k_cache;
+    g->v_cache = v_cache;
+    return BEVPOOL_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -249,37 +284,46 @@ bevpool_status bevpool_kv_append(
     if (st != BEVPOOL_OK) return st;
     if (n_tokens == 0) return BEVPOOL_OK;
     AppendArgs g = {};
-    st = cache_ok(k_cache, v_cache, page_stride, slot_stride, head_stride, n_pages, page_size, block_table, table_pages,
-                  kv_len, cu_q, n_seqs, n_k_heads, head_dim, e4m3 ? 1 : 2, &g.pg);
+    st = append_args(dtype, e4m3 ? 1 : 2, {k, k_token_stride, k_head_stride}, {v, v_token_stride, v_head_stride},
+                     {q, q_token_stride, q_head_stride}, n_tokens, n_q_heads, n_k_heads, head_dim, q_weight, k_weight, eps, positions,
+                     n_axes, sections, rotary_dim, inv_freq, interleaved, {q_out, q_out_token_stride, q_out_head_stride}, k_cache,
+                     v_cache, page_stride, slot_stride, head_stride, n_pages, page_size, block_table, table_pages, kv_len, cu_q, n_seqs,
+                     stream, &g);
     if (st != BEVPOOL_OK) return st;
-    if (!rows_ok(k, k_token_stride, k_head_stride) || !rows_ok(v, v_token_stride, v_head_stride) ||
-        !weight_ok(q_weight) || !weight_ok(k_weight) || !eps_ok(eps) ||
-        !rotary_ok(positions, n_axes, sections, rotary_dim, inv_freq, interleaved, head_dim, &g.f.rot))
-        return BEVPOOL_ERR_INVALID_ARG;
-    if (q && (!rows_ok(q, q_token_stride, q_head_stride) || !rows_ok(q_out, q_out_token_stride, q_out_head_stride)))
-        return BEVPOOL_ERR_INVALID_ARG;
     if (e4m3 && (!scale_ok(k_scale) || !scale_ok(v_scale))) return BEVPOOL_ERR_INVALID_ARG;
-    g.f.dtype = dtype;
-    g.f.q = {q, q_token_stride, q_head_stride};
-    g.f.k = {k, k_token_stride, k_head_stride};
-    g.f.q_out = {q_out, q_out_token_stride, q_out_head_stride};
-    g.f.T = n_tokens;
-    g.f.Hq = q ? n_q_heads : 0;
-    g.f.Hk = n_k_heads;
-    g.f.D = head_dim;
-    g.f.q_weight = q_weight;
-    g.f.k_weight = k_weight;
-    g.f.eps = eps;
-    g.f.stream = static_cast<cudaStream_t>(stream);
-    g.v = {v, v_token_stride, v_head_stride};
-    g.cache_e4m3 = e4m3;
-    g.k_cache = k_cache;
-    g.v_cache = v_cache;
     if (e4m3) {
         g.k_inv = inverse(k_scale);
         g.v_inv = inverse(v_scale);
     }
     return cuda_status(launch_kv_append(g));
+}
+
+bevpool_status bevpool_kv_append_scaled(
+    bevpool_dtype dtype, const void *k, int64_t k_token_stride, int64_t k_head_stride, const void *v,
+    int64_t v_token_stride, int64_t v_head_stride, const void *q, int64_t q_token_stride, int64_t q_head_stride,
+    int32_t n_tokens, int32_t n_q_heads, int32_t n_k_heads, int32_t head_dim, const float *q_weight,
+    const float *k_weight, float eps, const int32_t *positions, int32_t n_axes, const int32_t *sections,
+    int32_t rotary_dim, const float *inv_freq, int32_t interleaved, void *q_out, int64_t q_out_token_stride,
+    int64_t q_out_head_stride, void *k_cache, void *v_cache, int64_t page_stride, int64_t slot_stride,
+    int64_t head_stride, float *k_scales, float *v_scales, int32_t n_pages, int32_t page_size,
+    const int32_t *block_table, int32_t table_pages, const int32_t *kv_len, const int32_t *cu_q, int32_t n_seqs,
+    void *stream) {
+    if (!dtype_ok(dtype)) return BEVPOOL_ERR_UNSUPPORTED;
+    bevpool_status st = heads_ok(n_tokens, q ? n_q_heads : 1, n_k_heads, head_dim);
+    if (st != BEVPOOL_OK) return st;
+    if (head_dim != 64 && head_dim != 128) return BEVPOOL_ERR_UNSUPPORTED;
+    if (n_tokens == 0) return BEVPOOL_OK;
+    ScaledAppendArgs a = {};
+    st = append_args(dtype, 1, {k, k_token_stride, k_head_stride}, {v, v_token_stride, v_head_stride},
+                     {q, q_token_stride, q_head_stride}, n_tokens, n_q_heads, n_k_heads, head_dim, q_weight, k_weight, eps, positions,
+                     n_axes, sections, rotary_dim, inv_freq, interleaved, {q_out, q_out_token_stride, q_out_head_stride}, k_cache,
+                     v_cache, page_stride, slot_stride, head_stride, n_pages, page_size, block_table, table_pages, kv_len, cu_q, n_seqs,
+                     stream, &a.g);
+    if (st != BEVPOOL_OK) return st;
+    if (!k_scales || !v_scales || !aligned(k_scales, 4) || !aligned(v_scales, 4)) return BEVPOOL_ERR_INVALID_ARG;
+    a.k_scales = k_scales;
+    a.v_scales = v_scales;
+    return cuda_status(launch_append_scaled(a));
 }
 
 namespace {

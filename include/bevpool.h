@@ -551,6 +551,38 @@ BEVPOOL_API bevpool_status bevpool_kv_append(
     int32_t table_pages, const int32_t *kv_len, const int32_t *cu_q, int32_t n_seqs, float k_scale, float v_scale,
     void *stream);
 
+/*
+ * bevpool_kv_append to an E4M3 cache with a scale for each page and key head,
+ * which the call works out: key = code * k_scales[page][head], value = code *
+ * v_scales[page][head].
+ *
+ * With top the largest finite magnitude that a page and head get in this call:
+ * a page whose slot 0 is among the new tokens gets the scale top / 448; one that
+ * holds earlier tokens of the request (the new ones start inside it) keeps its
+ * scale times 2^n, the least n >= 0 with top <= 448 * scale * 2^n, and the
+ * earlier tokens' codes are multiplied by 2^-n and rounded to nearest even.
+ * Scales stay within [2^-48, 2^48] (an old one outside counts as the nearest
+ * bound).  The new codes are those of value / scale as in bevpool_kv_append:
+ * rounded to nearest even, saturating at +-448, so infinities become +-448; NaN
+ * stays NaN.
+ *   head_dim            64 or 128;
+ *   k_scales, v_scales  device float [n_pages][n_k_heads], written where a page
+ *                       gets tokens.
+ * A page that gets tokens belongs to one request, once: pages that several
+ * requests share must be full ones.  Other arguments and what is not written: as
+ * in bevpool_kv_append.  Results are deterministic.
+ */
+BEVPOOL_API bevpool_status bevpool_kv_append_scaled(
+    bevpool_dtype dtype, const void *k, int64_t k_token_stride, int64_t k_head_stride, const void *v,
+    int64_t v_token_stride, int64_t v_head_stride, const void *q, int64_t q_token_stride, int64_t q_head_stride,
+    int32_t n_tokens, int32_t n_q_heads, int32_t n_k_heads, int32_t head_dim, const float *q_weight,
+    const float *k_weight, float eps, const int32_t *positions, int32_t n_axes, const int32_t *sections,
+    int32_t rotary_dim, const float *inv_freq, int32_t interleaved, void *q_out, int64_t q_out_token_stride,
+    int64_t q_out_head_stride, void *k_cache, void *v_cache, int64_t page_stride, int64_t slot_stride,
+    int64_t head_stride, float *k_scales, float *v_scales, int32_t n_pages, int32_t page_size,
+    const int32_t *block_table, int32_t table_pages, const int32_t *kv_len, const int32_t *cu_q, int32_t n_seqs,
+    void *stream);
+
 /* Device workspace (bytes, 256-byte aligned) of bevpool_paged_attention with
  * these sizes on the current device; 0 where none is needed or a size is
  * invalid. */
