@@ -55,6 +55,9 @@ _lib.bevpool_paged_attention_workspace_size.restype = _sz
 _lib.bevpool_paged_attention.argtypes = ([_dt, _dt] + _rows + [_vp, _vp] + _pages + [_i32] * 6
                                          + [_f32, _i32, _i32, _f32, _f32] + _rows + [_vp, _vp, _sz, _vp])
 _lib.bevpool_paged_attention.restype = ctypes.c_int
+_lib.bevpool_paged_attention_scaled.argtypes = ([_dt] + _rows + [_vp, _vp] + _scaled_pages + [_i32] * 6 + [_f32, _i32, _i32]
+                                                + _rows + [_vp, _vp, _sz, _vp])
+_lib.bevpool_paged_attention_scaled.restype = ctypes.c_int
 _lib.bevpool_plan_pages.argtypes = [_vp] * 7 + [_i32] * 5 + [_vp] * 10
 _lib.bevpool_plan_pages.restype = ctypes.c_int
 _lib.bevpool_attention_timeouts.argtypes = [_vp]
@@ -91,6 +94,10 @@ def bevpool_paged_attention_workspace_size(n_seqs: int, n_tokens: int, n_q_heads
 
 def bevpool_paged_attention(*args) -> int:
     return _lib.bevpool_paged_attention(*args)
+
+
+def bevpool_paged_attention_scaled(*args) -> int:
+    return _lib.bevpool_paged_attention_scaled(*args)
 
 
 def bevpool_plan_pages(*args) -> int:
@@ -190,6 +197,20 @@ def paged_attention(q, k_cache, v_cache, block_table, kv_len, cu_q, *, max_q_len
                                         causal, window, k_scale, v_scale, out, return_lse)
     return _ops.paged_attention(q, workspace, k_cache, v_cache, block_table, kv_len, cu_q, max_q_len, max_kv_len, scale, causal,
                                 window, k_scale, v_scale, out, return_lse)
+
+
+def paged_attention_scaled(q, k_cache, v_cache, k_scales, v_scales, block_table, kv_len, cu_q, *, max_q_len: int, max_kv_len: int,
+                           scale: Optional[float] = None, causal: bool = True, window: int = 0, out=None,
+                           return_lse: bool = False, workspace=None, stream=None):
+    """bevpool_paged_attention_scaled: paged_attention over a cache of E4M3 codes
+    with a scale for each page and key head (k_scales, v_scales: float32 [n_pages,
+    n_k_heads]), as kv_append_scaled makes it."""
+    if stream is not None:
+        with _stream_of(stream):
+            return _ops.paged_attention_scaled(q, workspace, k_scales, v_scales, k_cache, v_cache, block_table, kv_len, cu_q,
+                                               max_q_len, max_kv_len, scale, causal, window, out, return_lse)
+    return _ops.paged_attention_scaled(q, workspace, k_scales, v_scales, k_cache, v_cache, block_table, kv_len, cu_q, max_q_len,
+                                       max_kv_len, scale, causal, window, out, return_lse)
 
 
 class PagePlan(NamedTuple):

@@ -309,29 +309,25 @@ PyObject *kv_append(Args a) {
     return THPVariable_Wrap(qo);
 }
 
-// k_scales, v_scales: checked against the cache that they belong to.
-struct PageScales {
-    at::Tensor k, v;
-    explicit PageScales(Args &a) : k(a.tensor("k_scales")), v(a.tensor("v_scales")) {}
-    float *of(const char *name, const at::Tensor &t, const Cache &c, const Like &l) const {
-        if (c.code != BEVPOOL_E4M3) refuse("caches: E4M3 codes are wanted", BEVPOOL_ERR_UNSUPPORTED);
-        if (t.dim() != 2 || t.size(0) != c.n_pages || t.size(1) != c.heads) refuse(std::string(name) + ": [n_pages, n_k_heads] is wanted");
-        return static_cast<float *>(vector(name, t, static_cast<int64_t>(c.n_pages) * c.heads, at::kFloat, l.device));
-    }
-};
+// A cache's scales of pages and heads.
+float *scales_of(const char *name, const at::Tensor &t, const Cache &c, const Like &l) {
+    if (c.code != BEVPOOL_E4M3) refuse("caches: E4M3 codes are wanted", BEVPOOL_ERR_UNSUPPORTED);
+    if (t.dim() != 2 || t.size(0) != c.n_pages || t.size(1) != c.heads) refuse(std::string(name) + ": [n_pages, n_k_heads] is wanted");
+    return static_cast<float *>(vector(name, t, static_cast<int64_t>(c.n_pages) * c.heads, at::kFloat, l.device));
+}
 
 // k, v, q, k_weight, q_weight, q_out, k_scales, v_scales, k_cache.. , eps, positions..
 PyObject *kv_append_scaled(Args a) {
     const at::Tensor k = a.tensor("k"), v = a.tensor("v"), q = a.maybe("q"), kw = a.maybe("k_weight"), qw = a.maybe("q_weight");
     at::Tensor qo = a.maybe("q_out");
-    const PageScales s(a);
+    const at::Tensor kt = a.tensor("k_scales"), vt = a.tensor("v_scales");
     const Like l = like("k", k);
     const Rows kr = rows("k", k, l, l.H), vr = rows("v", v, l, l.H);
     const Cache c = cache(a, l, l.H);
     const float eps = a.f32();
     const Positions p = positions(a, l);
     const float *w0 = weight("q_weight", qw, l), *w1 = weight("k_weight", kw, l);
-    float *ks = s.of("k_scales", s.k, c, l), *vs = s.of("v_scales", s.v, c, l);
+    float *ks = scales_of("k_scales", kt, c, l), *vs = scales_of("v_scales", vt, c, l);
     Rows qr = {nullptr, 0, 0}, qor = {nullptr, 0, 0};
     int64_t Hq = 0;
     if (q.defined()) {
@@ -350,14 +346,26 @@ PyObject *kv_append_scaled(Args a) {
     return THPVariable_Wrap(qo);
 }
 
-// q, workspace, k_cache.., max_q_len, max_kv_len, scale (None: head_dim ** -0.5), causal, window, k_scale, v_scale, out, lse?
-PyObject *paged_attention(Args a) {
+// q, workspace, (scaled: k_scales, v_scales,) k_cache.., max_q_len, max_kv_len, scale (None: head_dim ** -0.5), causal, window,
+// (not scaled: k_scale, v_scale,) out, lse?
+template <bool SCALED>
+PyObject *attend(Args a) {
     const at::Tensor q = a.tensor("q");
     at::Tensor ws = a.maybe("workspace");
     workspace_ok(ws);
+    at::Tensor kt, vt;
+    if (SCALED) {
+        kt = a.tensor("k_scales");
+        vt = a.tensor("v_scales");
+    }
     const Like l = like("q", q);
     const Rows qr = rows("q", q, l, l.H);
     const Cache c = cache(a, l, -1);
+    const float *kp = nullptr, *vp = nullptr;
+    if (SCALED) {
+        kp = scales_of("k_scales", kt, c, l);
+        vp = scales_of("v_scales", vt, c, l);
+    }
     const int32_t max_q = a.i32("max_q_len"), max_kv = a.i32("max_kv_len");
     PyObject *so = a.next();
     float scale = 1.0f / std::sqrt(static_cast<float>(l.D));
@@ -367,7 +375,11 @@ PyObject *paged_attention(Args a) {
     }
     const bool causal = a.flag();
     const int32_t window = a.i32("window");
-    const float ks = a.f32(), vs = a.f32();
+    float ks = 1.0f, vs = 1.0f;
+    if (!SCALED) {
+        ks = a.f32();
+        vs = a.f32();
+    }
     at::Tensor out = a.maybe("out"), lse;
     const bool want_lse = a.flag();
     if (!out.defined()) out = fresh(q.sizes(), l.type, l.device);
@@ -377,11 +389,19 @@ PyObject *paged_attention(Args a) {
         const size_t n = bevpool_paged_attention_workspace_size(c.n_seqs, l.T, l.H, c.heads, l.D, max_q, max_kv, window);
         if (n) ws = fresh({static_cast<int64_t>(n)}, at::kByte, l.device);
     }
-    done(bevpool_paged_attention(l.code, c.code, qr.p, qr.ts, qr.hs, c.k, c.v, c.ps, c.ss, c.hs, c.n_pages, c.page, c.table,
-                                 c.table_pages, c.kv_len, c.cu_q, c.n_seqs, l.T, l.H, c.heads, l.D, max_q, max_kv, scale, causal,
-                                 window, ks, vs, o.p, o.ts, o.hs, want_lse ? static_cast<float *>(lse.data_ptr()) : nullptr,
-                                 ws.defined() ? ws.data_ptr() : nullptr, ws.defined() ? ws.nbytes() : 0, l.stream),
-         "bevpool_paged_attention");
+    float *lp = want_lse ? static_cast<float *>(lse.data_ptr()) : nullptr;
+    void *wp = ws.defined() ? ws.data_ptr() : nullptr;
+    const size_t wn = ws.defined() ? ws.nbytes() : 0;
+    if (SCALED)
+        done(bevpool_paged_attention_scaled(l.code, qr.p, qr.ts, qr.hs, c.k, c.v, c.ps, c.ss, c.hs, kp, vp, c.n_pages, c.page, c.table,
+                                            c.table_pages, c.kv_len, c.cu_q, c.n_seqs, l.T, l.H, c.heads, l.D, max_q, max_kv, scale,
+                                            causal, window, o.p, o.ts, o.hs, lp, wp, wn, l.stream),
+             "bevpool_paged_attention_scaled");
+    else
+        done(bevpool_paged_attention(l.code, c.code, qr.p, qr.ts, qr.hs, c.k, c.v, c.ps, c.ss, c.hs, c.n_pages, c.page, c.table,
+                                     c.table_pages, c.kv_len, c.cu_q, c.n_seqs, l.T, l.H, c.heads, l.D, max_q, max_kv, scale, causal,
+                                     window, ks, vs, o.p, o.ts, o.hs, lp, wp, wn, l.stream),
+             "bevpool_paged_attention");
     if (!want_lse) return THPVariable_Wrap(out);
     return Py_BuildValue("NN", THPVariable_Wrap(out), THPVariable_Wrap(lse));
 }
@@ -487,7 +507,8 @@ PyMethodDef g_methods[] = {entry<qk_norm_rope, 11>("qk_norm_rope"),
                            entry<qk_norm_rope_backward, 14>("qk_norm_rope_backward"),
                            entry<kv_append, 18>("kv_append"),
                            entry<kv_append_scaled, 18>("kv_append_scaled"),
-                           entry<paged_attention, 16>("paged_attention"),
+                           entry<attend<false>, 16>("paged_attention"),
+                           entry<attend<true>, 16>("paged_attention_scaled"),
                            entry<plan_pages, 10>("plan_pages"),
                            {"set_error", set_error, METH_O, nullptr},
                            {nullptr, nullptr, 0, nullptr}};

@@ -122,9 +122,20 @@ cudaError_t launch_paged_attention(const AttnArgs &args, void *workspace) {
     a.part_o = static_cast<float *>(workspace);
     a.part_ml = a.part_o + pl.parts * a.D;
     a.cut = reinterpret_cast<int2 *>(a.part_ml + pl.parts * 2);
-    const cudaError_t e = pl.few ? launch_attend_few(a, pl) : launch_attend_tile(a, pl);
+    const bool scaled = a.cache == kCacheScaled;
+    const cudaError_t e = pl.few ? (scaled ? launch_attend_few_scaled(a, pl) : launch_attend_few(a, pl))
+                                 : (scaled ? launch_attend_tile_scaled(a, pl) : launch_attend_tile(a, pl));
     if (e != cudaSuccess || pl.parts == 0) return e;
     return launch_attend_join(a, pl);
+}
+
+cudaError_t attention_timeouts(int64_t *count) {
+    int64_t n = 0;
+    cudaError_t e = cudaDeviceSynchronize();               // a copy alone leaves out streams that do not wait for the default one
+    if (e == cudaSuccess) e = attend_tile_timeouts(&n);
+    if (e == cudaSuccess) e = attend_tile_scaled_timeouts(&n);
+    if (e == cudaSuccess) *count = n;
+    return e;
 }
 
 }  // namespace bevpool

@@ -6,11 +6,16 @@
 
 namespace bevpool {
 
+// What a cache holds: the heads' type; E4M3 codes of one scale; of a scale a page
+// and key head.
+enum { kCacheSame, kCacheE4M3, kCacheScaled };
+
 struct AttnArgs {
-    int dtype, cache_e4m3;
+    int dtype, cache;
     HeadRows q;
     HeadRowsOut out;
     const void *k_cache, *v_cache;
+    const float *k_scales, *v_scales; // kCacheScaled: [n_pages][Hk]
     PagedArgs pg;
     int32_t T, Hq, Hk, G, D;          // G = Hq / Hk
     int32_t max_q_len, max_kv_len;
@@ -44,7 +49,12 @@ struct AttnPlan {
 constexpr int32_t kPairRows = 256;     // rows of a pair of row tiles
 AttnPlan attention_plan(const AttnSizes &z);
 cudaError_t launch_attend_few(const AttnArgs &a, const AttnPlan &pl);      // attend_few.cu
+cudaError_t launch_attend_few_scaled(const AttnArgs &a, const AttnPlan &pl);       // attend_few_scaled.cu: kCacheScaled
 cudaError_t launch_attend_tile(const AttnArgs &a, const AttnPlan &pl);     // attend_tile.cu
+cudaError_t launch_attend_tile_scaled(const AttnArgs &a, const AttnPlan &pl);      // attend_tile_scaled.cu
+// Waits of the device's kernels that ran out, added to *count: of one cache and of the other.
+cudaError_t attend_tile_timeouts(int64_t *count);
+cudaError_t attend_tile_scaled_timeouts(int64_t *count);
 cudaError_t attention_timeouts(int64_t *count);
 cudaError_t launch_attend_join(const AttnArgs &a, const AttnPlan &pl);     // attend_join.cu: where there are parts
 
@@ -98,6 +108,25 @@ __device__ __forceinline__ float pow2(float x) {
     return y;
 }
 
+// Scales of a page and head as the products use them.  A key's score in base 2 is
+// q.code * score, its weight in the product with the values' codes 2^(that + lift),
+// and the sum takes the weights times `sum`, so that one exponential a key serves
+// both although the values' scales differ.  Scales stay within [2^-48, 2^48], so the
+// lift moves two keys at most 2^96 apart: what counts in the sum is no smaller than
+// 2^-126 of the largest weight.
+struct PageFactors {
+    float score, lift, sum;
+};
+
+__device__ __forceinline__ PageFactors page_factors(float score, float ks, float vs) {
+    PageFactors f;
+    const float v = fminf(fmaxf(vs, 0x1p-48f), 0x1p48f);   // NaN: the least
+    f.score = fmaxf(score * fminf(fmaxf(ks, 0x1p-48f), 0x1p48f), 0x1p-126f);       // never 0: 0 * -inf
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(f.lift) : "f"(v));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(f.sum) : "f"(v));
+    return f;
+}
+
 // Two E4M3 codes (low 16 bits) as two 16-bit values.
 template <typename T>
 __device__ __forceinline__ uint32_t widen2(uint32_t codes) {
@@ -132,7 +161,7 @@ __device__ __forceinline__ void load_cache(const void *p, int64_t at, float *x) 
 // One query row over the keys [lo, hi) by one warp, element by element: lane l
 // holds elements l*E .. l*E+E-1.  The running maximum *m (base 2), sum *l and
 // acc follow the softmax; keys not seen are never touched.
-template <typename T, bool E4M3, int D>
+template <typename T, int C, int D>
 __device__ void attend_row(const AttnArgs &a, int b, int hk, const float *q, int32_t lo, int32_t hi, float *m, float *l,
                            float *acc) {
     constexpr int E = D / 32;
@@ -145,23 +174,28 @@ __device__ void attend_row(const AttnArgs &a, int b, int hk, const float *q, int
             j = end;
             continue;
         }
+        PageFactors f = {a.scale_log2, 0.0f, 1.0f};
+        if constexpr (C == kCacheScaled) {
+            const int64_t i = static_cast<int64_t>(page) * a.Hk + hk;
+            f = page_factors(a.scale_log2, a.k_scales[i], a.v_scales[i]);
+        }
         int64_t at = page * a.pg.page_stride + (j & (a.pg.page_size - 1)) * a.pg.slot_stride + hk * a.pg.head_stride +
                      lane * E;
         for (; j < end; ++j, at += a.pg.slot_stride) {
             float k[E], v[E];
-            load_cache<T, E4M3, E>(a.k_cache, at, k);
-            load_cache<T, E4M3, E>(a.v_cache, at, v);
+            load_cache<T, C != kCacheSame, E>(a.k_cache, at, k);
+            load_cache<T, C != kCacheSame, E>(a.v_cache, at, v);
             float s = 0.0f;
 #pragma unroll
             for (int i = 0; i < E; ++i) s = fmaf(q[i], k[i], s);
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-            s *= a.scale_log2;
+            s = C == kCacheScaled ? fmaf(s, f.score, f.lift) : s * a.scale_log2;
             const float mn = fmaxf(*m, s);
             const float base = mn == -INFINITY ? 0.0f : mn;
             const float r = exp2f(*m - base), p = exp2f(s - base);
             *m = mn;
-            *l = fmaf(*l, r, p);
+            *l = fmaf(*l, r, C == kCacheScaled ? p * f.sum : p);
 #pragma unroll
             for (int i = 0; i < E; ++i) acc[i] = fmaf(acc[i], r, p * v[i]);
         }
@@ -170,7 +204,7 @@ __device__ void attend_row(const AttnArgs &a, int b, int hk, const float *q, int
 
 // The keys [c0, c1) of one row again, by attend_row: *m, *l, acc (lane l:
 // elements l*E ..).
-template <typename T, bool E4M3, int D>
+template <typename T, int C, int D>
 __device__ __noinline__ void redo_row(const AttnArgs &a, const Request &r, int b, int hk, int i, int h, int32_t c0,
                                       int32_t c1, float *m, float *l, float *acc) {
     constexpr int E = D / 32;
@@ -187,7 +221,7 @@ __device__ __noinline__ void redo_row(const AttnArgs &a, const Request &r, int b
     *l = 0.0f;
     int32_t lo, hi;
     seen_keys(a, r, i, &lo, &hi);
-    attend_row<T, E4M3, D>(a, b, hk, q, max(lo, c0), min(hi, c1), m, l, acc);
+    attend_row<T, C, D>(a, b, hk, q, max(lo, c0), min(hi, c1), m, l, acc);
 }
 
 __device__ __forceinline__ int64_t part_row(const AttnArgs &a, const AttnPlan &pl, int b, int hk, int chunk, int row) {

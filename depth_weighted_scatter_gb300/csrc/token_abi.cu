@@ -340,6 +340,54 @@ bevpool_status attention_sizes_ok(int32_t n_seqs, int32_t T, int32_t Hq, int32_t
     return BEVPOOL_OK;
 }
 
+// What both attentions take, launched.  k_scales null: one scale for the cache.
+bevpool_status attend(bevpool_dtype dtype, int cache, const HeadRows &q, const void *k_cache, const void *v_cache, int64_t page_stride,
+                      int64_t slot_stride, int64_t head_stride, const float *k_scales, const float *v_scales, int32_t n_pages,
+                      int32_t page_size, const int32_t *block_table, int32_t table_pages, const int32_t *kv_len, const int32_t *cu_q,
+                      int32_t n_seqs, int32_t T, int32_t Hq, int32_t Hk, int32_t D, int32_t max_q_len, int32_t max_kv_len, float scale,
+                      int32_t causal, int32_t window, float k_scale, float v_scale, const HeadRowsOut &out, float *lse, void *workspace,
+                      size_t workspace_bytes, void *stream) {
+    bevpool_status st = attention_sizes_ok(n_seqs, T, Hq, Hk, D, max_q_len, max_kv_len);
+    if (st != BEVPOOL_OK) return st;
+    if (T == 0 || n_seqs == 0 || max_q_len == 0) return BEVPOOL_OK;
+    AttnArgs a = {};
+    st = cache_ok(k_cache, v_cache, page_stride, slot_stride, head_stride, n_pages, page_size, block_table, table_pages, kv_len, cu_q,
+                  n_seqs, Hk, D, cache == kCacheSame ? 2 : 1, &a.pg);
+    if (st != BEVPOOL_OK) return st;
+    if (!rows_ok(q.p, q.token_stride, q.head_stride) || !rows_ok(out.p, out.token_stride, out.head_stride) || !aligned(lse, 4))
+        return BEVPOOL_ERR_INVALID_ARG;
+    if (cache == kCacheScaled && (!k_scales || !v_scales || !aligned(k_scales, 4) || !aligned(v_scales, 4))) return BEVPOOL_ERR_INVALID_ARG;
+    if (cache != kCacheE4M3) k_scale = v_scale = 1.0f;
+    // page scales reach 2^48
+    const float most = cache == kCacheScaled ? 0x1p48f : k_scale;
+    if (!(scale > 0.0f) || !scale_ok(k_scale) || !scale_ok(v_scale) || !std::isfinite(scale * most * 1.4427f)) return BEVPOOL_ERR_INVALID_ARG;
+    if (window < 0 || (window > 0 && !causal)) return BEVPOOL_ERR_INVALID_ARG;
+    const size_t need = attention_workspace_bytes({n_seqs, T, Hq, Hk, D, max_q_len, max_kv_len, window, 0});
+    if (need > 0 && (!workspace || !aligned(workspace, 256) || workspace_bytes < need)) return BEVPOOL_ERR_WORKSPACE;
+    a.dtype = dtype;
+    a.cache = cache;
+    a.q = q;
+    a.out = out;
+    a.k_cache = k_cache;
+    a.v_cache = v_cache;
+    a.k_scales = k_scales;
+    a.v_scales = v_scales;
+    a.T = T;
+    a.Hq = Hq;
+    a.Hk = Hk;
+    a.G = Hq / Hk;
+    a.D = D;
+    a.max_q_len = max_q_len;
+    a.max_kv_len = max_kv_len;
+    a.scale_log2 = static_cast<float>(static_cast<double>(scale) * k_scale * 1.4426950408889634);
+    a.v_scale = v_scale;
+    a.causal = causal != 0;
+    a.window = window;
+    a.lse = lse;
+    a.stream = static_cast<cudaStream_t>(stream);
+    return cuda_status(launch_paged_attention(a, workspace));
+}
+
 }  // namespace
 
 size_t bevpool_paged_attention_workspace_size(int32_t n_seqs, int32_t n_tokens, int32_t n_q_heads, int32_t n_k_heads,
@@ -360,43 +408,24 @@ bevpool_status bevpool_paged_attention(
     float v_scale, void *out, int64_t out_token_stride, int64_t out_head_stride, float *lse, void *workspace,
     size_t workspace_bytes, void *stream) {
     if (!dtype_ok(dtype) || (cache_dtype != dtype && cache_dtype != BEVPOOL_E4M3)) return BEVPOOL_ERR_UNSUPPORTED;
-    const bool e4m3 = cache_dtype == BEVPOOL_E4M3;
-    bevpool_status st = attention_sizes_ok(n_seqs, n_tokens, n_q_heads, n_k_heads, head_dim, max_q_len, max_kv_len);
-    if (st != BEVPOOL_OK) return st;
-    if (n_tokens == 0 || n_seqs == 0 || max_q_len == 0) return BEVPOOL_OK;
-    AttnArgs a = {};
-    st = cache_ok(k_cache, v_cache, page_stride, slot_stride, head_stride, n_pages, page_size, block_table, table_pages,
-                  kv_len, cu_q, n_seqs, n_k_heads, head_dim, e4m3 ? 1 : 2, &a.pg);
-    if (st != BEVPOOL_OK) return st;
-    if (!rows_ok(q, q_token_stride, q_head_stride) || !rows_ok(out, out_token_stride, out_head_stride) || !aligned(lse, 4))
-        return BEVPOOL_ERR_INVALID_ARG;
-    if (!e4m3) k_scale = v_scale = 1.0f;
-    if (!(scale > 0.0f) || !scale_ok(k_scale) || !scale_ok(v_scale) || !std::isfinite(scale * k_scale * 1.4427f))
-        return BEVPOOL_ERR_INVALID_ARG;
-    if (window < 0 || (window > 0 && !causal)) return BEVPOOL_ERR_INVALID_ARG;
-    const size_t need =
-        attention_workspace_bytes({n_seqs, n_tokens, n_q_heads, n_k_heads, head_dim, max_q_len, max_kv_len, window, 0});
-    if (need > 0 && (!workspace || !aligned(workspace, 256) || workspace_bytes < need)) return BEVPOOL_ERR_WORKSPACE;
-    a.dtype = dtype;
-    a.cache_e4m3 = e4m3;
-    a.q = {q, q_token_stride, q_head_stride};
-    a.out = {out, out_token_stride, out_head_stride};
-    a.k_cache = k_cache;
-    a.v_cache = v_cache;
-    a.T = n_tokens;
-    a.Hq = n_q_heads;
-    a.Hk = n_k_heads;
-    a.G = n_q_heads / n_k_heads;
-    a.D = head_dim;
-    a.max_q_len = max_q_len;
-    a.max_kv_len = max_kv_len;
-    a.scale_log2 = static_cast<float>(static_cast<double>(scale) * k_scale * 1.4426950408889634);
-    a.v_scale = v_scale;
-    a.causal = causal != 0;
-    a.window = window;
-    a.lse = lse;
-    a.stream = static_cast<cudaStream_t>(stream);
-    return cuda_status(launch_paged_attention(a, workspace));
+    return attend(dtype, cache_dtype == BEVPOOL_E4M3 ? kCacheE4M3 : kCacheSame, {q, q_token_stride, q_head_stride}, k_cache, v_cache, page_stride, slot_stride, head_stride, nullptr, nullptr,
+                  n_pages, page_size, block_table, table_pages, kv_len, cu_q, n_seqs, n_tokens, n_q_heads, n_k_heads, head_dim, max_q_len,
+                  max_kv_len, scale, causal, window, k_scale, v_scale, {out, out_token_stride, out_head_stride}, lse, workspace, workspace_bytes,
+                  stream);
+}
+
+bevpool_status bevpool_paged_attention_scaled(
+    bevpool_dtype dtype, const void *q, int64_t q_token_stride, int64_t q_head_stride, const void *k_cache,
+    const void *v_cache, int64_t page_stride, int64_t slot_stride, int64_t head_stride, const float *k_scales,
+    const float *v_scales, int32_t n_pages, int32_t page_size, const int32_t *block_table, int32_t table_pages,
+    const int32_t *kv_len, const int32_t *cu_q, int32_t n_seqs, int32_t n_tokens, int32_t n_q_heads, int32_t n_k_heads,
+    int32_t head_dim, int32_t max_q_len, int32_t max_kv_len, float scale, int32_t causal, int32_t window, void *out,
+    int64_t out_token_stride, int64_t out_head_stride, float *lse, void *workspace, size_t workspace_bytes, void *stream) {
+    if (!dtype_ok(dtype)) return BEVPOOL_ERR_UNSUPPORTED;
+    return attend(dtype, kCacheScaled, {q, q_token_stride, q_head_stride}, k_cache, v_cache, page_stride, slot_stride, head_stride, k_scales, v_scales,
+                  n_pages, page_size, block_table, table_pages, kv_len, cu_q, n_seqs, n_tokens, n_q_heads, n_k_heads, head_dim, max_q_len,
+                  max_kv_len, scale, causal, window, 1.0f, 1.0f, {out, out_token_stride, out_head_stride}, lse, workspace, workspace_bytes,
+                  stream);
 }
 
 bevpool_status bevpool_attention_timeouts(int64_t *h_count) {

@@ -623,6 +623,27 @@ BEVPOOL_API bevpool_status bevpool_paged_attention(
     float v_scale, void *out, int64_t out_token_stride, int64_t out_head_stride, float *lse, void *workspace,
     size_t workspace_bytes, void *stream);
 
+/*
+ * bevpool_paged_attention over a cache of E4M3 codes with a scale for each page
+ * and key head: key = code * k_scales[page][head], value = code *
+ * v_scales[page][head], as bevpool_kv_append_scaled makes it.
+ *   k_scales, v_scales  device float [n_pages][n_k_heads], within [2^-48, 2^48]
+ *                       (others count as the nearest bound, NaN as the lower);
+ *   scale               > 0, scale * 2^48 finite.
+ * The weights are rounded to 16 bits with their value's scale in them: relatively,
+ * so that pages of small values lose no more than others, down to 2^-28 of the
+ * largest weight times scale that a token sees (2^-21 in tiles of many rows; no end
+ * in tiles of bf16 heads), and by 2^-39 (2^-32) of that one below.  The workspace is
+ * that of bevpool_paged_attention; other arguments too.
+ */
+BEVPOOL_API bevpool_status bevpool_paged_attention_scaled(
+    bevpool_dtype dtype, const void *q, int64_t q_token_stride, int64_t q_head_stride, const void *k_cache,
+    const void *v_cache, int64_t page_stride, int64_t slot_stride, int64_t head_stride, const float *k_scales,
+    const float *v_scales, int32_t n_pages, int32_t page_size, const int32_t *block_table, int32_t table_pages,
+    const int32_t *kv_len, const int32_t *cu_q, int32_t n_seqs, int32_t n_tokens, int32_t n_q_heads, int32_t n_k_heads,
+    int32_t head_dim, int32_t max_q_len, int32_t max_kv_len, float scale, int32_t causal, int32_t window, void *out,
+    int64_t out_token_stride, int64_t out_head_stride, float *lse, void *workspace, size_t workspace_bytes, void *stream);
+
 /* Waits inside the attention kernels that ran out since the library was loaded
  * (0 unless the device misbehaves: every wait is bounded, and a CTA whose wait
  * runs out writes NaN to its rows).  h_count: host; the call synchronises with

@@ -14,8 +14,10 @@ Bounds (u, and what an element of a normed and turned key may be off, e =
     the value's scale, s the score in base 2.  Besides the score's own error d
     (token_ref) three FP32 roundings of numbers up to max|s| + max|log2 scale|
     each way: at most 2^-22 of the sum of both, relatively, in w and again in
-    the sum.  fp16 weights below 2^-14 of their type's range are off by 2^-24 of
-    the largest w: 2^-24 max w sum|code| / l.
+    the sum.  fp16 weights below 2^-14 are subnormal and off by 2^-25: of 2^14
+    times the largest w over few rows (whatever the heads' type), which is 2^-39
+    of it, of 2^7 times it or 1 elsewhere (fp16 heads); 2^-38 and 2^-24 of max w
+    sum|code| / l cover these.
 """
 import numpy as np
 import torch
@@ -129,7 +131,7 @@ def attention(q, k_cache, v_cache, k_scales, v_scales, block_table, kv_len, cu_q
                 l = p.sum(-1, keepdim=True)
                 o, mag = (p * f / l) @ code, (p * f / l) @ code.abs()
                 out[t, rows], lse[t, rows] = o, (m + torch.log(l))[:, 0]
-                sub = 2.0 ** -24 * (p * f).max(-1, keepdim=True).values * code.abs().sum(0)[None] / l if dtype == torch.float16 else 0.0
+                sub = 2.0 ** (-24 if dtype == torch.float16 else -38) * (p * f).max(-1, keepdim=True).values * code.abs().sum(0)[None] / l
                 tol[t, rows] = (u + 2 * d[:, None] + 2.0 ** -18) * mag + sub + u * o.abs() + ref.tiny(dtype)
                 lse_tol[t, rows] = d + 2.0 ** -18 + 2.0 ** -22 * lse[t, rows].abs()
     return out, lse, tol, lse_tol, done
