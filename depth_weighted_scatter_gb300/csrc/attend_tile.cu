@@ -7,7 +7,7 @@ namespace bevpool {
 cudaError_t attend_tile_timeouts(int64_t *count) { return timeouts_here(count); }
 
 cudaError_t launch_attend_tile(const AttnArgs &a, const AttnPlan &pl) {
-    return a.cache == kCacheSame ? launch_attend_tile_of<kCacheSame>(a, pl) : launch_attend_tile_of<kCacheE4M3>(a, pl);
+    return a.cache == kCacheSame ? launch_attend_tile_of<kCacheSame, 1>(a, pl) : launch_attend_tile_of<kCacheE4M3, 1>(a, pl);
 }
 
 }  // namespace bevpool

@@ -123,7 +123,9 @@ struct TileBars {                          // shared memory
     uint64_t q_full[2], s_full[2], p_full[2][2], s_read[2], o_full[2], turn[2], drain[2];
     uint32_t tmem, failed;
     TilePiece piece[2];                    // the one at work and the next
-    float4 factors[8][kBlock / 16];        // kCacheScaled, a softmax warp's own: its block's groups' score, lift, sum
+    // kCacheScaled, a softmax warp's own: its block's groups' score twice, lift twice; sum twice
+    float4 factors[8][kBlock / 16];
+    float2 sums[8][kBlock / 16];
     TileWalk walk;
     int64_t scan[16];
 };
@@ -269,14 +271,44 @@ __device__ __forceinline__ void init_bars(TileBars &bars, bool again) {
     bar_init_fence();
 }
 
+// A row of bf16 queries in shared memory (D / 64 runs of 128 bytes, 16-byte pieces
+// swapped by swz) to fp16, scaled by the power of two that brings its largest element
+// to 2^14: elements 2^-31 of it and more keep all their bits.  Returns the inverse.
+template <int D>
+__device__ __forceinline__ float row_to_half(uint32_t row, int swz) {
+    const auto piece = [&](int c) { return row + (c >> 3) * (kTileRows * 128) + (((c & 7) ^ swz) << 4); };
+    float top = 0.0f;
+#pragma unroll 4
+    for (int c = 0; c < D / 8; ++c) {
+        uint32_t w[4];
+        asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(piece(c)) : "memory");
+#pragma unroll
+        for (int i = 0; i < 4; ++i) top = max3(top, fabsf(__uint_as_float(w[i] << 16)), fabsf(__uint_as_float(w[i] & 0xffff0000u)));
+    }
+    const int e = min(max(static_cast<int>(__float_as_uint(top) >> 23) - 127, -100), 100);
+    const float up = __uint_as_float(static_cast<uint32_t>(127 + 14 - e) << 23);           // 2^(14 - e)
+#pragma unroll 4
+    for (int c = 0; c < D / 8; ++c) {
+        uint32_t w[4];
+        asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(piece(c)) : "memory");
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = pack2<__half>(__uint_as_float(w[i] << 16) * up, __uint_as_float(w[i] & 0xffff0000u) * up);
+        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(piece(c)), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
+    }
+    return __uint_as_float(static_cast<uint32_t>(127 - 14 + e) << 23);
+}
+
 enum { kSoftmax, kProducts, kLoads };
 
-// A role's part of one piece; false where a wait ran out.
-template <typename T, int C, int D, bool SHARED, int ROLE>
+// A role's part of one piece; false where a wait ran out.  NG: groups of a block's
+// keys that have page scales of their own (kCacheScaled): 1 for pages of 128 and 256
+// slots, 2 for 64, 8 for less.
+template <typename T, int C, int NG, int D, bool SHARED, int ROLE>
 __device__ __forceinline__ bool attend_piece(const AttnArgs &a, const AttnPlan &pl, const CUtensorMap &k_map,
                                              const CUtensorMap &v_map, TileBars &bars, int piece, uint32_t smem) {
     constexpr bool E4M3 = C != kCacheSame, SCALED = C == kCacheScaled;
     using S = TileShape<E4M3, D>;
+    using M = typename std::conditional<SCALED, __half, T>::type;          // type of both products
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const TilePiece pc = bars.piece[piece];
     const int hk = pc.hk, b = pc.b;
@@ -300,6 +332,7 @@ __device__ __forceinline__ bool attend_piece(const AttnArgs &a, const AttnPlan &
         int32_t lo = 0, hi = INT32_MAX;                                    // a place past the last row sees all, and is not kept
         int64_t token = 0;
         int32_t h = 0;
+        float q_factor = 1.0f;                                             // of this row's scores, as its queries were scaled
         if (used) {
             const int32_t i = row / a.G;
             token = r.q0 + i;
@@ -324,6 +357,10 @@ __device__ __forceinline__ bool attend_piece(const AttnArgs &a, const AttnPlan &
                              : "memory");
             }
             asm volatile("cp.async.wait_all;" ::: "memory");
+            if constexpr (!std::is_same<M, T>::value) {
+                __syncwarp();
+                q_factor = row_to_half<D>(q_smem + t * S::Q_BYTES + tid * 128, tid & 7);
+            }
             fence_shared_async();
             bar_arrive(shared_addr(&bars.q_full[t]));
         }
@@ -344,42 +381,64 @@ __device__ __forceinline__ bool attend_piece(const AttnArgs &a, const AttnPlan &
             return hole;
         };
         bool hole = !SCALED && tr.b1 > tr.b0 ? holes_of(tr.b0) : false;
-        // With scales: the page of a lane's group two blocks ahead (-1: none; past
-        // the last key any), its scales one.
-        auto page_of = [&](int32_t j) {
-            const int32_t k = j * kBlock + lane * 16;
-            const int32_t p = j < tr.b1 && lane < kBlock / 16 && k < r.kv_len ? table[k >> a.pg.page_shift] : 0;
-            return p < a.pg.n_pages ? p : -1;
-        };
-        int32_t page = 0, page_next = 0;
-        float ks = 1.0f, vs = 1.0f;
-        auto scales_of = [&](int32_t p) {
-            const int64_t i = static_cast<int64_t>(max(p, 0)) * a.Hk + hk;
-            if (lane < kBlock / 16) {
-                ks = a.k_scales[i];
-                vs = a.v_scales[i];
+        // With scales: the pages of a block's groups are looked up two blocks ahead (-1:
+        // none; past the last key any), their scales one.  Few groups: all lanes have all
+        // of them; eight: lane g has group g's, and the factors go through shared memory.
+        constexpr int KEEP = NG == 8 ? 1 : NG;
+        auto pages_of = [&](int32_t j, int32_t *p) {
+#pragma unroll
+            for (int g = 0; g < KEEP; ++g) {
+                const int32_t k = j * kBlock + (NG == 8 ? lane & 7 : g) * (kBlock / NG);
+                p[g] = j < tr.b1 && k < r.kv_len ? table[k >> a.pg.page_shift] : 0;
+                if (p[g] >= a.pg.n_pages) p[g] = -1;
             }
         };
-        const uint32_t factors = shared_addr(&bars.factors[warp][0]);
+        int32_t page[KEEP], page_next[KEEP];
+        float ks[KEEP], vs[KEEP];
+        auto scales_of = [&](const int32_t *p) {
+#pragma unroll
+            for (int g = 0; g < KEEP; ++g) {
+                const int64_t i = static_cast<int64_t>(max(p[g], 0)) * a.Hk + hk;
+                ks[g] = a.k_scales[i];
+                vs[g] = a.v_scales[i];
+            }
+        };
+        const uint32_t factors = shared_addr(&bars.factors[warp][0]), sums = shared_addr(&bars.sums[warp][0]);
         if constexpr (SCALED) {
-            page = page_of(tr.b0);
-            page_next = page_of(tr.b0 + 1);
+            pages_of(tr.b0, page);
+            pages_of(tr.b0 + 1, page_next);
             scales_of(page);
         }
         uint32_t phase = 0;
         for (int32_t j = tr.b0; j < tr.b1; ++j, phase ^= 1) {
+            PageFactors kept[KEEP];
+            uint32_t holes = 0;
             if constexpr (SCALED) {
-                hole = page < 0;
-                const PageFactors f = page_factors(a.scale_log2, ks, vs);
-                if (lane < kBlock / 16)
-                    asm volatile("st.shared.v4.f32 [%0], {%1,%2,%3,%3};" ::"r"(factors + lane * 16), "f"(f.score), "f"(f.lift), "f"(f.sum)
-                                 : "memory");
-                __syncwarp();
-                page = page_next;
+#pragma unroll
+                for (int g = 0; g < KEEP; ++g) {
+                    kept[g] = page_factors(a.scale_log2, ks[g], vs[g]);
+                    if (NG < 8 && page[g] < 0) holes |= ((1u << (8 / NG)) - 1) << (g * (8 / NG));
+                }
+                if constexpr (NG == 8) {
+                    holes = __ballot_sync(0xffffffffu, page[0] < 0) & 0xff;
+                    __syncwarp();                                          // the last block's are read
+                    if (lane < 8) {
+                        asm volatile("st.shared.v4.f32 [%0], {%1,%1,%2,%2};" ::"r"(factors + lane * 16), "f"(kept[0].score), "f"(kept[0].lift)
+                                     : "memory");
+                        asm volatile("st.shared.v2.f32 [%0], {%1,%1};" ::"r"(sums + lane * 8), "f"(kept[0].sum) : "memory");
+                    }
+                    __syncwarp();
+                } else if (!std::is_same<M, T>::value) {
+#pragma unroll
+                    for (int g = 0; g < KEEP; ++g) kept[g].score *= q_factor;
+                }
+#pragma unroll
+                for (int g = 0; g < KEEP; ++g) page[g] = page_next[g];
                 scales_of(page);
-                page_next = page_of(j + 2);
+                pages_of(j + 2, page_next);
+            } else {
+                holes = __ballot_sync(0xffffffffu, hole);
             }
-            const uint32_t holes = __ballot_sync(0xffffffffu, hole);
             if (!SCALED && j + 1 < tr.b1) hole = holes_of(j + 1);
             ok = bar_wait(shared_addr(&bars.s_full[t]), phase);
             if (!__all_sync(0xffffffffu, ok)) {
@@ -391,15 +450,17 @@ __device__ __forceinline__ bool attend_piece(const AttnArgs &a, const AttnPlan &
 #pragma unroll
             for (int c = 0; c < kBlock; c += 32) tmem_ld32(s_mem + c, s + c);
             tmem_wait_ld();
-            if constexpr (S::AHEAD) {                                      // S may be made again
+            const auto s_done = [&]() {                                    // S may be made again
                 tmem_fence_before();
                 bar_arrive(shared_addr(&bars.s_read[t]));
-            }
+            };
+            if constexpr (S::AHEAD && !SCALED) s_done();
             const int32_t k0 = j * kBlock;
-            if (!__all_sync(0xffffffffu, holes == 0 && lo <= k0 && hi - kBlock >= k0)) {
+            const bool masked = !__all_sync(0xffffffffu, holes == 0 && lo <= k0 && hi - kBlock >= k0);
+            auto mask = [&](int from_word, int to_word) {
                 // seen keys of the block, 32 a word
 #pragma unroll
-                for (int w = 0; w < kBlock / 32; ++w) {
+                for (int w = from_word; w < to_word; ++w) {
                     const int from = min(max(lo - k0 - 32 * w, 0), 32), to = min(max(hi - k0 - 32 * w, 0), 32);
                     uint32_t seen = static_cast<uint32_t>((1ull << to) - 1) & ~static_cast<uint32_t>((1ull << from) - 1);
                     if ((holes >> (2 * w)) & 1) seen &= 0xffff0000u;
@@ -407,14 +468,29 @@ __device__ __forceinline__ bool attend_piece(const AttnArgs &a, const AttnPlan &
 #pragma unroll
                     for (int c = 0; c < 32; ++c) s[32 * w + c] = (seen >> c) & 1 ? s[32 * w + c] : 0xff800000u;   // -inf
                 }
-            }
+            };
+            if (masked) mask(0, kBlock / 32);
+            // Factors of the 16 keys from 16 g on, each twice.
+            struct Twice {
+                uint64_t score, lift;
+            };
             auto factors_of = [&](int g) {
-                PageFactors f;
-                float rest;
-                asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];"
-                             : "=f"(f.score), "=f"(f.lift), "=f"(f.sum), "=f"(rest)
-                             : "r"(factors + g * 16)
-                             : "memory");
+                Twice f;
+                if constexpr (NG == 8) {
+                    asm volatile("ld.shared.v2.b64 {%0,%1}, [%2];" : "=l"(f.score), "=l"(f.lift) : "r"(factors + g * 16) : "memory");
+                    if constexpr (!std::is_same<M, T>::value) f.score = mul2(f.score, pair(q_factor, q_factor));
+                } else {
+                    const PageFactors &x = kept[g * NG / 8];
+                    f = {pair(x.score, x.score), pair(x.lift, x.lift)};
+                }
+                return f;
+            };
+            auto sum_of = [&](int g) {
+                uint64_t f;
+                if constexpr (NG == 8)
+                    asm volatile("ld.shared.b64 %0, [%1];" : "=l"(f) : "r"(sums + g * 8) : "memory");
+                else
+                    f = pair(kept[g * NG / 8].sum, kept[g * NG / 8].sum);
                 return f;
             };
             // P of one half and its sum, at the scale m.
@@ -422,25 +498,27 @@ __device__ __forceinline__ bool attend_piece(const AttnArgs &a, const AttnPlan &
             auto weights = [&](int h, uint32_t *p) {
                 const float base2 = m == -INFINITY ? 0.0f : -m;
                 if constexpr (SCALED) {
-                    uint64_t total = pair(0.0f, 0.0f);
+                    const uint64_t base = pair(base2, base2);
+                    uint64_t u = pair(0.0f, 0.0f), v = u;
 #pragma unroll
                     for (int g = 0; g < 4; ++g) {
-                        const PageFactors f = factors_of(4 * h + g);
-                        const uint64_t by = pair(f.score, f.score), from = pair(f.lift + base2, f.lift + base2);
-                        uint64_t u = pair(0.0f, 0.0f);
+                        const Twice f = factors_of(4 * h + g);
+                        const uint64_t from = add2(f.lift, base), by = sum_of(4 * h + g);
 #pragma unroll
-                        for (int c = 0; c < 8; ++c) {
-                            const int at = h * 64 + g * 16 + 2 * c;
+                        for (int c = g * 8; c < g * 8 + 8; ++c) {
+                            const int at = h * 64 + 2 * c;
                             float x, y;
-                            unpair(fma2(pair(__uint_as_float(s[at]), __uint_as_float(s[at + 1])), by, from), &x, &y);
+                            unpair(fma2(pair(__uint_as_float(s[at]), __uint_as_float(s[at + 1])), f.score, from), &x, &y);
                             x = pow2(x);
                             y = pow2(y);
-                            u = c == 0 ? pair(x, y) : add2(u, pair(x, y));
-                            p[g * 8 + c] = pack2<T>(x, y);
+                            if (c & 1)
+                                v = fma2(pair(x, y), by, v);
+                            else
+                                u = fma2(pair(x, y), by, u);
+                            p[c] = pack2<M>(x, y);
                         }
-                        total = fma2(u, pair(f.sum, f.sum), total);
                     }
-                    return total;
+                    return add2(u, v);
                 }
                 const uint64_t from2 = pair(base2, base2);
                 uint64_t u = pair(0.0f, 0.0f), v = u;
@@ -455,7 +533,7 @@ __device__ __forceinline__ bool attend_piece(const AttnArgs &a, const AttnPlan &
                         v = add2(v, pair(x, y));
                     else
                         u = add2(u, pair(x, y));
-                    p[c] = pack2<T>(x, y);
+                    p[c] = pack2<M>(x, y);
                 }
                 return add2(u, v);
             };
@@ -477,14 +555,32 @@ __device__ __forceinline__ bool attend_piece(const AttnArgs &a, const AttnPlan &
             float top;
             if constexpr (SCALED) {
                 top = -INFINITY;
+                constexpr int KEYS = kBlock / NG;
 #pragma unroll
-                for (int g = 0; g < kBlock / 16; ++g) {
-                    const PageFactors f = factors_of(g);
-                    const auto at = [&](int c) { return __uint_as_float(s[g * 16 + c]); };
-                    float x = at(0), y = at(1);
+                for (int g = 0; g < NG; ++g) {
+                    const auto at = [&](int c) { return __uint_as_float(s[g * KEYS + c]); };
+                    constexpr int W = KEYS == 16 ? 2 : 4;                  // chains
+                    float x[W];
 #pragma unroll
-                    for (int c = 2; c < 14; c += 4) x = max3(x, at(c), at(c + 1)), y = max3(y, at(c + 2), at(c + 3));
-                    top = fmaxf(top, fmaf(fmaxf(max3(x, at(14), at(15)), y), f.score, f.lift));
+                    for (int i = 0; i < W; ++i) x[i] = max3(at(i), at(W + i), at(2 * W + i));
+#pragma unroll
+                    for (int c = 3 * W; c + 2 * W <= KEYS; c += 2 * W)
+#pragma unroll
+                        for (int i = 0; i < W; ++i) x[i] = max3(x[i], at(c + i), at(c + W + i));
+                    if constexpr ((KEYS / W - 3) % 2 == 1)
+#pragma unroll
+                        for (int i = 0; i < W; ++i) x[i] = fmaxf(x[i], at(KEYS - W + i));
+                    const float y = W == 2 ? fmaxf(x[0], x[1]) : fmaxf(max3(x[0], x[1], x[2]), x[W - 1]);
+                    float score, lift, rest;
+                    if constexpr (NG == 8) {
+                        const Twice f = factors_of(g);
+                        unpair(f.score, &score, &rest);
+                        unpair(f.lift, &lift, &rest);
+                    } else {
+                        score = kept[g].score;
+                        lift = kept[g].lift;
+                    }
+                    top = fmaxf(top, fmaf(y, score, lift));
                 }
             } else {
                 float mx[4];
@@ -508,9 +604,9 @@ __device__ __forceinline__ bool attend_piece(const AttnArgs &a, const AttnPlan &
                 }
                 tmem_fence_after();
             }
-            const bool grown = top > m + kMost<T> || (m == -INFINITY && top > m);
+            const bool grown = top > m + kMost<M> || (m == -INFINITY && top > m);
             if (__any_sync(0xffffffffu, grown)) {
-                const float mn = grown ? top - kLift<T> : m;
+                const float mn = grown ? top - kLift<M> : m;
                 const float f = grown ? pow2(m - mn) : 1.0f;               // m = -inf: 0
                 m = mn;
                 if (j > tr.b0) {
@@ -525,8 +621,15 @@ __device__ __forceinline__ bool attend_piece(const AttnArgs &a, const AttnPlan &
                         tmem_st8(o_mem + c, o);
                     }
                 }
+                if constexpr (SCALED) {                                    // S is read again: its first half was not kept
+                    tmem_ld32(s_mem, s);
+                    tmem_ld32(s_mem + 32, s + 32);
+                    tmem_wait_ld();
+                    if (masked) mask(0, 2);
+                }
                 part = weights(0, p);
             }
+            if constexpr (S::AHEAD && SCALED) s_done();
             release(0, p);
             sum = add2(sum, part);
             part = weights(1, p);
@@ -645,7 +748,7 @@ __device__ __forceinline__ bool attend_piece(const AttnArgs &a, const AttnPlan &
         // A warp a tile: while one waits the other's products run.
         const int t = warp - 8;
         const TileRange tr = t == 0 ? t0 : t1;
-        constexpr int format = std::is_same<T, __half>::value ? 0 : 1;
+        constexpr int format = std::is_same<M, __half>::value ? 0 : 1;
         constexpr uint32_t s_desc = mma_desc(format, kBlock, false), o_desc = mma_desc(format, D, true);
         auto in = [&](int32_t j) { return j >= tr.b0 && j < tr.b1; };
         const uint32_t s_bar = shared_addr(&bars.s_full[t]), p_bar = shared_addr(&bars.p_full[t][0]);
@@ -874,7 +977,11 @@ __device__ __forceinline__ bool attend_piece(const AttnArgs &a, const AttnPlan &
         constexpr int CPR = D / 16;                                        // 16-byte pieces of a row of codes
         constexpr int RPI = S::LOADERS * 32 / CPR;                         // rows in one step of all loader warps
         constexpr int N = kBlock / RPI;
-        const int tid = threadIdx.x - 12 * 32, c = tid % CPR, row_i = tid / CPR;
+        // Eight lanes that store together have four pieces of a half in two rows: eight
+        // places of the swizzle.
+        const int tid = threadIdx.x - 12 * 32;
+        const int c = SCALED && CPR == 8 ? (lane & 3) | ((lane >> 4) << 2) : tid % CPR;
+        const int row_i = SCALED && CPR == 8 ? (tid >> 5) * 4 + ((lane >> 2) & 3) : tid / CPR;
         uint32_t at = 0, lap = 0;
         // Codes arrive by asynchronous copies two blocks ahead, each thread's own
         // pieces at its own place, so that it needs no other to widen them.
@@ -922,7 +1029,7 @@ __device__ __forceinline__ bool attend_piece(const AttnArgs &a, const AttnPlan &
 #pragma unroll
                 for (int y = 0; y < 8; ++y) {
                     const uint32_t codes = (u[y >> 1] >> (16 * (y & 1))) & 0xffffu;
-                    x[y] = widen2<T>(codes);
+                    x[y] = widen2<M>(codes);
                 }
 #pragma unroll
                 for (int y = 0; y < 2; ++y)
@@ -979,7 +1086,7 @@ __device__ __forceinline__ void sync_roles() {
 }
 
 // A role's part of all of the CTA's pieces; true where a wait ran out.
-template <typename T, int C, int D, bool SHARED, int ROLE>
+template <typename T, int C, int NG, int D, bool SHARED, int ROLE>
 __device__ __forceinline__ bool attend_pieces(const AttnArgs &a, const AttnPlan &pl, const CUtensorMap &k_map,
                                               const CUtensorMap &v_map, TileBars &bars, uint32_t smem) {
     constexpr bool E4M3 = C != kCacheSame;
@@ -987,7 +1094,7 @@ __device__ __forceinline__ bool attend_pieces(const AttnArgs &a, const AttnPlan 
     bool failed = false;
     for (int piece = 0; !SHARED || bars.piece[piece].b >= 0; piece ^= 1) {
         if (!SHARED || !failed) {
-            const bool ok = attend_piece<T, C, D, SHARED, ROLE>(a, pl, k_map, v_map, bars, piece, smem);
+            const bool ok = attend_piece<T, C, NG, D, SHARED, ROLE>(a, pl, k_map, v_map, bars, piece, smem);
             if (!ok) bars.failed = 1;
         } else if (ROLE == kSoftmax && threadIdx.x == 0) {
             bars.piece[piece ^ 1] = next_piece(a, pl, bars.walk);
@@ -1017,7 +1124,7 @@ __device__ __forceinline__ bool attend_pieces(const AttnArgs &a, const AttnPlan 
     return failed;
 }
 
-template <typename T, int C, int D, bool SHARED>
+template <typename T, int C, int NG, int D, bool SHARED>
 __global__ void __launch_bounds__(TileShape<C != kCacheSame, D>::THREADS, 1)
 k_attend_tile(AttnArgs a, AttnPlan pl, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
     constexpr bool E4M3 = C != kCacheSame;
@@ -1060,13 +1167,13 @@ k_attend_tile(AttnArgs a, AttnPlan pl, const __grid_constant__ CUtensorMap k_map
     bool failed = false;
     if (warp < 8) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(S::SOFTMAX_REGS));
-        failed = attend_pieces<T, C, D, SHARED, kSoftmax>(a, pl, k_map, v_map, bars, smem);
+        failed = attend_pieces<T, C, NG, D, SHARED, kSoftmax>(a, pl, k_map, v_map, bars, smem);
     } else if (warp < 12) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::PRODUCT_REGS));
-        failed = attend_pieces<T, C, D, SHARED, kProducts>(a, pl, k_map, v_map, bars, smem);
+        failed = attend_pieces<T, C, NG, D, SHARED, kProducts>(a, pl, k_map, v_map, bars, smem);
     } else if constexpr (E4M3) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::LOADER_REGS));
-        failed = attend_pieces<T, C, D, SHARED, kLoads>(a, pl, k_map, v_map, bars, smem);
+        failed = attend_pieces<T, C, NG, D, SHARED, kLoads>(a, pl, k_map, v_map, bars, smem);
     }
     if (warp == 8) tmem_free<512>(bars.tmem);
     if (failed && threadIdx.x == 0) atomicAdd(&g_attention_timeouts, 1ull);
@@ -1124,23 +1231,23 @@ cudaError_t timeouts_here(int64_t *count) {
 }
 
 // The launch of one of the caches' kernels.
-template <typename T, int C, int D, bool SHARED>
+template <typename T, int C, int NG, int D, bool SHARED>
 cudaError_t run_attend_tile(const AttnArgs &a, const AttnPlan &pl, dim3 grid) {
     using S = TileShape<C != kCacheSame, D>;
     CUtensorMap k_map = {}, v_map = {};
     if (C == kCacheSame && (!cache_map(a, a.k_cache, false, &k_map) || !cache_map(a, a.v_cache, true, &v_map))) return cudaErrorInvalidValue;
-    const cudaError_t e = allow_smem<&k_attend_tile<T, C, D, SHARED>>(S::SMEM);
+    const cudaError_t e = allow_smem<&k_attend_tile<T, C, NG, D, SHARED>>(S::SMEM);
     if (e != cudaSuccess) return e;
-    k_attend_tile<T, C, D, SHARED><<<grid, S::THREADS, S::SMEM, a.stream>>>(a, pl, k_map, v_map);
+    k_attend_tile<T, C, NG, D, SHARED><<<grid, S::THREADS, S::SMEM, a.stream>>>(a, pl, k_map, v_map);
     count_launch();
     return cudaGetLastError();
 }
 
-template <int C>
+template <int C, int NG>
 cudaError_t launch_attend_tile_of(const AttnArgs &a, const AttnPlan &pl) {
     auto run = [&](auto t, auto d) {
-        if (pl.share) return run_attend_tile<decltype(t), C, decltype(d)::value, true>(a, pl, dim3(static_cast<unsigned>(pl.share)));
-        return run_attend_tile<decltype(t), C, decltype(d)::value, false>(
+        if (pl.share) return run_attend_tile<decltype(t), C, NG, decltype(d)::value, true>(a, pl, dim3(static_cast<unsigned>(pl.share)));
+        return run_attend_tile<decltype(t), C, NG, decltype(d)::value, false>(
             a, pl, dim3(static_cast<unsigned>(pl.tiles * a.Hk), static_cast<unsigned>(pl.n_chunks), static_cast<unsigned>(a.pg.n_seqs)));
     };
     auto by_d = [&](auto t) {

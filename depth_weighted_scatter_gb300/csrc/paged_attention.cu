@@ -123,8 +123,14 @@ cudaError_t launch_paged_attention(const AttnArgs &args, void *workspace) {
     a.part_ml = a.part_o + pl.parts * a.D;
     a.cut = reinterpret_cast<int2 *>(a.part_ml + pl.parts * 2);
     const bool scaled = a.cache == kCacheScaled;
-    const cudaError_t e = pl.few ? (scaled ? launch_attend_few_scaled(a, pl) : launch_attend_few(a, pl))
-                                 : (scaled ? launch_attend_tile_scaled(a, pl) : launch_attend_tile(a, pl));
+    cudaError_t e;
+    if (pl.few)
+        e = scaled ? launch_attend_few_scaled(a, pl) : launch_attend_few(a, pl);
+    else if (!scaled)
+        e = launch_attend_tile(a, pl);
+    else
+        e = a.pg.page_size >= 128 ? launch_attend_tile_scaled_1(a, pl)
+            : a.pg.page_size == 64 ? launch_attend_tile_scaled_2(a, pl) : launch_attend_tile_scaled_8(a, pl);
     if (e != cudaSuccess || pl.parts == 0) return e;
     return launch_attend_join(a, pl);
 }
@@ -133,7 +139,9 @@ cudaError_t attention_timeouts(int64_t *count) {
     int64_t n = 0;
     cudaError_t e = cudaDeviceSynchronize();               // a copy alone leaves out streams that do not wait for the default one
     if (e == cudaSuccess) e = attend_tile_timeouts(&n);
-    if (e == cudaSuccess) e = attend_tile_scaled_timeouts(&n);
+    if (e == cudaSuccess) e = attend_tile_scaled_1_timeouts(&n);
+    if (e == cudaSuccess) e = attend_tile_scaled_2_timeouts(&n);
+    if (e == cudaSuccess) e = attend_tile_scaled_8_timeouts(&n);
     if (e == cudaSuccess) *count = n;
     return e;
 }

@@ -51,10 +51,14 @@ AttnPlan attention_plan(const AttnSizes &z);
 cudaError_t launch_attend_few(const AttnArgs &a, const AttnPlan &pl);      // attend_few.cu
 cudaError_t launch_attend_few_scaled(const AttnArgs &a, const AttnPlan &pl);       // attend_few_scaled.cu: kCacheScaled
 cudaError_t launch_attend_tile(const AttnArgs &a, const AttnPlan &pl);     // attend_tile.cu
-cudaError_t launch_attend_tile_scaled(const AttnArgs &a, const AttnPlan &pl);      // attend_tile_scaled.cu
-// Waits of the device's kernels that ran out, added to *count: of one cache and of the other.
+cudaError_t launch_attend_tile_scaled_1(const AttnArgs &a, const AttnPlan &pl);    // attend_tile_scaled_*.cu: by the groups of a
+cudaError_t launch_attend_tile_scaled_2(const AttnArgs &a, const AttnPlan &pl);    // block of keys that have scales of their own
+cudaError_t launch_attend_tile_scaled_8(const AttnArgs &a, const AttnPlan &pl);
+// Waits of each file's kernels that ran out, added to *count.
 cudaError_t attend_tile_timeouts(int64_t *count);
-cudaError_t attend_tile_scaled_timeouts(int64_t *count);
+cudaError_t attend_tile_scaled_1_timeouts(int64_t *count);
+cudaError_t attend_tile_scaled_2_timeouts(int64_t *count);
+cudaError_t attend_tile_scaled_8_timeouts(int64_t *count);
 cudaError_t attention_timeouts(int64_t *count);
 cudaError_t launch_attend_join(const AttnArgs &a, const AttnPlan &pl);     // attend_join.cu: where there are parts
 
