@@ -75,17 +75,19 @@ constexpr float kLift = std::is_same<T, __half>::value ? 7.0f : 0.0f;
 template <typename T>
 constexpr float kMost = std::is_same<T, __half>::value ? 15.0f : 8.0f;
 
-template <bool E4M3, int D>
+template <int C, int D>
 struct TileShape {
+    static constexpr bool E4M3 = C != kCacheSame, SCALED = C == kCacheScaled;
     // Warpgroups: two of softmax, one of products and TMA, and with E4M3 codes
     // one of loaders.  Registers a thread, by setmaxnreg; their sum is within
     // what the launch gives (168 a thread of 384, 128 of 512).
     static constexpr int LOADERS = E4M3 ? 4 : 1;                           // warps
+    static constexpr int ARRIVALS = SCALED ? 1 : 32;                       // of a warp at a barrier
     static constexpr int THREADS = E4M3 ? 512 : 384;
     static constexpr int LAUNCH_REGS = E4M3 ? 128 : 168;
-    static constexpr int SOFTMAX_REGS = E4M3 ? 184 : 208;
+    static constexpr int SOFTMAX_REGS = SCALED ? 200 : E4M3 ? 184 : 208;
     static constexpr int PRODUCT_REGS = E4M3 ? 56 : 80;
-    static constexpr int LOADER_REGS = 88;
+    static constexpr int LOADER_REGS = SCALED ? 56 : 88;
     static_assert(256 * SOFTMAX_REGS + 128 * PRODUCT_REGS + (E4M3 ? 128 * LOADER_REGS : 0) <= THREADS * LAUNCH_REGS,
                   "the split is within the launch's registers");
     static_assert(SOFTMAX_REGS >= LAUNCH_REGS && PRODUCT_REGS <= LAUNCH_REGS && (!E4M3 || LOADER_REGS <= LAUNCH_REGS),
@@ -98,7 +100,8 @@ struct TileShape {
     static constexpr int HALVES = D / 64;                                  // 128-byte columns of a block
     static constexpr int BLOCK_BYTES = kBlock * D * 2;
     static constexpr int STAGES = D == 64 ? 8 : E4M3 ? 4 : 5;              // K and V blocks in turn
-    static constexpr int RAW_BYTES = E4M3 ? 2 * kBlock * D : 0;            // two blocks of codes on their way
+    static constexpr int RAW_BLOCK = kBlock * D;
+    static constexpr int RAW_BYTES = E4M3 ? 2 * RAW_BLOCK : 0;             // two blocks of codes on their way
     static constexpr int Q_BYTES = kTileRows * D * 2;
     static constexpr int SMEM = 1024 + 2 * Q_BYTES + STAGES * BLOCK_BYTES + RAW_BYTES;     // 1024: alignment
 };
@@ -120,14 +123,17 @@ constexpr int32_t kStart = 4, kLeast = 6;  // kLeast: units of a share, at least
 
 struct TileBars {                          // shared memory
     uint64_t full[8], empty[8];            // ring
+    uint64_t raw_full[2], raw_empty[2];    // kCacheScaled: codes of K and of V
     uint64_t q_full[2], s_full[2], p_full[2][2], s_read[2], o_full[2], turn[2], drain[2];
     uint32_t tmem, failed;
     TilePiece piece[2];                    // the one at work and the next
     // kCacheScaled, a softmax warp's own: its block's groups' score twice, lift twice; sum twice
     float4 factors[8][kBlock / 16];
-    float2 sums[8][kBlock / 16];
+    union {
+        float2 sums[8][kBlock / 16];
+        int64_t scan[16];                  // (used before)
+    };
     TileWalk walk;
-    int64_t scan[16];
 };
 
 // What a row tile sees of the blocks [p0, p1): [b0, b1).
@@ -248,22 +254,26 @@ __device__ __forceinline__ TilePiece next_piece(const AttnArgs &a, const AttnPla
 }
 
 // Every barrier, set up; `again`: once more, with nothing left that arrives.
-template <int STAGES, int FULL>
+template <typename S>
 __device__ __forceinline__ void init_bars(TileBars &bars, bool again) {
     const auto init = [&](uint64_t *bar, uint32_t n) {
         if (again) bar_end(shared_addr(bar));
         bar_init(shared_addr(bar), n);
     };
-    for (int i = 0; i < STAGES; ++i) {
-        init(&bars.full[i], FULL);
+    for (int i = 0; i < S::STAGES; ++i) {
+        init(&bars.full[i], S::E4M3 ? S::LOADERS * S::ARRIVALS : 1);
         init(&bars.empty[i], 2);
     }
     for (int t = 0; t < 2; ++t) {
-        init(&bars.q_full[t], kTileRows);
+        if (S::SCALED) {
+            init(&bars.raw_full[t], 1);
+            init(&bars.raw_empty[t], S::LOADERS);
+        }
+        init(&bars.q_full[t], 4 * S::ARRIVALS);
         init(&bars.s_full[t], 1);
-        init(&bars.p_full[t][0], kTileRows);
-        init(&bars.p_full[t][1], kTileRows);
-        init(&bars.s_read[t], kTileRows);
+        init(&bars.p_full[t][0], 4 * S::ARRIVALS);
+        init(&bars.p_full[t][1], 4 * S::ARRIVALS);
+        init(&bars.s_read[t], 4 * S::ARRIVALS);
         init(&bars.o_full[t], 1);
         init(&bars.turn[t], 1);
         init(&bars.drain[t], 1);
@@ -298,6 +308,17 @@ __device__ __forceinline__ float row_to_half(uint32_t row, int swz) {
     return __uint_as_float(static_cast<uint32_t>(127 - 14 + e) << 23);
 }
 
+// A warp's arrival, after all of its lanes: by each of them or by one.
+template <typename S>
+__device__ __forceinline__ void warp_arrive(uint32_t bar) {
+    if constexpr (S::ARRIVALS == 1) {
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) bar_arrive(bar);
+    } else {
+        bar_arrive(bar);
+    }
+}
+
 enum { kSoftmax, kProducts, kLoads };
 
 // A role's part of one piece; false where a wait ran out.  NG: groups of a block's
@@ -307,7 +328,7 @@ template <typename T, int C, int NG, int D, bool SHARED, int ROLE>
 __device__ __forceinline__ bool attend_piece(const AttnArgs &a, const AttnPlan &pl, const CUtensorMap &k_map,
                                              const CUtensorMap &v_map, TileBars &bars, int piece, uint32_t smem) {
     constexpr bool E4M3 = C != kCacheSame, SCALED = C == kCacheScaled;
-    using S = TileShape<E4M3, D>;
+    using S = TileShape<C, D>;
     using M = typename std::conditional<SCALED, __half, T>::type;          // type of both products
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const TilePiece pc = bars.piece[piece];
@@ -362,7 +383,7 @@ __device__ __forceinline__ bool attend_piece(const AttnArgs &a, const AttnPlan &
                 q_factor = row_to_half<D>(q_smem + t * S::Q_BYTES + tid * 128, tid & 7);
             }
             fence_shared_async();
-            bar_arrive(shared_addr(&bars.q_full[t]));
+            warp_arrive<S>(shared_addr(&bars.q_full[t]));
         }
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t s_mem = tmem + lanes + t * kBlock, p_mem = tmem + lanes + S::P_COL + t * S::P_STEP, o_mem = tmem + lanes + 2 * kBlock + t * D;
@@ -452,7 +473,7 @@ __device__ __forceinline__ bool attend_piece(const AttnArgs &a, const AttnPlan &
             tmem_wait_ld();
             const auto s_done = [&]() {                                    // S may be made again
                 tmem_fence_before();
-                bar_arrive(shared_addr(&bars.s_read[t]));
+                warp_arrive<S>(shared_addr(&bars.s_read[t]));
             };
             if constexpr (S::AHEAD && !SCALED) s_done();
             const int32_t k0 = j * kBlock;
@@ -544,7 +565,7 @@ __device__ __forceinline__ bool attend_piece(const AttnArgs &a, const AttnPlan &
                 for (int g = 0; g < 4; ++g) tmem_st8(p_mem + h * 32 + g * 8, p + g * 8);
                 tmem_wait_st();
                 tmem_fence_before();
-                bar_arrive(shared_addr(&bars.p_full[t][h]));
+                warp_arrive<S>(shared_addr(&bars.p_full[t][h]));
             };
             // The first half's weights are worked out at the scale in use while
             // the row's maximum is still being found (other units do that), and
@@ -914,8 +935,106 @@ __device__ __forceinline__ bool attend_piece(const AttnArgs &a, const AttnPlan &
         if (elect_one()) mma_commit(shared_addr(&bars.drain[t]));
         __syncwarp();
         ok = bar_wait(shared_addr(&bars.drain[t]), 0) && ok;
-    } else if (ROLE == kProducts && (E4M3 || warp == 11)) {
+    } else if (ROLE == kProducts && ((E4M3 && !SCALED) || warp == 11)) {
         if (SHARED && warp == 11 && lane == 0) bars.piece[piece ^ 1] = next_piece(a, pl, bars.walk);
+    } else if constexpr (SCALED && ROLE == kProducts) {
+        // ------------------------------------------------------------ TMA of codes
+        const int per = a.pg.page_size < kBlock ? kBlock / a.pg.page_size : 1;         // pages of a block, a box each
+        const int high = kBlock / per;
+        const uint32_t raw = ring + S::STAGES * S::BLOCK_BYTES + lane * high * D;
+        auto page_of = [&](int32_t j) {                                    // n_pages (the box fills with zeros) where there is none
+            const int32_t k = j * kBlock + lane * high;
+            int32_t p = a.pg.n_pages;
+            if (lane < per && j < j1 && k < r.kv_len) {
+                const int32_t x = table[k >> a.pg.page_shift];
+                if (x >= 0 && x < a.pg.n_pages) p = x;
+            }
+            return p;
+        };
+        int32_t page = page_of(j0);
+        uint32_t phase = 0, issued[2] = {0, 0};
+        for (int32_t j = j0; j < j1 && ok; ++j, phase ^= 1) {
+            const int32_t now = page, slot = (j * kBlock + lane * high) & (a.pg.page_size - 1);
+            page = page_of(j + 1);
+#pragma unroll
+            for (int kv = 0; kv < 2; ++kv) {
+                ok = bar_wait(shared_addr(&bars.raw_empty[kv]), phase ^ 1);
+                if (!__all_sync(0xffffffffu, ok)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t full = shared_addr(&bars.raw_full[kv]);
+                if (lane == 0) bar_expect(full, S::RAW_BLOCK);
+                __syncwarp();
+                if (lane < per) tma_load_4d(raw + kv * S::RAW_BLOCK, kv ? &v_map : &k_map, full, 0, slot, hk, now);
+                ++issued[kv];
+            }
+        }
+        // All copies landed before the CTA ends.
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv)
+            if (issued[kv] > 0) ok = bar_wait(shared_addr(&bars.raw_full[kv]), (issued[kv] - 1) & 1) && ok;
+    } else if constexpr (SCALED) {
+        // ------------------------------------------------------------ codes to 16 bits
+        // The eight lanes that read and store together have eight places of the swizzle
+        // on both sides: four pieces of a row's half, in two rows whose places differ in
+        // bits 0 and 2 (head_dim 64: bit 0).
+        constexpr int CPR = D / 16, RPI = S::LOADERS * 32 / CPR, N = kBlock / RPI;
+        const int w = warp - 12;
+        const int c = CPR == 8 ? (lane & 3) | ((lane >> 4) << 2) : lane & 3;
+        const int row_i = CPR == 8 ? (w >> 1) * 8 + (((w & 1) * 2 + ((lane >> 3) & 1)) ^ (((lane >> 2) & 1) * 5)) : w * 8 + (lane >> 2);
+        const uint32_t from = ring + S::STAGES * S::BLOCK_BYTES + row_i * D + (CPR == 8 ? c ^ (row_i & 7) : c) * 16;
+        const uint32_t to = (c >> 2) * (kBlock * 128) + row_i * 128;       // steps are whole groups of 8 rows: the swizzle stays
+        const uint32_t place[2] = {to + ((((c & 3) * 2) ^ (row_i & 7)) << 4), to + ((((c & 3) * 2 + 1) ^ (row_i & 7)) << 4)};
+        uint32_t at = 0, lap = 0, phase = 0;
+        for (int32_t j = j0; j < j1 && ok; ++j, phase ^= 1) {
+#pragma unroll
+            for (int kv = 0; kv < 2; ++kv) {
+                ok = bar_wait(shared_addr(&bars.raw_full[kv]), phase);
+                ok = ok && bar_wait(shared_addr(&bars.empty[at]), lap ^ 1);
+                if (!__all_sync(0xffffffffu, ok)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t src = from + kv * S::RAW_BLOCK, dst = ring + at * S::BLOCK_BYTES;
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    uint32_t u[4], x[8];
+                    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]) : "r"(src + i * (RPI * D))
+                                 : "memory");
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        x[2 * y] = widen2<M>(u[y] & 0xffffu);
+                        x[2 * y + 1] = widen2<M>(u[y] >> 16);
+                    }
+#pragma unroll
+                    for (int y = 0; y < 2; ++y)
+                        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(dst + place[y] + i * (RPI * 128)), "r"(x[4 * y]), "r"(x[4 * y + 1]),
+                                     "r"(x[4 * y + 2]), "r"(x[4 * y + 3])
+                                     : "memory");
+                }
+                const int live = r.kv_len - j * kBlock;                    // values past the request's last key: as in clear_tail
+                if (kv == 1 && live < kBlock) {
+                    for (int row = row_i; row < kBlock; row += RPI)
+                        if (row >= live)
+#pragma unroll
+                            for (int y = 0; y < 2; ++y)
+                                asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(dst + place[y] + (row - row_i) * 128), "r"(0) : "memory");
+                }
+                fence_shared_async();
+                warp_arrive<S>(shared_addr(&bars.full[at]));
+                if (lane == 0) bar_arrive(shared_addr(&bars.raw_empty[kv]));
+                if (++at == S::STAGES) {
+                    at = 0;
+                    lap ^= 1;
+                }
+            }
+        }
+        for (int i = 0; SHARED && i < S::STAGES && i < 2 * (j1 - j0) && ok; ++i) {     // every place let go of
+            if (at == 0) lap ^= 1;
+            at = at == 0 ? S::STAGES - 1 : at - 1;
+            ok = bar_wait(shared_addr(&bars.empty[at]), lap);
+        }
     } else if constexpr (!E4M3) {
         // ------------------------------------------------------------ TMA
         const int per = a.pg.page_size < kBlock ? kBlock / a.pg.page_size : 1;         // pages of a block
@@ -977,11 +1096,7 @@ __device__ __forceinline__ bool attend_piece(const AttnArgs &a, const AttnPlan &
         constexpr int CPR = D / 16;                                        // 16-byte pieces of a row of codes
         constexpr int RPI = S::LOADERS * 32 / CPR;                         // rows in one step of all loader warps
         constexpr int N = kBlock / RPI;
-        // Eight lanes that store together have four pieces of a half in two rows: eight
-        // places of the swizzle.
-        const int tid = threadIdx.x - 12 * 32;
-        const int c = SCALED && CPR == 8 ? (lane & 3) | ((lane >> 4) << 2) : tid % CPR;
-        const int row_i = SCALED && CPR == 8 ? (tid >> 5) * 4 + ((lane >> 2) & 3) : tid / CPR;
+        const int tid = threadIdx.x - 12 * 32, c = tid % CPR, row_i = tid / CPR;
         uint32_t at = 0, lap = 0;
         // Codes arrive by asynchronous copies two blocks ahead, each thread's own
         // pieces at its own place, so that it needs no other to widen them.
@@ -1089,8 +1204,7 @@ __device__ __forceinline__ void sync_roles() {
 template <typename T, int C, int NG, int D, bool SHARED, int ROLE>
 __device__ __forceinline__ bool attend_pieces(const AttnArgs &a, const AttnPlan &pl, const CUtensorMap &k_map,
                                               const CUtensorMap &v_map, TileBars &bars, uint32_t smem) {
-    constexpr bool E4M3 = C != kCacheSame;
-    using S = TileShape<E4M3, D>;
+    using S = TileShape<C, D>;
     bool failed = false;
     for (int piece = 0; !SHARED || bars.piece[piece].b >= 0; piece ^= 1) {
         if (!SHARED || !failed) {
@@ -1118,17 +1232,17 @@ __device__ __forceinline__ bool attend_pieces(const AttnArgs &a, const AttnPlan 
             }
         }
         if (!SHARED) break;
-        if (ROLE == kSoftmax && threadIdx.x == 0 && !failed) init_bars<S::STAGES, E4M3 ? S::LOADERS * 32 : 1>(bars, true);
+        if (ROLE == kSoftmax && threadIdx.x == 0 && !failed) init_bars<S>(bars, true);
         sync_roles();
     }
     return failed;
 }
 
 template <typename T, int C, int NG, int D, bool SHARED>
-__global__ void __launch_bounds__(TileShape<C != kCacheSame, D>::THREADS, 1)
+__global__ void __launch_bounds__(TileShape<C, D>::THREADS, 1)
 k_attend_tile(AttnArgs a, AttnPlan pl, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
     constexpr bool E4M3 = C != kCacheSame;
-    using S = TileShape<E4M3, D>;
+    using S = TileShape<C, D>;
     extern __shared__ uint8_t raw_smem[];
     __shared__ TileBars bars;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -1152,7 +1266,7 @@ k_attend_tile(AttnArgs a, AttnPlan pl, const __grid_constant__ CUtensorMap k_map
         if (threadIdx.x == 0) bars.piece[0] = pc;
     }
     if (threadIdx.x == 0) {
-        init_bars<S::STAGES, E4M3 ? S::LOADERS * 32 : 1>(bars, false);
+        init_bars<S>(bars, false);
         bars.failed = 0;
     }
     if (warp == 8) tmem_alloc<512>(shared_addr(&bars.tmem));
@@ -1223,6 +1337,23 @@ bool cache_map(const AttnArgs &a, const void *cache, bool columns, CUtensorMap *
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// A cache of codes as a tensor (element, slot, head, page) in boxes of the slots of
+// a page that a block takes; rows of 128 bytes in the 128-byte swizzle.
+bool code_map(const AttnArgs &a, const void *cache, CUtensorMap *map) {
+    const EncodeTiled encode = encode_tiled();
+    if (!encode) return false;
+    const auto stride = [&](int64_t s, int64_t n) { return static_cast<cuuint64_t>(n > 1 ? s : a.D); };
+    const cuuint64_t dims[4] = {static_cast<cuuint64_t>(a.D), static_cast<cuuint64_t>(a.pg.page_size), static_cast<cuuint64_t>(a.Hk),
+                                static_cast<cuuint64_t>(a.pg.n_pages)};
+    const cuuint64_t strides[3] = {stride(a.pg.slot_stride, a.pg.page_size), stride(a.pg.head_stride, a.Hk),
+                                   stride(a.pg.page_stride, a.pg.n_pages)};
+    const cuuint32_t box[4] = {static_cast<cuuint32_t>(a.D), static_cast<cuuint32_t>(a.pg.page_size < kBlock ? a.pg.page_size : kBlock), 1, 1};
+    const cuuint32_t ones[4] = {1, 1, 1, 1};
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void *>(cache), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  a.D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 cudaError_t timeouts_here(int64_t *count) {
     unsigned long long n = 0;
     const cudaError_t e = cudaMemcpyFromSymbol(&n, g_attention_timeouts, sizeof(n));
@@ -1233,9 +1364,10 @@ cudaError_t timeouts_here(int64_t *count) {
 // The launch of one of the caches' kernels.
 template <typename T, int C, int NG, int D, bool SHARED>
 cudaError_t run_attend_tile(const AttnArgs &a, const AttnPlan &pl, dim3 grid) {
-    using S = TileShape<C != kCacheSame, D>;
+    using S = TileShape<C, D>;
     CUtensorMap k_map = {}, v_map = {};
     if (C == kCacheSame && (!cache_map(a, a.k_cache, false, &k_map) || !cache_map(a, a.v_cache, true, &v_map))) return cudaErrorInvalidValue;
+    if (C == kCacheScaled && (!code_map(a, a.k_cache, &k_map) || !code_map(a, a.v_cache, &v_map))) return cudaErrorInvalidValue;
     const cudaError_t e = allow_smem<&k_attend_tile<T, C, NG, D, SHARED>>(S::SMEM);
     if (e != cudaSuccess) return e;
     k_attend_tile<T, C, NG, D, SHARED><<<grid, S::THREADS, S::SMEM, a.stream>>>(a, pl, k_map, v_map);
