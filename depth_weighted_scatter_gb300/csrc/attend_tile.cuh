@@ -1241,7 +1241,6 @@ __device__ __forceinline__ bool attend_pieces(const AttnArgs &a, const AttnPlan 
 template <typename T, int C, int NG, int D, bool SHARED>
 __global__ void __launch_bounds__(TileShape<C, D>::THREADS, 1)
 k_attend_tile(AttnArgs a, AttnPlan pl, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
-    constexpr bool E4M3 = C != kCacheSame;
     using S = TileShape<C, D>;
     extern __shared__ uint8_t raw_smem[];
     __shared__ TileBars bars;
@@ -1285,7 +1284,7 @@ k_attend_tile(AttnArgs a, AttnPlan pl, const __grid_constant__ CUtensorMap k_map
     } else if (warp < 12) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::PRODUCT_REGS));
         failed = attend_pieces<T, C, NG, D, SHARED, kProducts>(a, pl, k_map, v_map, bars, smem);
-    } else if constexpr (E4M3) {
+    } else if constexpr (S::E4M3) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::LOADER_REGS));
         failed = attend_pieces<T, C, NG, D, SHARED, kLoads>(a, pl, k_map, v_map, bars, smem);
     }
