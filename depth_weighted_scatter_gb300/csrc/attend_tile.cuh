@@ -82,7 +82,6 @@ struct TileShape {
     // one of loaders.  Registers a thread, by setmaxnreg; their sum is within
     // what the launch gives (168 a thread of 384, 128 of 512).
     static constexpr int LOADERS = E4M3 ? 4 : 1;                           // warps
-    static constexpr int ARRIVALS = SCALED ? 1 : 32;                       // of a warp at a barrier
     static constexpr int THREADS = E4M3 ? 512 : 384;
     static constexpr int LAUNCH_REGS = E4M3 ? 128 : 168;
     static constexpr int SOFTMAX_REGS = SCALED ? 200 : E4M3 ? 184 : 208;
@@ -261,7 +260,7 @@ __device__ __forceinline__ void init_bars(TileBars &bars, bool again) {
         bar_init(shared_addr(bar), n);
     };
     for (int i = 0; i < S::STAGES; ++i) {
-        init(&bars.full[i], S::E4M3 ? S::LOADERS * S::ARRIVALS : 1);
+        init(&bars.full[i], S::E4M3 ? S::LOADERS * 32 : 1);
         init(&bars.empty[i], 2);
     }
     for (int t = 0; t < 2; ++t) {
@@ -269,11 +268,11 @@ __device__ __forceinline__ void init_bars(TileBars &bars, bool again) {
             init(&bars.raw_full[t], 1);
             init(&bars.raw_empty[t], S::LOADERS);
         }
-        init(&bars.q_full[t], 4 * S::ARRIVALS);
+        init(&bars.q_full[t], kTileRows);
         init(&bars.s_full[t], 1);
-        init(&bars.p_full[t][0], 4 * S::ARRIVALS);
-        init(&bars.p_full[t][1], 4 * S::ARRIVALS);
-        init(&bars.s_read[t], 4 * S::ARRIVALS);
+        init(&bars.p_full[t][0], kTileRows);
+        init(&bars.p_full[t][1], kTileRows);
+        init(&bars.s_read[t], kTileRows);
         init(&bars.o_full[t], 1);
         init(&bars.turn[t], 1);
         init(&bars.drain[t], 1);
@@ -306,17 +305,6 @@ __device__ __forceinline__ float row_to_half(uint32_t row, int swz) {
         asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(piece(c)), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
     }
     return __uint_as_float(static_cast<uint32_t>(127 - 14 + e) << 23);
-}
-
-// A warp's arrival, after all of its lanes: by each of them or by one.
-template <typename S>
-__device__ __forceinline__ void warp_arrive(uint32_t bar) {
-    if constexpr (S::ARRIVALS == 1) {
-        __syncwarp();
-        if ((threadIdx.x & 31) == 0) bar_arrive(bar);
-    } else {
-        bar_arrive(bar);
-    }
 }
 
 enum { kSoftmax, kProducts, kLoads };
@@ -383,7 +371,7 @@ __device__ __forceinline__ bool attend_piece(const AttnArgs &a, const AttnPlan &
                 q_factor = row_to_half<D>(q_smem + t * S::Q_BYTES + tid * 128, tid & 7);
             }
             fence_shared_async();
-            warp_arrive<S>(shared_addr(&bars.q_full[t]));
+            bar_arrive(shared_addr(&bars.q_full[t]));
         }
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t s_mem = tmem + lanes + t * kBlock, p_mem = tmem + lanes + S::P_COL + t * S::P_STEP, o_mem = tmem + lanes + 2 * kBlock + t * D;
@@ -473,7 +461,7 @@ __device__ __forceinline__ bool attend_piece(const AttnArgs &a, const AttnPlan &
             tmem_wait_ld();
             const auto s_done = [&]() {                                    // S may be made again
                 tmem_fence_before();
-                warp_arrive<S>(shared_addr(&bars.s_read[t]));
+                bar_arrive(shared_addr(&bars.s_read[t]));
             };
             if constexpr (S::AHEAD && !SCALED) s_done();
             const int32_t k0 = j * kBlock;
@@ -565,7 +553,7 @@ __device__ __forceinline__ bool attend_piece(const AttnArgs &a, const AttnPlan &
                 for (int g = 0; g < 4; ++g) tmem_st8(p_mem + h * 32 + g * 8, p + g * 8);
                 tmem_wait_st();
                 tmem_fence_before();
-                warp_arrive<S>(shared_addr(&bars.p_full[t][h]));
+                bar_arrive(shared_addr(&bars.p_full[t][h]));
             };
             // The first half's weights are worked out at the scale in use while
             // the row's maximum is still being found (other units do that), and
@@ -1024,7 +1012,8 @@ __device__ __forceinline__ bool attend_piece(const AttnArgs &a, const AttnPlan &
                                 asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(dst + place[y] + (row - row_i) * 128), "r"(0) : "memory");
                 }
                 fence_shared_async();
-                warp_arrive<S>(shared_addr(&bars.full[at]));
+                bar_arrive(shared_addr(&bars.full[at]));
+                __syncwarp();
                 if (lane == 0) bar_arrive(shared_addr(&bars.raw_empty[kv]));
                 if (++at == S::STAGES) {
                     at = 0;
