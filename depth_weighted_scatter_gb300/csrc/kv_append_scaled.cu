@@ -12,10 +12,12 @@
 // Powers of two move the earlier codes, so that they are rounded again only where
 // they fall among E4M3's subnormal ones.
 //
-// Two layouts.  Pages with many new tokens: a group is a CTA, a thread has a lane's
-// place in STEPS rows, whose angles it keeps for all of the part of the heads that
-// the CTA takes.  Few tokens (a decoding step): a group is a warp, with one head of
-// one page.  A page with more tokens than a group has rows is read twice.
+// Two layouts.  Pages with many new tokens: a group is as many warps as a page's
+// rows fill (2, 4 or 8), a thread has a lane's place in STEPS rows, whose angles it
+// keeps for all of the heads that its group takes.  Few tokens (a decoding step): a
+// group is a warp, with one head of one page.  A page with more tokens than a group
+// has rows is read twice, its angles kept in shared memory.
+//
 #include "rotary.cuh"
 
 namespace bevpool {
@@ -76,10 +78,23 @@ __device__ __forceinline__ int64_t first_place(const PagedArgs &pg, int32_t T, i
 }
 
 // 1 / s in two parts of one sign (the lower one is never zero: an infinite value
-// times either has its sign).  s is in [2^-48, 2^48].
+// times either has its sign).  s is in [2^-48, 2^48].  One Newton step leaves the
+// approximate reciprocal within a unit in the last place of 1 / s, two units below
+// that it is less than 1 / s, and what is left is a positive number.
 __device__ __forceinline__ AppendArgs::Inverse inverse_of(float s) {
-    const float hi = __frcp_rz(s);
-    return {hi, fmaxf(fmaf(-s, hi, 1.0f) * hi, hi * 0x1p-60f)};
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+    r = fmaf(fmaf(-s, r, 1.0f), r, r);
+    const float hi = __uint_as_float(__float_as_uint(r) - 2);
+    return {hi, fmaf(-s, hi, 1.0f) * hi};
+}
+
+// top / 448, rounded to nearest: the remainder of the rounded product corrects it
+// (top is at least 448 * 2^-48 where that counts, so nothing is subnormal).
+__device__ __forceinline__ float over_largest(float top) {
+    constexpr float inv = 1.0f / kLargest;
+    const float q = top * inv;
+    return fmaf(fmaf(-kLargest, q, top), inv, q);
 }
 
 __device__ __forceinline__ uint64_t quotient(uint64_t x, const AppendArgs::Inverse &inv) {
@@ -93,7 +108,7 @@ __device__ __forceinline__ float clamp_scale(float s) { return fminf(fmaxf(s, kS
 // two that the earlier codes are to be multiplied by.
 __device__ __forceinline__ float new_scale(float top, bool held, float old, float *move) {
     *move = 1.0f;
-    if (!held) return clamp_scale(__fdiv_rn(top, kLargest));
+    if (!held) return clamp_scale(over_largest(top));
     const float was = clamp_scale(old), x = __fdiv_rn(top, kLargest * was);
     if (!(x > 1.0f)) return was;
     const uint32_t u = __float_as_uint(x);
@@ -134,31 +149,95 @@ __device__ __forceinline__ float largest(float m, const uint64_t *y) {
     return m;
 }
 
+// CTAs a page: its heads are shared out so that the waves of CTAs (slots: what the
+// GPU holds at a time) take least, a CTA costing what its heads' rows cost and about
+// kSetUp rows besides (its request, its rows' angles).
+int64_t append_parts(int64_t pages, int jobs, int groups, int64_t slots) {
+    constexpr int64_t kSetUp = 4;
+    int64_t best = 1, least = INT64_MAX;
+    for (int64_t parts = 1; parts <= jobs; ++parts) {
+        const int64_t cost = div_up(pages * parts, slots) * (div_up(jobs, parts * groups) + kSetUp);
+        if (cost < least) {
+            least = cost;
+            best = parts;
+        }
+    }
+    return best;
+}
+
 struct TurnTable {             // of the pairs, in shared memory
-    unsigned long long turns[kMaxHeadDim / 2];
-    int32_t axis[kMaxHeadDim / 2];
+    unsigned long long turns[128 / 2];
+    int32_t axis[128 / 2];
 };
 
-// GROUP: warps of a group, all of the CTA's (pages) or one (tokens).
-template <typename T, int LPR, bool IL, bool FULL, int GROUP, int STEPS>
-__global__ void __launch_bounds__(kThreads, GROUP == 1 ? 4 : STEPS == 2 ? 3 : 2)
-k_append_scaled(ScaledAppendArgs a, int parts) {
-    constexpr bool PAGES = GROUP > 1;
-    constexpr int RPS = 32 / LPR, ROWS = GROUP * RPS * STEPS, D = LPR * 8;
+// cos and sin of position * inv_freq, off by 2^-21 at most: the angle, reduced exactly
+// (rotary.cuh), goes to the hardware's functions.  (sincospif's last three bits cost
+// as much as ten heads' rows where a group has few heads.)
+__device__ __forceinline__ float2 cos_sin_fast(unsigned long long turns, int32_t pos) {
+    const uint32_t top = static_cast<uint32_t>((turns * static_cast<unsigned long long>(static_cast<long long>(pos))) >> 32);
+    const float angle = static_cast<float>(static_cast<int32_t>(top)) * 1.4629180792671596e-9f;      // pi 2^-31
+    return make_float2(__cosf(angle), __sinf(angle));
+}
+
+// A row's cos and sin of a lane's four pairs, and the row turned by them.
+template <bool IL>
+struct RowTurn {
+    uint64_t c[2], s[2];                                   // pairs 0 1 and 2 3
+    __device__ __forceinline__ void set(const float2 *cs) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            c[i] = pair(cs[2 * i].x, cs[2 * i + 1].x);
+            s[i] = pair(cs[2 * i].y, cs[2 * i + 1].y);
+        }
+    }
+    __device__ __forceinline__ void turn(uint64_t *y) const {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            if constexpr (IL) {                            // words 2i, 2i + 1 hold a pair each
+                float cc[2], ss[2];
+                unpair(c[i], &cc[0], &cc[1]);
+                unpair(s[i], &ss[0], &ss[1]);
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    float a, b;
+                    unpair(y[2 * i + k], &a, &b);
+                    y[2 * i + k] = pair(fmaf(a, cc[k], -(b * ss[k])), fmaf(b, cc[k], a * ss[k]));
+                }
+            } else {                                       // word i holds the first elements, word i + 2 the second
+                const uint64_t u = y[i], v = y[i + 2];
+                float u0, u1, c0, c1, t0, t1;
+                unpair(u, &u0, &u1);
+                unpair(c[i], &c0, &c1);
+                unpair(mul2(v, s[i]), &t0, &t1);
+                y[i] = pair(fmaf(u0, c0, -t0), fmaf(u1, c1, -t1));
+                y[i + 2] = fma2(v, c[i], mul2(u, s[i]));
+            }
+        }
+    }
+};
+
+// Groups of one warp (tokens), or of `group_warps` (pages).
+template <typename T, int LPR, bool IL, bool PAGES, int STEPS>
+__global__ void __launch_bounds__(kThreads, PAGES ? (STEPS == 2 ? 3 : 2) : 3)
+k_append_scaled(ScaledAppendArgs a, int parts, int group_warps) {
+    constexpr int RPS = 32 / LPR, D = LPR * 8;
     __shared__ __align__(16) RowWeights weights;
     __shared__ TurnTable table;
-    __shared__ uint32_t tops[2][kWarps];
+    __shared__ uint32_t tops[PAGES ? kWarps : 1][3];
+    extern __shared__ float2 angles[];                     // pages of several batches: [row][pair]
     const NormRopeArgs &f = a.g.f;
     const PagedArgs &pg = a.g.pg;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, rg = lane / LPR;
     const int jobs = f.Hq + 2 * f.Hk;
+    const int apart = PAGES ? group_warps * RPS : RPS, rows = apart * STEPS;       // rows between a thread's, and of a group
+    const int group = PAGES ? warp / group_warps : warp, group_warp = PAGES ? warp % group_warps : 0;
 
     // This group's tokens and heads: [job0, job1) of queries, keys, values.
     PageRun run = {0, 0, 0, -1, 0, false};
     int job0 = 0, job1 = 0;
     if constexpr (PAGES) {
         const int64_t place = blockIdx.x / parts;
-        const int part = static_cast<int>(blockIdx.x % parts);
+        const int groups = kWarps / group_warps, part = static_cast<int>(blockIdx.x % parts) * groups + group;
         int lo = 0, hi = pg.n_seqs + 1;                    // first_place(lo) <= place
         while (hi - lo > 1) {
             const int step = (hi - lo + 31) / 32, i = lo + (lane + 1) * step;
@@ -171,8 +250,8 @@ k_append_scaled(ScaledAppendArgs a, int parts) {
         bounds_of(pg, f.T, lo, &c0, &c1, &start);
         run = page_run(pg, lo, c0, c1, start, (start >> pg.page_shift) + place - first_place(pg, f.T, lo));
         if (run.t0 >= run.t1) return;                      // the same for the whole CTA
-        job0 = part * jobs / parts;
-        job1 = (part + 1) * jobs / parts;
+        job0 = part * jobs / (parts * groups);
+        job1 = (part + 1) * jobs / (parts * groups);
     } else {
         const int64_t u = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
         if (u < static_cast<int64_t>(f.T) * jobs) {
@@ -190,202 +269,237 @@ k_append_scaled(ScaledAppendArgs a, int parts) {
             }
         }
     }
+    const int n = run.t1 - run.t0, batches = (n + rows - 1) / rows;
+    const int pairs = f.rot.rotary_dim / 2;
     weights.load(f.q_weight, f.k_weight, f.D);
-    for (int i = threadIdx.x; i < f.rot.rotary_dim / 2; i += kThreads) {
+    for (int i = threadIdx.x; i < pairs; i += kThreads) {
         table.turns[i] = turn_of(f.rot.inv_freq[i]);
         table.axis[i] = pair_axis(f.rot, i);
     }
+    if (PAGES && threadIdx.x < kWarps * 3) tops[threadIdx.x / 3][threadIdx.x % 3] = 0;
     const LaneRow p = lane_row<IL>(f.rot, D, lane % LPR);
     __syncthreads();
-    if (run.t0 >= run.t1) return;
-    const int n = run.t1 - run.t0, batches = (n + ROWS - 1) / ROWS;
-    const int row0 = (PAGES ? warp * RPS : 0) + rg;        // this thread's first row; the others RPS * GROUP apart
+    if (PAGES && batches > 1) {                            // the same for the whole CTA
+        for (int i = threadIdx.x; i < n * pairs; i += kThreads) {
+            const int row = i / pairs, pr = i - row * pairs;
+            angles[i] = cos_sin_fast(table.turns[pr], f.rot.positions[static_cast<int64_t>(run.t0 + row) * f.rot.n_axes + table.axis[pr]]);
+        }
+        __syncthreads();
+    }
+    if (job0 >= job1) return;
+    const int row0 = group_warp * RPS + rg;                // this thread's first row
     const float inv_d = 1.0f / static_cast<float>(D);
+    const auto sync_group = [&]() {
+        if constexpr (PAGES)
+            asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(group_warps * 32) : "memory");
+        else
+            __syncwarp();
+    };
 
-    // Angles of the rows of a batch.
-    float cs[STEPS][4], sn[STEPS][4];
-    const auto angles = [&](int batch) {
+    RowTurn<IL> turns[STEPS];
+    const auto set_turns = [&](int batch) {
 #pragma unroll
         for (int s = 0; s < STEPS; ++s) {
-            const int row = batch * ROWS + s * (GROUP * RPS) + row0;
+            const int row = batch * rows + s * apart + row0;
+            float2 cs[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                cs[s][i] = 1.0f;
-                sn[s][i] = 0.0f;
+                cs[i] = make_float2(1.0f, 0.0f);
                 if (p.turned && row < n) {
                     const int pr = p.c * 4 + i;
-                    turn_cos_sin(table.turns[pr], f.rot.positions[static_cast<int64_t>(run.t0 + row) * f.rot.n_axes + table.axis[pr]], &cs[s][i],
-                                 &sn[s][i]);
+                    cs[i] = PAGES && batches > 1
+                                ? angles[row * pairs + pr]
+                                : cos_sin_fast(table.turns[pr], f.rot.positions[static_cast<int64_t>(run.t0 + row) * f.rot.n_axes + table.axis[pr]]);
                 }
             }
+            turns[s].set(cs);
         }
     };
-    LaneWords raw[STEPS];
-    const auto read = [&](int job, int batch) {
-        const bool q = job < f.Hq, k = !q && job < f.Hq + f.Hk;
-        const HeadRows &src = q ? f.q : k ? f.k : a.g.v;
-        const int h = q ? job : k ? job - f.Hq : job - f.Hq - f.Hk;
-        const T *at = static_cast<const T *>(src.p) + h * src.head_stride;
-#pragma unroll
-        for (int s = 0; s < STEPS; ++s) {
-            const int row = batch * ROWS + s * (GROUP * RPS) + row0;
-            if (row < n) {
-                const T *x = at + static_cast<int64_t>(run.t0 + row) * src.token_stride;
-                if constexpr (IL) {
-                    const uint4 w = *reinterpret_cast<const uint4 *>(x + p.e0);
-                    raw[s].w[0] = w.x, raw[s].w[1] = w.y, raw[s].w[2] = w.z, raw[s].w[3] = w.w;
-                } else {
-                    const uint2 w = *reinterpret_cast<const uint2 *>(x + p.e0), v = *reinterpret_cast<const uint2 *>(x + p.e1);
-                    raw[s].w[0] = w.x, raw[s].w[1] = w.y, raw[s].w[2] = v.x, raw[s].w[3] = v.y;
-                }
-            } else {
-                raw[s].w[0] = raw[s].w[1] = raw[s].w[2] = raw[s].w[3] = 0;
-            }
-        }
-    };
-    // The largest of a group's threads' magnitudes.
-    int flip = 0;
+    int turn_slot = 0;                                     // of tops
+    // The largest magnitude of a group's rows.
     const auto over_group = [&](float m) {
         uint32_t u = __reduce_max_sync(0xffffffffu, __float_as_uint(m));   // not below 0: the order of the bits
         if constexpr (PAGES) {
-            if (lane == 0) tops[flip][warp] = u;
-            __syncthreads();
-            u = tops[flip][0];
-#pragma unroll
-            for (int w = 1; w < kWarps; ++w) u = max(u, tops[flip][w]);
-            flip ^= 1;
+            uint32_t *top = tops[group];
+            if (lane == 0) atomicMax(&top[turn_slot], u);
+            sync_group();
+            u = top[turn_slot];
+            // the place before this one was read before the barrier, and is written again after the next
+            const int before = turn_slot == 0 ? 2 : turn_slot - 1;
+            if (group_warp == 0 && lane == 0) top[before] = 0;
+            turn_slot = turn_slot == 2 ? 0 : turn_slot + 1;
         }
         return __uint_as_float(u);
     };
 
-    angles(0);
-    if (batches == 1) read(job0, 0);
-    for (int job = job0; job < job1; ++job) {
-        const bool is_q = job < f.Hq, is_k = !is_q && job < f.Hq + f.Hk;
-        const int h = is_q ? job : is_k ? job - f.Hq : job - f.Hq - f.Hk;
-        uint64_t y[STEPS][4];
-        // The rows of a batch as they are stored, but for the scale.
-        const auto work_out = [&]() {
-            if (!is_q && !is_k) {
-#pragma unroll
-                for (int s = 0; s < STEPS; ++s)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) y[s][i] = widen<T>(raw[s].w[i]);
-                return;
-            }
-            float wu[4], wv[4];
-            lane_weights(weights.w[is_k], p, wu, wv);
-            const bool norm = (is_q ? f.q_weight : f.k_weight) != nullptr;
-#pragma unroll
-            for (int s = 0; s < STEPS; ++s) {
-                uint64_t fa[4], fb[4];
-                lane_factors<IL>(cs[s], sn[s], wu, wv, fa, fb);
-                turn_row<T, LPR, IL, FULL>(raw[s], p, fa, fb, norm, inv_d, f.eps, y[s]);
-            }
-        };
-        const auto store_q = [&](int batch) {
+    // One of the three tensors: PART 0 queries, 1 keys, 2 values; its heads [h0, h1).
+    const auto part_of = [&](auto part_c, int h0, int h1) {
+        constexpr int PART = decltype(part_c)::value;
+        if (h0 >= h1 || (PART > 0 && run.page < 0)) return;
+        const HeadRows &src = PART == 0 ? f.q : PART == 1 ? f.k : a.g.v;
+        const int64_t head_bytes = src.head_stride * 2, step_bytes = static_cast<int64_t>(apart) * src.token_stride * 2;
+        const char *from = static_cast<const char *>(src.p) + (static_cast<int64_t>(run.t0 + row0) * src.token_stride + h0 * src.head_stride) * 2;
+        const float *weight = PART == 0 ? f.q_weight : f.k_weight;
+        uint64_t w[4];
+        if constexpr (PART < 2) {
+            float u[4], v[4];
+            lane_weights(weights.w[PART], p, u, v);
+            w[0] = pair(u[0], u[1]), w[1] = pair(u[2], u[3]), w[2] = pair(v[0], v[1]), w[3] = pair(v[2], v[3]);
+        }
+        // where this thread's first row goes
+        const int64_t to_step = static_cast<int64_t>(apart) * (PART == 0 ? f.q_out.token_stride * 2 : pg.slot_stride);
+        const int64_t to_head = PART == 0 ? f.q_out.head_stride * 2 : pg.head_stride;
+        char *to = PART == 0 ? static_cast<char *>(f.q_out.p) + static_cast<int64_t>(run.t0 + row0) * f.q_out.token_stride * 2
+                             : static_cast<char *>(PART == 1 ? a.g.k_cache : a.g.v_cache) + run.page * pg.page_stride +
+                                   (run.slot + row0) * pg.slot_stride;
+        to += h0 * to_head;
+        LaneWords raw[STEPS];
+        const auto read = [&](const char *x, int first) {
 #pragma unroll
             for (int s = 0; s < STEPS; ++s) {
-                const int row = batch * ROWS + s * (GROUP * RPS) + row0;
-                if (row < n)
-                    store_lane<IL, T>(static_cast<T *>(f.q_out.p) + static_cast<int64_t>(run.t0 + row) * f.q_out.token_stride + h * f.q_out.head_stride, p, y[s]);
-            }
-        };
-        // A pass over the batches for the largest (queries: all there is), one to store.
-        const bool once = batches == 1;
-        float top = 0.0f;
-        bool again = false;                                // an infinity was met: the largest finite one is wanted
-        AppendArgs::Inverse inv = {};
-        const int64_t head = run.page * pg.page_stride + h * pg.head_stride;
-        uint8_t *cache = static_cast<uint8_t *>(is_k ? a.g.k_cache : a.g.v_cache) + head;
-        for (int pass = 0; pass < 2; ++pass) {
-            for (int batch = 0; batch < batches; ++batch) {
-                if (!once) {
-                    if (is_q || is_k) angles(batch);
-                    read(job, batch);
+                if (first + s * apart < n) {
+                    const T *row = reinterpret_cast<const T *>(x + s * step_bytes);
+                    if constexpr (IL) {
+                        const uint4 q = *reinterpret_cast<const uint4 *>(row + p.e0);
+                        raw[s].w[0] = q.x, raw[s].w[1] = q.y, raw[s].w[2] = q.z, raw[s].w[3] = q.w;
+                    } else {
+                        const uint2 q = *reinterpret_cast<const uint2 *>(row + p.e0), v = *reinterpret_cast<const uint2 *>(row + p.e1);
+                        raw[s].w[0] = q.x, raw[s].w[1] = q.y, raw[s].w[2] = v.x, raw[s].w[3] = v.y;
+                    }
+                } else {
+                    raw[s].w[0] = raw[s].w[1] = raw[s].w[2] = raw[s].w[3] = 0;
                 }
-                if (!once || (pass == 0 && !again)) work_out();
-                if (once && pass == 0 && !again && job + 1 < job1) read(job + 1, 0);
-                if (is_q) {
-                    store_q(batch);
-                } else if (pass == 0) {
+            }
+        };
+        uint64_t y[STEPS][4];
+        // The rows read, as they are stored but for the scale.
+        const auto work_out = [&]() {
 #pragma unroll
-                    for (int s = 0; s < STEPS; ++s) top = again ? largest<true>(top, y[s]) : largest<false>(top, y[s]);
-                } else if (run.page >= 0) {
+            for (int s = 0; s < STEPS; ++s) {
 #pragma unroll
-                    for (int s = 0; s < STEPS; ++s) {
-                        const int row = batch * ROWS + s * (GROUP * RPS) + row0;
-                        uint64_t z[4];
+                for (int i = 0; i < 4; ++i) y[s][i] = widen<T>(raw[s].w[i]);
+                if constexpr (PART < 2) {
+                    float r = 1.0f;
+                    if (weight) r = rsqrtf(fmaf(row_sum<LPR>(lane_dot(y[s], y[s])), inv_d, f.eps));
+                    if (weight) {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) z[i] = quotient(y[s][i], inv);
-                        if (row < n) store_lane_e4m3<IL>(cache + (run.slot + row) * pg.slot_stride, p, z);
+                        for (int i = 0; i < 4; ++i) y[s][i] = mul2(mul2(y[s][i], pair(r, r)), w[i]);
+                    }
+                    if (p.turned) turns[s].turn(y[s]);
+                }
+            }
+        };
+        const bool once = batches == 1;
+        if (once) read(from, row0);
+        for (int h = h0; h < h1; ++h, from += head_bytes, to += to_head) {
+            float old = 0.0f;
+            float *scale = nullptr;
+            if constexpr (PART > 0) {
+                scale = (PART == 1 ? a.k_scales : a.v_scales) + static_cast<int64_t>(run.page) * f.Hk + h;
+                if (run.held) old = *scale;
+            }
+            float top = 0.0f;
+            bool again = false;                            // an infinity was met: the largest finite one is wanted
+            AppendArgs::Inverse inv = {};
+            // A pass over the batches for the largest (queries: all there is), one to store.
+            for (int pass = 0; pass < 2; ++pass) {
+                for (int batch = 0; batch < batches; ++batch) {
+                    const int first = batch * rows + row0;
+                    if (!once) {
+                        if (PART < 2) set_turns(batch);
+                        read(from + batch * STEPS * step_bytes, first);
+                    }
+                    if (!once || (pass == 0 && !again)) {
+                        work_out();
+                        if (once && h + 1 < h1) read(from + head_bytes, row0);
+                    }
+                    if constexpr (PART == 0) {
+#pragma unroll
+                        for (int s = 0; s < STEPS; ++s)
+                            if (first + s * apart < n) store_lane<IL, T>(reinterpret_cast<T *>(to + (batch * STEPS + s) * to_step), p, y[s]);
+                    } else if (pass == 0) {
+#pragma unroll
+                        for (int s = 0; s < STEPS; ++s) top = again ? largest<true>(top, y[s]) : largest<false>(top, y[s]);
+                    } else {
+#pragma unroll
+                        for (int s = 0; s < STEPS; ++s) {
+                            uint64_t z[4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) z[i] = quotient(y[s][i], inv);
+                            if (first + s * apart < n)
+                                store_lane_e4m3<IL>(reinterpret_cast<uint8_t *>(to + (batch * STEPS + s) * to_step), p, z);
+                        }
                     }
                 }
-            }
-            if (is_q) break;
-            if (pass == 0) {
-                top = over_group(top);
-                if (!again && top == INFINITY) {           // the same for the group
-                    again = true;
-                    top = 0.0f;
-                    pass = -1;
-                    continue;
-                }
-                if (run.page < 0) break;
-                float *scale = (is_k ? a.k_scales : a.v_scales) + static_cast<int64_t>(run.page) * f.Hk + h;
-                float move;
-                const float old = run.held ? *scale : 0.0f;
-                const float now = new_scale(top, run.held, old, &move);
-                inv = inverse_of(now);
-                if (run.held) {
-                    if constexpr (PAGES) __syncthreads(); else __syncwarp();       // all have read the old one
-                }
-                if (PAGES ? threadIdx.x == 0 : lane == 0) *scale = now;
-                if (move != 1.0f) {                        // the earlier tokens' codes
-                    constexpr int CPR = D / 16;
-                    for (int i = PAGES ? threadIdx.x : lane; i < run.slot * CPR; i += GROUP * 32) {
-                        uint4 *c = reinterpret_cast<uint4 *>(cache + (i / CPR) * pg.slot_stride + (i % CPR) * 16);
-                        *c = move_codes(*c, move);
+                if (PART == 0) break;
+                if (pass == 0) {
+                    top = over_group(top);
+                    if (!again && top == INFINITY) {       // the same for the group
+                        again = true;
+                        top = 0.0f;
+                        pass = -1;
+                        continue;
+                    }
+                    float move;
+                    const float now = new_scale(top, run.held, old, &move);
+                    inv = inverse_of(now);
+                    if (group_warp == 0 && lane == 0) *scale = now;        // after all have read the old one
+                    if (move != 1.0f) {                    // the earlier tokens' codes
+                        constexpr int CPR = D / 16;
+                        uint8_t *page = static_cast<uint8_t *>(PART == 1 ? a.g.k_cache : a.g.v_cache) + run.page * pg.page_stride + h * pg.head_stride;
+                        for (int i = group_warp * 32 + lane; i < run.slot * CPR; i += (PAGES ? group_warps : 1) * 32) {
+                            uint4 *c = reinterpret_cast<uint4 *>(page + (i / CPR) * pg.slot_stride + (i % CPR) * 16);
+                            *c = move_codes(*c, move);
+                        }
                     }
                 }
             }
         }
-    }
+    };
+    const int q1 = f.Hq, k1 = q1 + f.Hk;
+    if (batches == 1 && job0 < k1) set_turns(0);
+    part_of(std::integral_constant<int, 0>{}, job0, min(job1, q1));
+    part_of(std::integral_constant<int, 1>{}, max(job0, q1) - q1, min(job1, k1) - q1);
+    part_of(std::integral_constant<int, 2>{}, max(job0, k1) - k1, job1 - k1);
 }
 
 }  // namespace
 
 cudaError_t launch_append_scaled(const ScaledAppendArgs &a) {
     const NormRopeArgs &f = a.g.f;
+    const PagedArgs &pg = a.g.pg;
     const int jobs = f.Hq + 2 * f.Hk;
-    const auto run = [&](auto t, auto lpr, auto il, auto full, auto group, auto steps) {
-        constexpr int LPR = decltype(lpr)::value, GROUP = decltype(group)::value, STEPS = decltype(steps)::value;
+    using std::integral_constant;
+    const auto run = [&](auto t, auto lpr, auto il, auto pages_c) {
+        constexpr int LPR = decltype(lpr)::value, STEPS = !decltype(pages_c)::value ? 1 : LPR == 8 ? 2 : 4;
+        constexpr bool IL = decltype(il)::value, PAGES = decltype(pages_c)::value;
         int64_t grid, parts = 1;
-        if constexpr (GROUP > 1) {
-            const int64_t places = (f.T >> a.g.pg.page_shift) + 2 * (static_cast<int64_t>(a.g.pg.n_seqs) + 1);
-            const int64_t pages = (f.T >> a.g.pg.page_shift) + a.g.pg.n_seqs;
-            parts = div_up(152 * 8, pages);
-            if (parts > jobs) parts = jobs;
+        int group_warps = 1, smem = 0;
+        if constexpr (PAGES) {
+            group_warps = pg.page_size >= 64 ? 8 : pg.page_size / 8;       // 64 rows at most
+            const int groups = kWarps / group_warps;
+            const int64_t full = f.T >> pg.page_shift, places = full + 2 * (static_cast<int64_t>(pg.n_seqs) + 1), pages = full + pg.n_seqs;
+            parts = append_parts(pages, jobs, groups, 152 * (STEPS == 2 ? 3 : 2));
             grid = places * parts;
+            if (pg.page_size > 64) {
+                smem = pg.page_size * (f.rot.rotary_dim / 2) * static_cast<int>(sizeof(float2));
+                const cudaError_t e = allow_smem<&k_append_scaled<decltype(t), LPR, IL, PAGES, STEPS>>(256 * (LPR * 4) * static_cast<int>(sizeof(float2)));
+                if (e != cudaSuccess) return e;
+            }
         } else {
             grid = div_up(static_cast<int64_t>(f.T) * jobs, kWarps);
         }
         if (grid > INT32_MAX) return cudaErrorInvalidValue;
-        k_append_scaled<decltype(t), LPR, decltype(il)::value, decltype(full)::value, GROUP, STEPS>
-            <<<static_cast<unsigned>(grid), kThreads, 0, f.stream>>>(a, static_cast<int>(parts));
+        k_append_scaled<decltype(t), LPR, IL, PAGES, STEPS>
+            <<<static_cast<unsigned>(grid), kThreads, smem, f.stream>>>(a, static_cast<int>(parts), group_warps);
         count_launch();
         return cudaGetLastError();
     };
-    using std::integral_constant;
-    const auto by_group = [&](auto t, auto lpr, auto il, auto full) {
-        if (f.T <= 4 * static_cast<int64_t>(a.g.pg.n_seqs)) return run(t, lpr, il, full, integral_constant<int, 1>{}, integral_constant<int, 1>{});
-        return run(t, lpr, il, full, integral_constant<int, kWarps>{}, integral_constant<int, decltype(lpr)::value == 8 ? 2 : 4>{});
-    };
-    const auto by_full = [&](auto t, auto lpr, auto il) {
-        return f.rot.rotary_dim == f.D ? by_group(t, lpr, il, std::true_type{}) : by_group(t, lpr, il, std::false_type{});
+    const auto by_group = [&](auto t, auto lpr, auto il) {
+        return f.T <= 4 * static_cast<int64_t>(pg.n_seqs) ? run(t, lpr, il, std::false_type{}) : run(t, lpr, il, std::true_type{});
     };
     const auto by_il = [&](auto t, auto lpr) {
-        return f.rot.interleaved ? by_full(t, lpr, std::true_type{}) : by_full(t, lpr, std::false_type{});
+        return f.rot.interleaved ? by_group(t, lpr, std::true_type{}) : by_group(t, lpr, std::false_type{});
     };
     const auto by_lpr = [&](auto t) {
         return f.D == 64 ? by_il(t, integral_constant<int, 8>{}) : by_il(t, integral_constant<int, 16>{});
