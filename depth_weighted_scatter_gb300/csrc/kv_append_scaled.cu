@@ -290,10 +290,12 @@ k_append_scaled(ScaledAppendArgs a, int parts, int group_warps) {
     const int row0 = group_warp * RPS + rg;                // this thread's first row
     const float inv_d = 1.0f / static_cast<float>(D);
     const auto sync_group = [&]() {
-        if constexpr (PAGES)
-            asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(group_warps * 32) : "memory");
-        else
+        if constexpr (!PAGES)
             __syncwarp();
+        else if (group_warps == kWarps)
+            __syncthreads();
+        else
+            asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(group_warps * 32) : "memory");
     };
 
     RowTurn<IL> turns[STEPS];
@@ -353,6 +355,7 @@ k_append_scaled(ScaledAppendArgs a, int parts, int group_warps) {
                              : static_cast<char *>(PART == 1 ? a.g.k_cache : a.g.v_cache) + run.page * pg.page_stride +
                                    (run.slot + row0) * pg.slot_stride;
         to += h0 * to_head;
+        float *scales = PART == 0 ? nullptr : (PART == 1 ? a.k_scales : a.v_scales) + static_cast<int64_t>(run.page) * f.Hk;
         LaneWords raw[STEPS];
         const auto read = [&](const char *x, int first) {
 #pragma unroll
@@ -389,71 +392,93 @@ k_append_scaled(ScaledAppendArgs a, int parts, int group_warps) {
                 }
             }
         };
-        const bool once = batches == 1;
-        if (once) read(from, row0);
-        for (int h = h0; h < h1; ++h, from += head_bytes, to += to_head) {
-            float old = 0.0f;
-            float *scale = nullptr;
-            if constexpr (PART > 0) {
-                scale = (PART == 1 ? a.k_scales : a.v_scales) + static_cast<int64_t>(run.page) * f.Hk + h;
-                if (run.held) old = *scale;
+        // Once a head's largest is known: its scale, the earlier tokens' codes; what the
+        // new ones are divided by.
+        const auto settle = [&](int h, float top, float old) {
+            float move;
+            const float now = new_scale(top, run.held, old, &move);
+            if (group_warp == 0 && lane == 0) scales[h] = now;             // after all have read the old one
+            if (run.held && move != 1.0f) {
+                constexpr int CPR = D / 16;
+                uint8_t *page = static_cast<uint8_t *>(PART == 1 ? a.g.k_cache : a.g.v_cache) + run.page * pg.page_stride + h * pg.head_stride;
+                for (int i = group_warp * 32 + lane; i < run.slot * CPR; i += (PAGES ? group_warps : 1) * 32) {
+                    uint4 *c = reinterpret_cast<uint4 *>(page + (i / CPR) * pg.slot_stride + (i % CPR) * 16);
+                    *c = move_codes(*c, move);
+                }
             }
+            return inverse_of(now);
+        };
+        const auto store = [&](int batch, const AppendArgs::Inverse &inv) {
+#pragma unroll
+            for (int s = 0; s < STEPS; ++s) {
+                if (batch * rows + s * apart + row0 >= n) continue;
+                char *x = to + (batch * STEPS + s) * to_step;
+                if constexpr (PART == 0) {
+                    store_lane<IL, T>(reinterpret_cast<T *>(x), p, y[s]);
+                } else {
+                    uint64_t z[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) z[i] = quotient(y[s][i], inv);
+                    store_lane_e4m3<IL>(reinterpret_cast<uint8_t *>(x), p, z);
+                }
+            }
+        };
+        if (batches == 1) {
+            read(from, row0);
+#pragma unroll 1
+            for (int h = h0; h < h1; ++h, from += head_bytes, to += to_head) {
+                const float old = PART > 0 && run.held ? scales[h] : 0.0f;
+                work_out();
+                if (h + 1 < h1) read(from + head_bytes, row0);
+                if constexpr (PART == 0) {
+                    store(0, {});
+                } else {
+                    float top = 0.0f;
+#pragma unroll
+                    for (int s = 0; s < STEPS; ++s) top = largest<false>(top, y[s]);
+                    top = over_group(top);
+                    if (top == INFINITY) {                 // the same for the group: the largest finite one
+                        top = 0.0f;
+#pragma unroll
+                        for (int s = 0; s < STEPS; ++s) top = largest<true>(top, y[s]);
+                        top = over_group(top);
+                    }
+                    store(0, settle(h, top, old));
+                }
+            }
+            return;
+        }
+        // A pass over the batches for the largest (queries: all there is; once more where
+        // an infinity was met), one to store.
+#pragma unroll 1
+        for (int h = h0; h < h1; ++h, from += head_bytes, to += to_head) {
+            const float old = PART > 0 && run.held ? scales[h] : 0.0f;
             float top = 0.0f;
-            bool again = false;                            // an infinity was met: the largest finite one is wanted
             AppendArgs::Inverse inv = {};
-            // A pass over the batches for the largest (queries: all there is), one to store.
-            for (int pass = 0; pass < 2; ++pass) {
+            int pass = 0;                                  // 0: the largest, 1: the largest finite one, 2: store
+            do {
+                top = 0.0f;
+#pragma unroll 1
                 for (int batch = 0; batch < batches; ++batch) {
-                    const int first = batch * rows + row0;
-                    if (!once) {
-                        if (PART < 2) set_turns(batch);
-                        read(from + batch * STEPS * step_bytes, first);
-                    }
-                    if (!once || (pass == 0 && !again)) {
-                        work_out();
-                        if (once && h + 1 < h1) read(from + head_bytes, row0);
-                    }
-                    if constexpr (PART == 0) {
-#pragma unroll
-                        for (int s = 0; s < STEPS; ++s)
-                            if (first + s * apart < n) store_lane<IL, T>(reinterpret_cast<T *>(to + (batch * STEPS + s) * to_step), p, y[s]);
-                    } else if (pass == 0) {
-#pragma unroll
-                        for (int s = 0; s < STEPS; ++s) top = again ? largest<true>(top, y[s]) : largest<false>(top, y[s]);
+                    if (PART < 2) set_turns(batch);
+                    read(from + batch * STEPS * step_bytes, batch * rows + row0);
+                    work_out();
+                    if (PART == 0 || pass == 2) {
+                        store(batch, inv);
                     } else {
 #pragma unroll
-                        for (int s = 0; s < STEPS; ++s) {
-                            uint64_t z[4];
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) z[i] = quotient(y[s][i], inv);
-                            if (first + s * apart < n)
-                                store_lane_e4m3<IL>(reinterpret_cast<uint8_t *>(to + (batch * STEPS + s) * to_step), p, z);
-                        }
+                        for (int s = 0; s < STEPS; ++s) top = pass == 1 ? largest<true>(top, y[s]) : largest<false>(top, y[s]);
                     }
                 }
-                if (PART == 0) break;
-                if (pass == 0) {
-                    top = over_group(top);
-                    if (!again && top == INFINITY) {       // the same for the group
-                        again = true;
-                        top = 0.0f;
-                        pass = -1;
-                        continue;
-                    }
-                    float move;
-                    const float now = new_scale(top, run.held, old, &move);
-                    inv = inverse_of(now);
-                    if (group_warp == 0 && lane == 0) *scale = now;        // after all have read the old one
-                    if (move != 1.0f) {                    // the earlier tokens' codes
-                        constexpr int CPR = D / 16;
-                        uint8_t *page = static_cast<uint8_t *>(PART == 1 ? a.g.k_cache : a.g.v_cache) + run.page * pg.page_stride + h * pg.head_stride;
-                        for (int i = group_warp * 32 + lane; i < run.slot * CPR; i += (PAGES ? group_warps : 1) * 32) {
-                            uint4 *c = reinterpret_cast<uint4 *>(page + (i / CPR) * pg.slot_stride + (i % CPR) * 16);
-                            *c = move_codes(*c, move);
-                        }
-                    }
+                if (PART == 0 || pass == 2) break;
+                top = over_group(top);
+                if (pass == 0 && top == INFINITY) {
+                    pass = 1;
+                } else {
+                    inv = settle(h, top, old);
+                    pass = 2;
                 }
-            }
+            } while (true);
         }
     };
     const int q1 = f.Hq, k1 = q1 + f.Hk;
