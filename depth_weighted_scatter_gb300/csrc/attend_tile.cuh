@@ -54,11 +54,10 @@
 // bevpool_attention_timeouts counts it.
 #pragma once
 
-#include <cuda.h>
-
 #include "paged_attention.cuh"
 #include "packed.cuh"
 #include "tcgen05.cuh"
+#include "tensor_map.cuh"
 
 namespace bevpool {
 
@@ -1284,23 +1283,6 @@ k_attend_tile(AttnArgs a, AttnPlan pl, const __grid_constant__ CUtensorMap k_map
     grid_dep_allow();
 }
 
-// The driver's tensor-map encoder, found through the runtime.
-using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
-                                 const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiled encode_tiled() {
-    static const EncodeTiled fn = [] {
-        void *p = nullptr;
-        cudaDriverEntryPointQueryResult found;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &found) != cudaSuccess ||
-            found != cudaDriverEntryPointSuccess)
-            p = nullptr;
-        return reinterpret_cast<EncodeTiled>(p);
-    }();
-    return fn;
-}
-
 // A 16-bit cache as a tensor (element, slot, head, page) in boxes of 64 elements
 // by the slots of a page that a block takes; for V the head's 64-element columns
 // are an axis of their own, all of them in a box.  (K's columns have to lie a
@@ -1327,23 +1309,6 @@ bool cache_map(const AttnArgs &a, const void *cache, bool columns, CUtensorMap *
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// A cache of codes as a tensor (element, slot, head, page) in boxes of the slots of
-// a page that a block takes; rows of 128 bytes in the 128-byte swizzle.
-bool code_map(const AttnArgs &a, const void *cache, CUtensorMap *map) {
-    const EncodeTiled encode = encode_tiled();
-    if (!encode) return false;
-    const auto stride = [&](int64_t s, int64_t n) { return static_cast<cuuint64_t>(n > 1 ? s : a.D); };
-    const cuuint64_t dims[4] = {static_cast<cuuint64_t>(a.D), static_cast<cuuint64_t>(a.pg.page_size), static_cast<cuuint64_t>(a.Hk),
-                                static_cast<cuuint64_t>(a.pg.n_pages)};
-    const cuuint64_t strides[3] = {stride(a.pg.slot_stride, a.pg.page_size), stride(a.pg.head_stride, a.Hk),
-                                   stride(a.pg.page_stride, a.pg.n_pages)};
-    const cuuint32_t box[4] = {static_cast<cuuint32_t>(a.D), static_cast<cuuint32_t>(a.pg.page_size < kBlock ? a.pg.page_size : kBlock), 1, 1};
-    const cuuint32_t ones[4] = {1, 1, 1, 1};
-    return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void *>(cache), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  a.D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 cudaError_t timeouts_here(int64_t *count) {
     unsigned long long n = 0;
     const cudaError_t e = cudaMemcpyFromSymbol(&n, g_attention_timeouts, sizeof(n));
@@ -1357,7 +1322,8 @@ cudaError_t run_attend_tile(const AttnArgs &a, const AttnPlan &pl, dim3 grid) {
     using S = TileShape<C, D>;
     CUtensorMap k_map = {}, v_map = {};
     if (C == kCacheSame && (!cache_map(a, a.k_cache, false, &k_map) || !cache_map(a, a.v_cache, true, &v_map))) return cudaErrorInvalidValue;
-    if (C == kCacheScaled && (!code_map(a, a.k_cache, &k_map) || !code_map(a, a.v_cache, &v_map))) return cudaErrorInvalidValue;
+    if (C == kCacheScaled && (!code_map(a, a.k_cache, kBlock, D == 128, &k_map) || !code_map(a, a.v_cache, kBlock, D == 128, &v_map)))
+        return cudaErrorInvalidValue;
     const cudaError_t e = allow_smem<&k_attend_tile<T, C, NG, D, SHARED>>(S::SMEM);
     if (e != cudaSuccess) return e;
     k_attend_tile<T, C, NG, D, SHARED><<<grid, S::THREADS, S::SMEM, a.stream>>>(a, pl, k_map, v_map);

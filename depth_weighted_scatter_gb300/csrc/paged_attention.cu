@@ -125,7 +125,7 @@ cudaError_t launch_paged_attention(const AttnArgs &args, void *workspace) {
     const bool scaled = a.cache == kCacheScaled;
     cudaError_t e;
     if (pl.few)
-        e = scaled ? launch_attend_few_scaled(a, pl) : launch_attend_few(a, pl);
+        e = !scaled ? launch_attend_few(a, pl) : pl.rows <= 8 ? launch_attend_codes(a, pl) : launch_attend_few_scaled(a, pl);
     else if (!scaled)
         e = launch_attend_tile(a, pl);
     else
@@ -138,6 +138,7 @@ cudaError_t launch_paged_attention(const AttnArgs &args, void *workspace) {
 cudaError_t attention_timeouts(int64_t *count) {
     int64_t n = 0;
     cudaError_t e = cudaDeviceSynchronize();               // a copy alone leaves out streams that do not wait for the default one
+    if (e == cudaSuccess) e = attend_codes_timeouts(&n);
     if (e == cudaSuccess) e = attend_tile_timeouts(&n);
     if (e == cudaSuccess) e = attend_tile_scaled_1_timeouts(&n);
     if (e == cudaSuccess) e = attend_tile_scaled_2_timeouts(&n);

@@ -50,11 +50,13 @@ constexpr int32_t kPairRows = 256;     // rows of a pair of row tiles
 AttnPlan attention_plan(const AttnSizes &z);
 cudaError_t launch_attend_few(const AttnArgs &a, const AttnPlan &pl);      // attend_few.cu
 cudaError_t launch_attend_few_scaled(const AttnArgs &a, const AttnPlan &pl);       // attend_few_scaled.cu: kCacheScaled
+cudaError_t launch_attend_codes(const AttnArgs &a, const AttnPlan &pl);    // attend_codes.cu: kCacheScaled, at most 8 rows
 cudaError_t launch_attend_tile(const AttnArgs &a, const AttnPlan &pl);     // attend_tile.cu
 cudaError_t launch_attend_tile_scaled_1(const AttnArgs &a, const AttnPlan &pl);    // attend_tile_scaled_*.cu: by the groups of a
 cudaError_t launch_attend_tile_scaled_2(const AttnArgs &a, const AttnPlan &pl);    // block of keys that have scales of their own
 cudaError_t launch_attend_tile_scaled_8(const AttnArgs &a, const AttnPlan &pl);
 // Waits of each file's kernels that ran out, added to *count.
+cudaError_t attend_codes_timeouts(int64_t *count);
 cudaError_t attend_tile_timeouts(int64_t *count);
 cudaError_t attend_tile_scaled_1_timeouts(int64_t *count);
 cudaError_t attend_tile_scaled_2_timeouts(int64_t *count);
