@@ -55,6 +55,8 @@ _lib.bevpool_paged_attention_workspace_size.restype = _sz
 _lib.bevpool_paged_attention.argtypes = ([_dt, _dt] + _rows + [_vp, _vp] + _pages + [_i32] * 6
                                          + [_f32, _i32, _i32, _f32, _f32] + _rows + [_vp, _vp, _sz, _vp])
 _lib.bevpool_paged_attention.restype = ctypes.c_int
+_lib.bevpool_paged_attention_scaled_workspace_size.argtypes = [_i32] * 8
+_lib.bevpool_paged_attention_scaled_workspace_size.restype = _sz
 _lib.bevpool_paged_attention_scaled.argtypes = ([_dt] + _rows + [_vp, _vp] + _scaled_pages + [_i32] * 6 + [_f32, _i32, _i32]
                                                 + _rows + [_vp, _vp, _sz, _vp])
 _lib.bevpool_paged_attention_scaled.restype = ctypes.c_int
@@ -94,6 +96,12 @@ def bevpool_paged_attention_workspace_size(n_seqs: int, n_tokens: int, n_q_heads
 
 def bevpool_paged_attention(*args) -> int:
     return _lib.bevpool_paged_attention(*args)
+
+
+def bevpool_paged_attention_scaled_workspace_size(n_seqs: int, n_tokens: int, n_q_heads: int, n_k_heads: int, head_dim: int,
+                                                  max_q_len: int, max_kv_len: int, window: int) -> int:
+    return _lib.bevpool_paged_attention_scaled_workspace_size(n_seqs, n_tokens, n_q_heads, n_k_heads, head_dim, max_q_len,
+                                                              max_kv_len, window)
 
 
 def bevpool_paged_attention_scaled(*args) -> int:

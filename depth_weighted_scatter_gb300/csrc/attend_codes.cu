@@ -27,7 +27,7 @@ namespace {
 
 __device__ unsigned long long g_timeouts;
 
-constexpr int kCodesWarps = 4, kCodesStages = 3, kCodesRows = 8;
+constexpr int kCodesWarps = 4, kCodesStages = 2, kCodesRows = 8;
 
 template <int D>
 struct CodesShape {
@@ -49,7 +49,7 @@ __device__ __forceinline__ void rest4(uint32_t codes, float *x) {
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kCodesWarps * 32, 2)
+__global__ void __launch_bounds__(kCodesWarps * 32, kCodesCtas)
 k_attend_codes(AttnArgs a, AttnPlan pl, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
     using S = CodesShape<D>;
     constexpr bool FINE = std::is_same<T, __half>::value;  // a third part

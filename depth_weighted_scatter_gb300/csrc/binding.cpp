@@ -386,7 +386,8 @@ PyObject *attend(Args a) {
     const Rows o = rows("out", out, l, l.H);
     if (want_lse) lse = fresh({l.T, l.H}, at::kFloat, l.device);
     if (!ws.defined()) {
-        const size_t n = bevpool_paged_attention_workspace_size(c.n_seqs, l.T, l.H, c.heads, l.D, max_q, max_kv, window);
+        const auto size = SCALED ? bevpool_paged_attention_scaled_workspace_size : bevpool_paged_attention_workspace_size;
+        const size_t n = size(c.n_seqs, l.T, l.H, c.heads, l.D, max_q, max_kv, window);
         if (n) ws = fresh({static_cast<int64_t>(n)}, at::kByte, l.device);
     }
     float *lp = want_lse ? static_cast<float *>(lse.data_ptr()) : nullptr;

@@ -15,11 +15,12 @@ namespace {
 // is near sqrt(t / 8 us); a lone request is not ragged.  Measured with w = 1 /
 // 2 / 4 / 8: one request of 40000 keys (8 key heads of 128, bf16) - / 41 / 49 /
 // 55 us, 64 of up to 8192 - / 248 / 240 / 236 us.
-int64_t few_ctas(int64_t keys, int64_t pairs, int32_t n_seqs, int32_t D) {
-    if (n_seqs == 1) return 152 * 2;
+int64_t few_ctas(int64_t keys, int64_t pairs, int32_t n_seqs, int32_t D, bool codes) {
+    const int64_t wave = 152 * (codes ? kCodesCtas : 2);
+    if (n_seqs == 1) return wave;
     const double t = static_cast<double>(keys) * static_cast<double>(pairs) * D * 4 / 6.7e6;      // us, 16-bit cache
     const int64_t w = static_cast<int64_t>(std::sqrt(t / 8) + 0.5);
-    return 152 * 2 * (w < 1 ? 1 : w > 6 ? 6 : w);
+    return wave * (w < 1 ? 1 : w > 6 ? 6 : w);
 }
 
 constexpr int32_t kSms = 152;
@@ -86,11 +87,12 @@ AttnPlan attention_plan(const AttnSizes &z) {
     const int32_t q_len = z.max_q_len < z.T ? z.max_q_len : z.T;
     pl.rows = q_len * (z.Hq / z.Hk);
     pl.few = pl.rows <= 16;
+    pl.codes = z.scaled && pl.rows <= 8;
     pl.align = pl.few ? kFewAlign : kTileAlign;
     const int64_t keys = keys_of(q_len, z.max_kv_len, z.window, pl.align), pairs = static_cast<int64_t>(z.n_seqs) * z.Hk;
     int64_t n = 1;
     if (pl.few) {
-        if (pairs > 0) n = (few_ctas(keys, pairs, z.n_seqs, z.D) + pairs / 2) / pairs;
+        if (pairs > 0) n = (few_ctas(keys, pairs, z.n_seqs, z.D, pl.codes) + pairs / 2) / pairs;
     } else {
         bool share;
         pl.tiles = static_cast<int32_t>(div_up(pl.rows, kPairRows));
@@ -118,14 +120,14 @@ size_t attention_workspace_bytes(AttnSizes z) {
 
 cudaError_t launch_paged_attention(const AttnArgs &args, void *workspace) {
     AttnArgs a = args;
-    const AttnPlan pl = attention_plan({a.pg.n_seqs, a.T, a.Hq, a.Hk, a.D, a.max_q_len, a.max_kv_len, a.window, a.causal});
+    const bool scaled = a.cache == kCacheScaled;
+    const AttnPlan pl = attention_plan({a.pg.n_seqs, a.T, a.Hq, a.Hk, a.D, a.max_q_len, a.max_kv_len, a.window, a.causal, scaled});
     a.part_o = static_cast<float *>(workspace);
     a.part_ml = a.part_o + pl.parts * a.D;
     a.cut = reinterpret_cast<int2 *>(a.part_ml + pl.parts * 2);
-    const bool scaled = a.cache == kCacheScaled;
     cudaError_t e;
     if (pl.few)
-        e = !scaled ? launch_attend_few(a, pl) : pl.rows <= 8 ? launch_attend_codes(a, pl) : launch_attend_few_scaled(a, pl);
+        e = !scaled ? launch_attend_few(a, pl) : pl.codes ? launch_attend_codes(a, pl) : launch_attend_few_scaled(a, pl);
     else if (!scaled)
         e = launch_attend_tile(a, pl);
     else

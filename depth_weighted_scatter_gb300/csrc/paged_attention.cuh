@@ -30,12 +30,13 @@ struct AttnArgs {
 };
 
 struct AttnSizes {
-    int32_t n_seqs, T, Hq, Hk, D, max_q_len, max_kv_len, window, causal;
+    int32_t n_seqs, T, Hq, Hk, D, max_q_len, max_kv_len, window, causal, scaled;
 };
 
 // How one call is laid out, from its sizes alone.
 struct AttnPlan {
     int32_t few;              // 1: at most 16 query rows a request and key head
+    int32_t codes;            // 1: at most 8, over codes with page scales
     int32_t align;            // the first chunk starts at a multiple of this many keys, and has a multiple of it
     int32_t rows;             // query rows a request and key head, at most
     int32_t chunk;            // keys of one CTA
@@ -47,6 +48,7 @@ struct AttnPlan {
     int64_t parts;            // rows of partial results
 };
 constexpr int32_t kPairRows = 256;     // rows of a pair of row tiles
+constexpr int32_t kCodesCtas = 3;      // CTAs of attend_codes.cu that an SM holds
 AttnPlan attention_plan(const AttnSizes &z);
 cudaError_t launch_attend_few(const AttnArgs &a, const AttnPlan &pl);      // attend_few.cu
 cudaError_t launch_attend_few_scaled(const AttnArgs &a, const AttnPlan &pl);       // attend_few_scaled.cu: kCacheScaled

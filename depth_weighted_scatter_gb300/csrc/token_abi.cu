@@ -340,6 +340,12 @@ bevpool_status attention_sizes_ok(int32_t n_seqs, int32_t T, int32_t Hq, int32_t
     return BEVPOOL_OK;
 }
 
+size_t workspace_size(const AttnSizes &z) {
+    if (attention_sizes_ok(z.n_seqs, z.T, z.Hq, z.Hk, z.D, z.max_q_len, z.max_kv_len) != BEVPOOL_OK || z.window < 0) return 0;
+    if (z.n_seqs == 0 || z.T == 0 || z.max_q_len == 0) return 0;
+    return attention_workspace_bytes(z);
+}
+
 // What both attentions take, launched.  k_scales null: one scale for the cache.
 bevpool_status attend(bevpool_dtype dtype, int cache, const HeadRows &q, const void *k_cache, const void *v_cache, int64_t page_stride,
                       int64_t slot_stride, int64_t head_stride, const float *k_scales, const float *v_scales, int32_t n_pages,
@@ -362,7 +368,7 @@ bevpool_status attend(bevpool_dtype dtype, int cache, const HeadRows &q, const v
     const float most = cache == kCacheScaled ? 0x1p48f : k_scale;
     if (!(scale > 0.0f) || !scale_ok(k_scale) || !scale_ok(v_scale) || !std::isfinite(scale * most * 1.4427f)) return BEVPOOL_ERR_INVALID_ARG;
     if (window < 0 || (window > 0 && !causal)) return BEVPOOL_ERR_INVALID_ARG;
-    const size_t need = attention_workspace_bytes({n_seqs, T, Hq, Hk, D, max_q_len, max_kv_len, window, 0});
+    const size_t need = attention_workspace_bytes({n_seqs, T, Hq, Hk, D, max_q_len, max_kv_len, window, 0, cache == kCacheScaled});
     if (need > 0 && (!workspace || !aligned(workspace, 256) || workspace_bytes < need)) return BEVPOOL_ERR_WORKSPACE;
     a.dtype = dtype;
     a.cache = cache;
@@ -392,11 +398,13 @@ bevpool_status attend(bevpool_dtype dtype, int cache, const HeadRows &q, const v
 
 size_t bevpool_paged_attention_workspace_size(int32_t n_seqs, int32_t n_tokens, int32_t n_q_heads, int32_t n_k_heads,
                                               int32_t head_dim, int32_t max_q_len, int32_t max_kv_len, int32_t window) {
-    if (attention_sizes_ok(n_seqs, n_tokens, n_q_heads, n_k_heads, head_dim, max_q_len, max_kv_len) != BEVPOOL_OK ||
-        window < 0)
-        return 0;
-    if (n_seqs == 0 || n_tokens == 0 || max_q_len == 0) return 0;
-    return attention_workspace_bytes({n_seqs, n_tokens, n_q_heads, n_k_heads, head_dim, max_q_len, max_kv_len, window, 0});
+    return workspace_size({n_seqs, n_tokens, n_q_heads, n_k_heads, head_dim, max_q_len, max_kv_len, window, 0, 0});
+}
+
+size_t bevpool_paged_attention_scaled_workspace_size(int32_t n_seqs, int32_t n_tokens, int32_t n_q_heads, int32_t n_k_heads,
+                                                     int32_t head_dim, int32_t max_q_len, int32_t max_kv_len,
+                                                     int32_t window) {
+    return workspace_size({n_seqs, n_tokens, n_q_heads, n_k_heads, head_dim, max_q_len, max_kv_len, window, 0, 1});
 }
 
 bevpool_status bevpool_paged_attention(

@@ -623,6 +623,11 @@ BEVPOOL_API bevpool_status bevpool_paged_attention(
     float v_scale, void *out, int64_t out_token_stride, int64_t out_head_stride, float *lse, void *workspace,
     size_t workspace_bytes, void *stream);
 
+/* The same of bevpool_paged_attention_scaled. */
+BEVPOOL_API size_t bevpool_paged_attention_scaled_workspace_size(int32_t n_seqs, int32_t n_tokens, int32_t n_q_heads,
+                                                                 int32_t n_k_heads, int32_t head_dim, int32_t max_q_len,
+                                                                 int32_t max_kv_len, int32_t window);
+
 /*
  * bevpool_paged_attention over a cache of E4M3 codes with a scale for each page
  * and key head: key = code * k_scales[page][head], value = code *
@@ -633,8 +638,8 @@ BEVPOOL_API bevpool_status bevpool_paged_attention(
  * The weights are rounded to 16 bits with their value's scale in them: relatively,
  * so that pages of small values lose no more than others, down to 2^-28 of the
  * largest weight times scale that a token sees (2^-21 in tiles of many rows; no end
- * in tiles of bf16 heads), and by 2^-39 (2^-32) of that one below.  The workspace is
- * that of bevpool_paged_attention; other arguments too.
+ * in tiles of bf16 heads), and by 2^-39 (2^-32) of that one below.  Other
+ * arguments are those of bevpool_paged_attention.
  */
 BEVPOOL_API bevpool_status bevpool_paged_attention_scaled(
     bevpool_dtype dtype, const void *q, int64_t q_token_stride, int64_t q_head_stride, const void *k_cache,

@@ -275,6 +275,39 @@ def test_caches_past_32_bits(A):
     assert all(torch.equal(a, b) for a, b in zip(got, near))
 
 
+@pytest.mark.parametrize("q_len, kv_len", [([1, 1], [9000, 5000]), ([4], [9000]), ([70], [9000])])
+def test_workspace_of_the_caller(A, q_len, kv_len):
+    """One of the size that is named serves; a smaller one is refused."""
+    from depth_weighted_scatter_gb300.bevpool import BevpoolError
+
+    x = inputs((q_len, kv_len, 8, 2, 128, True, 0, BF16, "", 16, False), seed=60)
+    size = A.bevpool_paged_attention_scaled_workspace_size(len(q_len), sum(q_len), 8, 2, 128, max(q_len), max(kv_len), 0)
+    own = torch.empty(size, dtype=torch.uint8, device="cuda")
+    assert all(torch.equal(a, b) for a, b in zip(attend(A, x, workspace=own), attend(A, x)))
+    with pytest.raises(BevpoolError):
+        attend(A, x, workspace=own[:size - 256])
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("value", [float("inf"), float("nan"), 1e38])
+def test_queries_that_are_not_finite(A, dtype, value):
+    """Rows of infinite or NaN queries are NaN, also over few rows whose queries become codes; the others are not touched."""
+    if value == 1e38 and dtype == F16:
+        value = 65504.0
+    x = inputs(([2, 1], [300, 90], 4, 2, 64, True, 0, dtype, "", 16, False), seed=70)
+    want = attend(A, x)
+    x["q"][1, 2, 5] = value
+    out, lse = attend(A, x)
+    keep = torch.ones(3, 4, dtype=torch.bool)
+    keep[1, 2] = False
+    assert torch.equal(out[keep.cuda()], want[0][keep.cuda()]) and torch.equal(lse[keep.cuda()], want[1][keep.cuda()])
+    if value < 1e39 and value == value:
+        x["scale"] = 2.0 ** -140 if dtype == BF16 else 2.0 ** -20
+        check(A, x)
+    else:
+        assert out[1, 2].isnan().all() and lse[1, 2].isnan()
+
+
 def test_refusals_on_the_gpu(A):
     from depth_weighted_scatter_gb300.bevpool import BevpoolError
 

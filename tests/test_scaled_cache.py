@@ -72,3 +72,12 @@ def test_helpers_refuse(A):
             call(g)
         with pytest.raises(BevpoolError, match="tensor"):
             call(1.0)
+
+
+def test_workspace_sizes(A):
+    """Chunks of few rows are cut for the kernel that reads them; others are those of the plain cache."""
+    plain, scaled = A.bevpool_paged_attention_workspace_size, A.bevpool_paged_attention_scaled_workspace_size
+    assert scaled(0, 5, 8, 2, 128, 2, 64, 0) == 0 and scaled(3, 5, 8, 3, 128, 2, 64, 0) == 0 and scaled(3, 5, 8, 2, 96, 2, 64, 0) == 0
+    assert 0 < scaled(1, 1, 8, 2, 128, 1, 100000, 0) <= scaled(2, 2, 8, 2, 128, 1, 100000, 0)
+    for sizes in ((2, 700, 16, 8, 64, 700, 5000, 0), (1, 3, 16, 4, 128, 3, 5000, 0)):      # tiles; nine to sixteen rows
+        assert scaled(*sizes) == plain(*sizes) > 0
