@@ -414,6 +414,14 @@ struct Span {
     bool meets(const Span &o) const { return from < o.to && o.from < to; }
 };
 
+// A contiguous tensor on the bytes of `all` from `at` on.
+at::Tensor part_of(const at::Tensor &all, int64_t at, at::IntArrayRef sizes, at::ScalarType type) {
+    at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(all.storage()), all.key_set(), c10::scalarTypeToTypeMeta(type));
+    t.unsafeGetTensorImpl()->set_sizes_contiguous(sizes);
+    t.unsafeGetTensorImpl()->set_storage_offset(at / static_cast<int64_t>(c10::elementSize(type)));
+    return t;
+}
+
 // q_len, kv_len, first, drop, block_table, free_pages, n_free, page_size, n_tokens, out (None or its nine tensors)
 PyObject *plan_pages(Args a) {
     const at::Tensor q = a.tensor("q_len"), kv = a.tensor("kv_len"), first = a.tensor("first"), drop = a.maybe("drop"),
@@ -439,10 +447,16 @@ PyObject *plan_pages(Args a) {
     at::Tensor out[N];
     void *p[N];
     if (given == Py_None) {
+        // One allocation for all of them: nine take longer than the plan of a small batch.
+        int64_t at[N], bytes = 0;
         for (int i = 0; i < N; ++i) {
-            const auto type = i == SLOTS ? at::kLong : at::kInt;
-            out[i] = i == 5 ? fresh({B, W}, type, device) : fresh({sizes[i]}, type, device);
-            p[i] = out[i].data_ptr();
+            at[i] = bytes;
+            bytes += (sizes[i] * (i == SLOTS ? 8 : 4) + 255) / 256 * 256;
+        }
+        const at::Tensor all = fresh({bytes}, at::kByte, device);
+        for (int i = 0; i < N; ++i) {
+            out[i] = i == 5 ? part_of(all, at[i], {B, W}, at::kInt) : part_of(all, at[i], {sizes[i]}, i == SLOTS ? at::kLong : at::kInt);
+            p[i] = static_cast<char *>(all.data_ptr()) + at[i];
         }
     } else {
         PyObject *seq = PySequence_Fast(given, "out: the tensors of a plan are wanted");
