@@ -71,18 +71,21 @@ k_plan_pages(PlanArgs a) {
     const int B = a.n_seqs, W = a.table_pages, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int32_t *cu = smem, *wants = cu + B + 1, *drops = wants + B + 1;
 
-    // The sums: a run of requests a thread.
-    const int per = (B + kPlanThreads - 1) / kPlanThreads;
-    const int b0 = min(static_cast<int>(threadIdx.x) * per, B), b1 = min(b0 + per, B);
-    Sums s = {0, 0, 0};
+    // What each request adds, read in order; then the sums, a run of requests a thread.
     bool bad = false;
-    for (int b = b0; b < b1; ++b) {
+#pragma unroll 4
+    for (int b = threadIdx.x; b < B; b += kPlanThreads) {
         const Change c = change_of(a, b);
         bad = bad || c.has > W || c.pages > W || c.q > a.n_tokens;
-        s.q += c.q;
-        s.want += c.has - c.had;
-        s.drop += c.drop;
+        cu[b] = c.q;
+        wants[b] = c.has - c.had;
+        drops[b] = c.drop;
     }
+    __syncthreads();
+    const int per = (B + kPlanThreads - 1) / kPlanThreads | 1;             // odd: lanes' runs start in different banks
+    const int b0 = min(static_cast<int>(threadIdx.x) * per, B), b1 = min(b0 + per, B);
+    Sums s = {0, 0, 0};
+    for (int b = b0; b < b1; ++b) s.q += cu[b], s.want += wants[b], s.drop += drops[b];
     const Sums mine = s;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -109,11 +112,11 @@ k_plan_pages(PlanArgs a) {
     const bool ok = fits && all.want <= top;
     if (ok) {                                              // the sums fit 32 bits then
         for (int b = b0; b < b1; ++b) {
-            const Change c = change_of(a, b);
+            const int32_t q = cu[b], w = wants[b], d = drops[b];
             cu[b] = static_cast<int32_t>(at.q);
             wants[b] = static_cast<int32_t>(at.want);
             drops[b] = static_cast<int32_t>(at.drop);
-            at.q += c.q, at.want += c.has - c.had, at.drop += c.drop;
+            at.q += q, at.want += w, at.drop += d;
         }
         if (threadIdx.x == 0) {
             cu[B] = static_cast<int32_t>(all.q);
@@ -164,6 +167,7 @@ k_plan_pages(PlanArgs a) {
     }
     // the stack
     const int32_t left = ok ? static_cast<int32_t>(top - all.want) : min(n_free, a.n_pool);
+#pragma unroll 4
     for (int64_t i = thread; i < a.n_pool; i += threads)
         a.free_out[i] = i < left ? (ok ? stacked(static_cast<int32_t>(i)) : a.free_pages[i]) : -1;
     // requests
