@@ -8,6 +8,10 @@ values, and its queries attend over this and the last frames in the cache
 are handed to the new one.  `train_step` fits the norms' weights on a frame:
 the forward and backward of the norm and rotation.
 
+`PlannedAttention` does the same for several vehicles at once: their frames'
+pages are planned on the GPU, and their cache holds E4M3 codes with a scale for
+each page and key head.
+
     python examples/temporal_bev.py            # needs the GPU and the built library
 """
 import os
@@ -82,6 +86,39 @@ class TemporalAttention:
         return float(eq.square().mean() + ek.square().mean())
 
 
+class PlannedAttention(TemporalAttention):
+    """A batch of vehicles, each with its own frames, over one pool of pages."""
+
+    def __init__(self, C, Y, X, vehicles, frames=4, **more):
+        super().__init__(C, Y, X, frames=frames, cache_dtype=torch.float8_e4m3fn, **more)
+        i32 = dict(dtype=torch.int32, device="cuda")
+        pool, width = (vehicles * (frames + 1)) * self.pages, (frames + 1) * self.pages
+        shape = (pool, self.Hk, PAGE, self.D)
+        self.k_cache, self.v_cache = (torch.zeros(shape, device="cuda").to(torch.float8_e4m3fn) for _ in range(2))
+        self.k_scales, self.v_scales = (torch.ones(pool, self.Hk, device="cuda") for _ in range(2))
+        # lengths, positions of the first tokens kept, tables and free pages: all on the GPU, from one plan to the next
+        self.state = [torch.zeros(vehicles, **i32), torch.zeros(vehicles, **i32), torch.full((vehicles, width), -1, **i32),
+                      torch.arange(pool, **i32), torch.tensor([pool], **i32)]
+        self.vehicles = vehicles
+
+    def step(self, bevs, drive):
+        """A frame of the vehicles that drive (a truth value each; bevs: their cells, one after the other).
+        -> [cells of those that drive, heads, head_dim]"""
+        q, k, v = (bevs @ self.project).view(-1, self.H + 2 * self.Hk, self.D).split([self.H, self.Hk, self.Hk], dim=1)
+        on = torch.tensor(drive, dtype=torch.int32, device="cuda")
+        # a vehicle whose cache is full gives its oldest frame's pages back first
+        drop = on * (self.state[0] >= self.frames * self.cells).to(torch.int32) * self.pages
+        plan = attention.plan_pages(on * self.cells, *self.state, page_size=PAGE, n_tokens=len(bevs), drop=drop)
+        self.state = [plan.kv_len, plan.first, plan.block_table, plan.free_pages, plan.n_free]
+        # token i of a vehicle is cell i % cells of frame i // cells
+        at = plan.positions
+        positions = torch.stack([at // self.cells, self.yx[at % self.cells, 0], self.yx[at % self.cells, 1]], dim=1).to(torch.int32)
+        pages = (self.k_cache, self.v_cache, self.k_scales, self.v_scales, plan.block_table, plan.kv_len, plan.cu_q)
+        q = attention.kv_append_scaled(k, v, *pages, positions, self.inv_freq, sections=self.sections, q=q, q_weight=self.q_weight,
+                                       k_weight=self.k_weight)
+        return attention.paged_attention_scaled(q, *pages, max_q_len=self.cells, max_kv_len=self.frames * self.cells, causal=False)
+
+
 def pooled_frame(seed, C=64, Y=32, X=40):
     """BEV cells [Y * X, C] (fp16) of one synthetic frame."""
     NC, D, H, W = 2, 10, 8, 16
@@ -100,6 +137,11 @@ def main():
         y = model.step(bev)
         print(f"frame {t}: {len(model.order)} frames in the cache, output {tuple(y.shape)}, "
               f"mean magnitude {y.float().abs().mean().item():.4f}")
+    fleet = PlannedAttention(64, 32, 40, vehicles=3)
+    for t in range(6):
+        drive = [True, t % 2 == 0, t > 2]
+        y = fleet.step(torch.cat([pooled_frame(10 * i + t) for i, on in enumerate(drive) if on]), drive)
+        print(f"fleet, frame {t}: {[n // fleet.cells for n in fleet.state[0].tolist()]} frames in the cache, output {tuple(y.shape)}")
     bev = pooled_frame(0)
     q, k, _ = model.qkv(bev)
     target = attention.qk_norm_rope(q, k, model.positions(), model.inv_freq, sections=model.sections,
