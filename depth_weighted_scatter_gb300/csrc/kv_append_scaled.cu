@@ -216,6 +216,8 @@ struct RowTurn {
     }
 };
 
+constexpr int kAppendAhead = 4;            // heads whose rows are on their way
+
 // Groups of one warp (tokens), or of `group_warps` (pages).
 template <typename T, int LPR, bool IL, bool PAGES, int STEPS>
 __global__ void __launch_bounds__(kThreads, PAGES ? (STEPS == 2 ? 3 : 2) : 3)
@@ -224,7 +226,8 @@ k_append_scaled(ScaledAppendArgs a, int parts, int group_warps) {
     __shared__ __align__(16) RowWeights weights;
     __shared__ TurnTable table;
     __shared__ uint32_t tops[PAGES ? kWarps : 1][3];
-    extern __shared__ float2 angles[];                     // pages of several batches: [row][pair]
+    extern __shared__ __align__(16) uint8_t dynamic[];     // pages: rows on their way; of several batches, their angles
+    float2 *angles = reinterpret_cast<float2 *>(dynamic + kAppendAhead * STEPS * kThreads * 16);       // [row][pair]
     const NormRopeArgs &f = a.g.f;
     const PagedArgs &pg = a.g.pg;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, rg = lane / LPR;
@@ -424,12 +427,52 @@ k_append_scaled(ScaledAppendArgs a, int parts, int group_warps) {
             }
         };
         if (batches == 1) {
-            read(from, row0);
+            // Pages: a thread's own pieces of the next heads' rows come by asynchronous
+            // copies to its own place.
+            const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(dynamic)) + threadIdx.x * 16;
+            const auto fetch = [&](int h, int slot) {
+                if (h < h1) {
+#pragma unroll
+                    for (int s = 0; s < STEPS; ++s) {
+                        const bool on = row0 + s * apart < n;              // else zeros
+                        const T *row = reinterpret_cast<const T *>(on ? from + (h - h0) * head_bytes + s * step_bytes : from);
+                        const uint32_t d = ring + (slot * STEPS + s) * (kThreads * 16);
+                        if constexpr (IL) {
+                            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(row + p.e0), "r"(on ? 16 : 0) : "memory");
+                        } else {
+                            asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(d), "l"(row + p.e0), "r"(on ? 8 : 0) : "memory");
+                            asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(d + 8), "l"(row + p.e1), "r"(on ? 8 : 0) : "memory");
+                        }
+                    }
+                }
+                asm volatile("cp.async.commit_group;" ::: "memory");
+            };
+            [[maybe_unused]] int slot = 0;
+            if constexpr (PAGES) {
+#pragma unroll
+                for (int i = 0; i < kAppendAhead; ++i) fetch(h0 + i, i);
+            } else {
+                read(from, row0);
+            }
+            float old_next = PART > 0 && run.held ? scales[h0] : 0.0f;
 #pragma unroll 1
-            for (int h = h0; h < h1; ++h, from += head_bytes, to += to_head) {
-                const float old = PART > 0 && run.held ? scales[h] : 0.0f;
+            for (int h = h0; h < h1; ++h, to += to_head) {
+                const float old = old_next;
+                if constexpr (PAGES) {
+                    asm volatile("cp.async.wait_group %0;" ::"n"(kAppendAhead - 1) : "memory");
+#pragma unroll
+                    for (int s = 0; s < STEPS; ++s)
+                        asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                                     : "=r"(raw[s].w[0]), "=r"(raw[s].w[1]), "=r"(raw[s].w[2]), "=r"(raw[s].w[3])
+                                     : "r"(ring + (slot * STEPS + s) * (kThreads * 16))
+                                     : "memory");
+                }
                 work_out();
-                if (h + 1 < h1) read(from + head_bytes, row0);
+                if constexpr (PAGES) {
+                    fetch(h + kAppendAhead, slot);
+                    slot = slot == kAppendAhead - 1 ? 0 : slot + 1;
+                }
+                if (PART > 0 && run.held && h + 1 < h1) old_next = scales[h + 1];
                 if constexpr (PART == 0) {
                     store(0, {});
                 } else {
@@ -506,11 +549,11 @@ cudaError_t launch_append_scaled(const ScaledAppendArgs &a) {
             const int64_t full = f.T >> pg.page_shift, places = full + 2 * (static_cast<int64_t>(pg.n_seqs) + 1), pages = full + pg.n_seqs;
             parts = append_parts(pages, jobs, groups, 152 * (STEPS == 2 ? 3 : 2));
             grid = places * parts;
-            if (pg.page_size > 64) {
-                smem = pg.page_size * (f.rot.rotary_dim / 2) * static_cast<int>(sizeof(float2));
-                const cudaError_t e = allow_smem<&k_append_scaled<decltype(t), LPR, IL, PAGES, STEPS>>(256 * (LPR * 4) * static_cast<int>(sizeof(float2)));
-                if (e != cudaSuccess) return e;
-            }
+            constexpr int ring = kAppendAhead * STEPS * kThreads * 16;
+            smem = ring;
+            if (pg.page_size > 64) smem += pg.page_size * (f.rot.rotary_dim / 2) * static_cast<int>(sizeof(float2));
+            const cudaError_t e = allow_smem<&k_append_scaled<decltype(t), LPR, IL, PAGES, STEPS>>(ring + 256 * (LPR * 4) * static_cast<int>(sizeof(float2)));
+            if (e != cudaSuccess) return e;
         } else {
             grid = div_up(static_cast<int64_t>(f.T) * jobs, kWarps);
         }
