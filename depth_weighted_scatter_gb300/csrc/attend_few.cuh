@@ -22,6 +22,9 @@
 // fp16 weights carry a factor of 2^14, so that they keep 11 bits down to 2^-28
 // of the largest.
 //
+// Page scales (nine to sixteen rows; fewer: attend_codes.cu): a tile's scales come with
+// it, by copies of 4 bytes, and go into its scores, weights and sums (PageFactors).
+//
 // Measured on a GB300, 32 query and 8 key heads of 128: 64 requests of up to 8192
 // keys, bf16: 233 us (6.6 TB/s, 98 % of measured copy); two requests of up to
 // 131072 keys in E4M3: 91 us (4.6 TB/s, 68 %: no unit is saturated (ALU 44 %, issue
@@ -113,7 +116,7 @@ k_attend_few(AttnArgs a, AttnPlan pl) {
                     top = fmaxf(top, fmaxf(fabsf(__uint_as_float(qf[k][y] << 16)), fabsf(__uint_as_float(qf[k][y] & 0xffff0000u))));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            const int e = min(max(static_cast<int>(__float_as_uint(top) >> 23) - 127, -100), 100);     // its exponent
+            const int e = min(max(static_cast<int>(__float_as_uint(top) >> 23) - 127, -112), 127);     // its exponent
             const float up = __uint_as_float(static_cast<uint32_t>(127 + 14 - e) << 23);               // 2^(14 - e)
             scale[x] *= __uint_as_float(static_cast<uint32_t>(127 - 14 + e) << 23);
 #pragma unroll

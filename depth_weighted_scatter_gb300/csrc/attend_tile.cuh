@@ -11,7 +11,8 @@
 //   warp 10          loads K and V: a TMA box for each page and 64 elements of
 //                    the head, into a ring of 128-byte-swizzled blocks
 //   warps 12-15      (E4M3 cache instead) load codes, widen them to 16 bits and
-//                    store them in the same layout
+//                    store them in the same layout; with page scales warp 10 loads
+//                    the codes, by TMA, and these widen
 // While one tile is in its softmax the tensor core works on the other.
 //
 // Where there are few pairs of row tiles they may be shared out (AttnPlan::share): each
@@ -49,6 +50,26 @@
 // 158).  Two threads a row gave no gain (they share the exponentials' unit: 471 us
 // for the prompt against 473 at the time), nor did going on with other places of the
 // grid in one CTA (423 against 417).
+//
+// Page scales.  A key's score takes its page's scale in the multiply-add before the
+// exponential, which adds the values' scale too (paged_attention.cuh, PageFactors), so
+// a block's keys fall into groups of one page each: one, two or eight a block, a kernel
+// for each (the chunks below over pages of 128 / 64 / 16 slots: 295 / 308 / 337 us).  All products are of
+// fp16, a conversion from the codes (bf16 heads: a row of queries is scaled by a power
+// of two first; prompt of 8192 tokens 612 us before, 575 after).  The first half of S is
+// not kept in registers for the rare case that a row's scale has to move, but read
+// again: no registers spill (575 to 494).
+//
+// What bounds it then: the codes' way through shared memory (read, widened, written:
+// 128 KB a block pair beside the products' 192; without it 419 us for 449 at head_dim
+// 128) and the instruction cache, as four roles' code is at work: hence the short code
+// of the widening warps.  Measured on a GB300, 32 query and 8 key heads of 128, bf16: a
+// prompt of 8192 tokens, pages of 128, 449 us (1225 TFLOP/s of 1950 measured); six
+// ragged chunks of up to 500 tokens over up to 12000 keys, pages of 16, 338 us (1015
+// TFLOP/s); two requests of up to 2500 tokens of 8 heads of 64 over up to 12500 keys,
+// fp16, pages of 64, 134 us (640 TFLOP/s).  Over one scale for the cache 507, 356 and
+// 133 us.  One arrival a warp at the barriers instead of one a thread: 135.5 for the
+// last, no change else; issuing the products from rolled loops: 490, 362, 146.
 //
 // A wait that runs out (it never should) ends the CTA: its rows become NaN and
 // bevpool_attention_timeouts counts it.
@@ -293,7 +314,7 @@ __device__ __forceinline__ float row_to_half(uint32_t row, int swz) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) top = max3(top, fabsf(__uint_as_float(w[i] << 16)), fabsf(__uint_as_float(w[i] & 0xffff0000u)));
     }
-    const int e = min(max(static_cast<int>(__float_as_uint(top) >> 23) - 127, -100), 100);
+    const int e = min(max(static_cast<int>(__float_as_uint(top) >> 23) - 127, -112), 127);
     const float up = __uint_as_float(static_cast<uint32_t>(127 + 14 - e) << 23);           // 2^(14 - e)
 #pragma unroll 4
     for (int c = 0; c < D / 8; ++c) {

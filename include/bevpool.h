@@ -407,8 +407,9 @@ BEVPOOL_API bevpool_status bevpool_probe_gather(const void *feat, int32_t n_rows
  *
  * The pooled cells of a frame are tokens; the queries of new tokens attend
  * over the keys and values of this and earlier frames, kept in a paged
- * cache.  Three operators: norms of queries and keys with rotary positions
- * (forward and backward), the append to the cache, and the attention.
+ * cache.  Norms of queries and keys with rotary positions (forward and
+ * backward), the plan of a batch's pages, the append to the cache, and the
+ * attention; the last two also for codes with a scale a page and key head.
  *
  * Conventions, beside those at the top of this file:
  *   - q, k, v and outputs are [token][head][head_dim] with strides in
@@ -634,7 +635,7 @@ BEVPOOL_API size_t bevpool_paged_attention_scaled_workspace_size(int32_t n_seqs,
  * v_scales[page][head], as bevpool_kv_append_scaled makes it.
  *   k_scales, v_scales  device float [n_pages][n_k_heads], within [2^-48, 2^48]
  *                       (others count as the nearest bound, NaN as the lower);
- *   scale               > 0, scale * 2^48 finite.
+ *   scale               2^-78 or more, scale * 2^48 finite.
  * The weights are rounded to 16 bits with their value's scale in them: relatively,
  * so that pages of small values lose no more than others, down to 2^-28 of the
  * largest weight times scale that a token sees (2^-21 in tiles of many rows; no end

@@ -288,21 +288,26 @@ def test_workspace_of_the_caller(A, q_len, kv_len):
         attend(A, x, workspace=own[:size - 256])
 
 
+@pytest.mark.parametrize("q_len, Hq", [([2, 1], 4), ([1, 1], 20), ([40, 1], 4)])
 @pytest.mark.parametrize("dtype", [F16, BF16])
 @pytest.mark.parametrize("value", [float("inf"), float("nan"), 1e38])
-def test_queries_that_are_not_finite(A, dtype, value):
-    """Rows of infinite or NaN queries are NaN, also over few rows whose queries become codes; the others are not touched."""
+def test_queries_that_are_not_finite(A, q_len, Hq, dtype, value):
+    """Rows of infinite or NaN queries are NaN, also where queries become codes or fp16; the others are not touched, and the
+    largest finite ones serve."""
     if value == 1e38 and dtype == F16:
         value = 65504.0
-    x = inputs(([2, 1], [300, 90], 4, 2, 64, True, 0, dtype, "", 16, False), seed=70)
+    x = inputs((q_len, [300, 90], Hq, 2, 64, True, 0, dtype, "", 16, False), seed=70)
     want = attend(A, x)
     x["q"][1, 2, 5] = value
     out, lse = attend(A, x)
-    keep = torch.ones(3, 4, dtype=torch.bool)
+    keep = torch.ones(sum(q_len), Hq, dtype=torch.bool)
     keep[1, 2] = False
     assert torch.equal(out[keep.cuda()], want[0][keep.cuda()]) and torch.equal(lse[keep.cuda()], want[1][keep.cuda()])
     if value < 1e39 and value == value:
-        x["scale"] = 2.0 ** -140 if dtype == BF16 else 2.0 ** -20
+        # scores of the order of 1: a small scale, and keys' scales near the least
+        x["scale"] = 2.0 ** -77 if dtype == BF16 else 2.0 ** -20
+        if dtype == BF16:
+            x["k_scales"] *= 2.0 ** -42
         check(A, x)
     else:
         assert out[1, 2].isnan().all() and lse[1, 2].isnan()

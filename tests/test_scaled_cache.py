@@ -48,7 +48,7 @@ def test_attention_refusals(A):
     check(A.bevpool_paged_attention_scaled, attend_args(),
           HEADS_INVALID + pages(PAGES_INVALID) + SCALES_INVALID
           + [dict(q=0), dict(o=0), dict(o=FAKE + 8), dict(q_ts=2), dict(Hk=3), dict(max_q=-1), dict(max_kv=-1), dict(scale=float("nan")),
-             dict(scale=float("inf")), dict(scale=0.0), dict(scale=-1.0), dict(scale=2.0 ** 80), dict(window=-1), dict(causal=0, window=5),
+             dict(scale=float("inf")), dict(scale=0.0), dict(scale=-1.0), dict(scale=2.0 ** 80), dict(scale=2.0 ** -79), dict(window=-1), dict(causal=0, window=5),
              dict(lse=FAKE + 2), dict(n_seqs=65536), dict(max_kv=2 ** 31 - 1), dict(max_q=2 ** 31 - 1), dict(T=1 << 28, Hq=32), dict(ss=136)],
           HEADS_UNSUPPORTED + pages(PAGES_UNSUPPORTED) + [dict(D=96), dict(D=256), dict(D=32)],
           [dict(ws=0, max_kv=100000), dict(ws=FAKE + 64, max_kv=100000), dict(ws_bytes=16, max_kv=100000)])
