@@ -1,14 +1,15 @@
 """Thin ctypes binding of libbevpool's token operators (include/bevpool.h):
-head norms with rotary positions, the append to a paged key/value cache, and
-attention of new tokens over that cache.
+head norms with rotary positions, the plan of a batch's pages, the append to a
+paged key/value cache, and attention of new tokens over that cache.
 
 The functions named like the C entry points only marshal arguments.  The
 tensor-level helpers (``qk_norm_rope``, ``qk_norm_rope_backward``,
-``kv_append``, ``paged_attention``) go through the native module
-``_token_ops``, which checks shapes and types, allocates outputs and
-workspaces with PyTorch and names the stream.  Every step of the computation
-runs in the library's CUDA kernels; there is no CPU fallback.  Importing this
-module raises if the library or ``_token_ops`` has not been built.
+``plan_pages``, ``kv_append``, ``paged_attention`` and the last two's forms for a
+cache with page scales, ``..._scaled``) go through the native module
+``_token_ops``, which checks shapes and types, allocates outputs and workspaces
+with PyTorch and names the stream.  Every step of the computation runs in the
+library's CUDA kernels; there is no CPU fallback.  Importing this module raises
+if the library or ``_token_ops`` has not been built.
 
 Head tensors are [tokens, heads, head_dim], fp16 or bf16, with any token and
 head strides that are multiples of 8 elements (a slice of a fused projection

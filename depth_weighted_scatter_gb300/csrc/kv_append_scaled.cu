@@ -18,6 +18,14 @@
 // group is a warp, with one head of one page.  A page with more tokens than a group
 // has rows is read twice, its angles kept in shared memory.
 //
+// Measured on a GB300: 65536 tokens of 8 + 8 + 8 heads of 64, fp16, pages of 64: 63 us
+// (4.0 TB/s of 6.8 measured copy; with one scale for the cache 65); six chunks of up to
+// 1501 tokens of 32 + 8 + 8 heads of 128, bf16: 46 us, 104 pages being too few CTAs to
+// cover what a head's rows wait for (a sum over lanes, a largest over warps) with each
+// other; 64 single tokens: 6.2 us a call, the launch and its call. The rows through
+// registers a head ahead instead of asynchronous copies: 74 and 51 us; sincospif for
+// the angles and factors anew for each head: 112 and 78.
+//
 #include "rotary.cuh"
 
 namespace bevpool {
@@ -151,11 +159,13 @@ __device__ __forceinline__ float largest(float m, const uint64_t *y) {
 
 // CTAs a page: its heads are shared out so that the waves of CTAs (slots: what the
 // GPU holds at a time) take least, a CTA costing what its heads' rows cost and about
-// kSetUp rows besides (its request, its rows' angles).
+// kSetUp heads besides (its request, its rows' angles).  Measured with 1 / 2 / 3 / 4 / 5
+// parts, before the rows came by asynchronous copies: 1024 pages of 24 heads 74 / 77 /
+// 74 / 80 / 85 us, 104 of 48 heads 78 / 52 / 65 / 55 / 52.
 int64_t append_parts(int64_t pages, int jobs, int groups, int64_t slots) {
-    constexpr int64_t kSetUp = 4;
+    constexpr int64_t kSetUp = 4, kMost = 4096;
     int64_t best = 1, least = INT64_MAX;
-    for (int64_t parts = 1; parts <= jobs; ++parts) {
+    for (int64_t parts = 1; parts <= jobs && parts <= kMost; ++parts) {
         const int64_t cost = div_up(pages * parts, slots) * (div_up(jobs, parts * groups) + kSetUp);
         if (cost < least) {
             least = cost;
@@ -216,18 +226,20 @@ struct RowTurn {
     }
 };
 
-constexpr int kAppendAhead = 4;            // heads whose rows are on their way
+// Heads whose rows are on their way: 32 KB a CTA where an SM holds three, 48 KB where
+// it holds two (one head more or less: 63 to 64 us and 47 to 56 of the cases below).
+constexpr int append_ahead(int steps) { return steps == 2 ? 4 : 3; }
 
 // Groups of one warp (tokens), or of `group_warps` (pages).
 template <typename T, int LPR, bool IL, bool PAGES, int STEPS>
 __global__ void __launch_bounds__(kThreads, PAGES ? (STEPS == 2 ? 3 : 2) : 3)
 k_append_scaled(ScaledAppendArgs a, int parts, int group_warps) {
-    constexpr int RPS = 32 / LPR, D = LPR * 8;
+    constexpr int RPS = 32 / LPR, D = LPR * 8, AHEAD = append_ahead(STEPS);
     __shared__ __align__(16) RowWeights weights;
     __shared__ TurnTable table;
     __shared__ uint32_t tops[PAGES ? kWarps : 1][3];
     extern __shared__ __align__(16) uint8_t dynamic[];     // pages: rows on their way; of several batches, their angles
-    float2 *angles = reinterpret_cast<float2 *>(dynamic + kAppendAhead * STEPS * kThreads * 16);       // [row][pair]
+    float2 *angles = reinterpret_cast<float2 *>(dynamic + AHEAD * STEPS * kThreads * 16);       // [row][pair]
     const NormRopeArgs &f = a.g.f;
     const PagedArgs &pg = a.g.pg;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, rg = lane / LPR;
@@ -253,8 +265,8 @@ k_append_scaled(ScaledAppendArgs a, int parts, int group_warps) {
         bounds_of(pg, f.T, lo, &c0, &c1, &start);
         run = page_run(pg, lo, c0, c1, start, (start >> pg.page_shift) + place - first_place(pg, f.T, lo));
         if (run.t0 >= run.t1) return;                      // the same for the whole CTA
-        job0 = part * jobs / (parts * groups);
-        job1 = (part + 1) * jobs / (parts * groups);
+        job0 = static_cast<int>(static_cast<int64_t>(part) * jobs / (parts * groups));
+        job1 = static_cast<int>((static_cast<int64_t>(part) + 1) * jobs / (parts * groups));
     } else {
         const int64_t u = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
         if (u < static_cast<int64_t>(f.T) * jobs) {
@@ -450,7 +462,7 @@ k_append_scaled(ScaledAppendArgs a, int parts, int group_warps) {
             [[maybe_unused]] int slot = 0;
             if constexpr (PAGES) {
 #pragma unroll
-                for (int i = 0; i < kAppendAhead; ++i) fetch(h0 + i, i);
+                for (int i = 0; i < AHEAD; ++i) fetch(h0 + i, i);
             } else {
                 read(from, row0);
             }
@@ -459,7 +471,7 @@ k_append_scaled(ScaledAppendArgs a, int parts, int group_warps) {
             for (int h = h0; h < h1; ++h, to += to_head) {
                 const float old = old_next;
                 if constexpr (PAGES) {
-                    asm volatile("cp.async.wait_group %0;" ::"n"(kAppendAhead - 1) : "memory");
+                    asm volatile("cp.async.wait_group %0;" ::"n"(AHEAD - 1) : "memory");
 #pragma unroll
                     for (int s = 0; s < STEPS; ++s)
                         asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
@@ -469,8 +481,8 @@ k_append_scaled(ScaledAppendArgs a, int parts, int group_warps) {
                 }
                 work_out();
                 if constexpr (PAGES) {
-                    fetch(h + kAppendAhead, slot);
-                    slot = slot == kAppendAhead - 1 ? 0 : slot + 1;
+                    fetch(h + AHEAD, slot);
+                    slot = slot == AHEAD - 1 ? 0 : slot + 1;
                 }
                 if (PART > 0 && run.held && h + 1 < h1) old_next = scales[h + 1];
                 if constexpr (PART == 0) {
@@ -549,7 +561,7 @@ cudaError_t launch_append_scaled(const ScaledAppendArgs &a) {
             const int64_t full = f.T >> pg.page_shift, places = full + 2 * (static_cast<int64_t>(pg.n_seqs) + 1), pages = full + pg.n_seqs;
             parts = append_parts(pages, jobs, groups, 152 * (STEPS == 2 ? 3 : 2));
             grid = places * parts;
-            constexpr int ring = kAppendAhead * STEPS * kThreads * 16;
+            constexpr int ring = append_ahead(STEPS) * STEPS * kThreads * 16;
             smem = ring;
             if (pg.page_size > 64) smem += pg.page_size * (f.rot.rotary_dim / 2) * static_cast<int>(sizeof(float2));
             const cudaError_t e = allow_smem<&k_append_scaled<decltype(t), LPR, IL, PAGES, STEPS>>(ring + 256 * (LPR * 4) * static_cast<int>(sizeof(float2)));

@@ -14,12 +14,15 @@ namespace {
 // waves leave about 1 / (2 w) of the time t of the read to ragged lengths, so w
 // is near sqrt(t / 8 us); a lone request is not ragged.  Measured with w = 1 /
 // 2 / 4 / 8: one request of 40000 keys (8 key heads of 128, bf16) - / 41 / 49 /
-// 55 us, 64 of up to 8192 - / 248 / 240 / 236 us.
+// 55 us, 64 of up to 8192 - / 248 / 240 / 236 us.  Over codes with page scales an SM
+// holds three; the same rule (bytes are half there): 64 of up to 8192 keys 137 us, 138
+// and 139 with w smaller by 1.4 and 2; two of up to 131072 86 with w = 4, 82 with 2.
 int64_t few_ctas(int64_t keys, int64_t pairs, int32_t n_seqs, int32_t D, bool codes) {
     const int64_t wave = 152 * (codes ? kCodesCtas : 2);
     if (n_seqs == 1) return wave;
     const double t = static_cast<double>(keys) * static_cast<double>(pairs) * D * 4 / 6.7e6;      // us, 16-bit cache
-    const int64_t w = static_cast<int64_t>(std::sqrt(t / 8) + 0.5);
+    int64_t w = static_cast<int64_t>(std::sqrt(t / 8) + 0.5);
+    if (codes && w > n_seqs) w = n_seqs;                   // few requests leave few ragged ends
     return wave * (w < 1 ? 1 : w > 6 ? 6 : w);
 }
 

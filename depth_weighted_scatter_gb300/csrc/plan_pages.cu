@@ -8,6 +8,12 @@
 // length; a call is bound by its launch.)  The free pages are a stack whose top is
 // handed out first; pages given back lie on top of it in the requests' order, so
 // that a page taken from there is found by a search of the sums.
+//
+// Measured on a GB300, a call: 64 single tokens over up to 8192, 8.3 to 8.7 us (launch
+// and call: its nine outputs are one allocation, 17 us with nine); 46000 tokens of four
+// frames, 9.1 to 10.2; 4000 requests of up to 7 tokens over up to 2000, 14.3: the sums
+// and then four lookups that wait for each other.  Two CTAs an SM: 19.8, as each works
+// the sums out.
 #include "plan_pages.cuh"
 
 namespace bevpool {
