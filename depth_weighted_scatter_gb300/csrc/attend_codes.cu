@@ -20,7 +20,7 @@
 //
 // Measured on a GB300, 32 query and 8 key heads of 128, bf16: 64 requests of up to 8192
 // keys, pages of 16: 137 us (5.6 TB/s, 82 % of measured copy; the few-rows kernel 154);
-// two requests of up to 131072 keys, pages of 64: 86 us (4.8 TB/s, 71 %; 94): what is
+// two requests of up to 131072 keys, pages of 64: 82 us (5.0 TB/s, 74 %; 94): what is
 // left is mostly a CTA's start (four lookups that wait for each other) and the join;
 // one request of 777 keys, 8 heads of 64: 10.5 to 12 us a call (13.5).  Two CTAs an SM
 // with three tiles a ring instead of three with two: 144 and 91 us; four with tiles of
