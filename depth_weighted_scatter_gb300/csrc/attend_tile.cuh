@@ -300,11 +300,23 @@ __device__ __forceinline__ void init_bars(TileBars &bars, bool again) {
     bar_init_fence();
 }
 
+// The least exponent that a row of bf16 queries is scaled by (row_to_half): with it
+// the inverse, 2^(e - 14), times the least factor of a key's score, scale_log2 * 2^-48,
+// is 2^-126 or more, so that the product is never 0 and a masked score never 0 * -inf.
+// (NaN there meant that padded rows were taken again key by key: 2000 tokens of zeros,
+// 8 heads of 128, 11.5 ms for 0.045.)  A row below it gives up bits of fp16 instead: at most 2^-25 *
+// 2^(e - 14) an element, which is 2^-38 of a score under the largest scale.
+__device__ __forceinline__ int least_exponent(float scale_log2) {
+    const int x = static_cast<int>(__float_as_uint(scale_log2) >> 23) - 127 - 48;          // of the least factor; -126 or more
+    return max(-112, -112 - x);
+}
+
 // A row of bf16 queries in shared memory (D / 64 runs of 128 bytes, 16-byte pieces
 // swapped by swz) to fp16, scaled by the power of two that brings its largest element
-// to 2^14: elements 2^-31 of it and more keep all their bits.  Returns the inverse.
+// to 2^14 (rows below 2^least: by that one's): elements 2^-31 of it and more keep all
+// their bits.  Returns the inverse.
 template <int D>
-__device__ __forceinline__ float row_to_half(uint32_t row, int swz) {
+__device__ __forceinline__ float row_to_half(uint32_t row, int swz, int least) {
     const auto piece = [&](int c) { return row + (c >> 3) * (kTileRows * 128) + (((c & 7) ^ swz) << 4); };
     float top = 0.0f;
 #pragma unroll 4
@@ -314,7 +326,7 @@ __device__ __forceinline__ float row_to_half(uint32_t row, int swz) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) top = max3(top, fabsf(__uint_as_float(w[i] << 16)), fabsf(__uint_as_float(w[i] & 0xffff0000u)));
     }
-    const int e = min(max(static_cast<int>(__float_as_uint(top) >> 23) - 127, -112), 127);
+    const int e = min(max(static_cast<int>(__float_as_uint(top) >> 23) - 127, least), 127);
     const float up = __uint_as_float(static_cast<uint32_t>(127 + 14 - e) << 23);           // 2^(14 - e)
 #pragma unroll 4
     for (int c = 0; c < D / 8; ++c) {
@@ -388,7 +400,7 @@ __device__ __forceinline__ bool attend_piece(const AttnArgs &a, const AttnPlan &
             asm volatile("cp.async.wait_all;" ::: "memory");
             if constexpr (!std::is_same<M, T>::value) {
                 __syncwarp();
-                q_factor = row_to_half<D>(q_smem + t * S::Q_BYTES + tid * 128, tid & 7);
+                q_factor = row_to_half<D>(q_smem + t * S::Q_BYTES + tid * 128, tid & 7, least_exponent(a.scale_log2));
             }
             fence_shared_async();
             bar_arrive(shared_addr(&bars.q_full[t]));

@@ -129,7 +129,8 @@ struct PageFactors {
 __device__ __forceinline__ PageFactors page_factors(float score, float ks, float vs) {
     PageFactors f;
     const float v = fminf(fmaxf(vs, 0x1p-48f), 0x1p48f);   // NaN: the least
-    f.score = fmaxf(score * fminf(fmaxf(ks, 0x1p-48f), 0x1p48f), 0x1p-126f);       // never 0: 0 * -inf
+    // never 0, as 0 * -inf is NaN; tiles of bf16 rows see to their factor besides (least_exponent)
+    f.score = fmaxf(score * fminf(fmaxf(ks, 0x1p-48f), 0x1p48f), 0x1p-126f);
     asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(f.lift) : "f"(v));
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(f.sum) : "f"(v));
     return f;

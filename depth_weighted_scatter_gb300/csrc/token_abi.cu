@@ -364,7 +364,7 @@ bevpool_status attend(bevpool_dtype dtype, int cache, const HeadRows &q, const v
         return BEVPOOL_ERR_INVALID_ARG;
     if (cache == kCacheScaled && (!k_scales || !v_scales || !aligned(k_scales, 4) || !aligned(v_scales, 4))) return BEVPOOL_ERR_INVALID_ARG;
     if (cache != kCacheE4M3) k_scale = v_scale = 1.0f;
-    // page scales reach from 2^-48 to 2^48; a score's factor is a normal number throughout
+    // page scales reach from 2^-48 to 2^48; their products with the scale are normal numbers
     if (cache == kCacheScaled && !(scale >= 0x1p-78f)) return BEVPOOL_ERR_INVALID_ARG;
     const float most = cache == kCacheScaled ? 0x1p48f : k_scale;
     if (!(scale > 0.0f) || !scale_ok(k_scale) || !scale_ok(v_scale) || !std::isfinite(scale * most * 1.4427f)) return BEVPOOL_ERR_INVALID_ARG;
