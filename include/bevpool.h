@@ -636,11 +636,11 @@ BEVPOOL_API size_t bevpool_paged_attention_scaled_workspace_size(int32_t n_seqs,
  *   k_scales, v_scales  device float [n_pages][n_k_heads], within [2^-48, 2^48]
  *                       (others count as the nearest bound, NaN as the lower);
  *   scale               2^-78 or more, scale * 2^48 finite.
- * The weights are rounded to 16 bits with their value's scale in them: relatively,
- * so that pages of small values lose no more than others, down to 2^-28 of the
- * largest weight times scale that a token sees (2^-21 in tiles of many rows; no end
- * in tiles of bf16 heads), and by 2^-39 (2^-32) of that one below.  Other
- * arguments are those of bevpool_paged_attention.
+ * The weights are rounded to fp16, whatever the heads' type, with their value's scale
+ * in them: relatively, so that pages of small values lose no more than others, down to
+ * 2^-28 of the largest weight times scale that a token sees (2^-21 where a request and
+ * key head has more than 16 query rows), and by 2^-39 (2^-32) of that one below.
+ * Other arguments are those of bevpool_paged_attention.
  */
 BEVPOOL_API bevpool_status bevpool_paged_attention_scaled(
     bevpool_dtype dtype, const void *q, int64_t q_token_stride, int64_t q_head_stride, const void *k_cache,

@@ -51,3 +51,50 @@ def test_small_queries_of_large_keys(A, D, page):  # noqa: F811
     x["q"] = (x["q"].float() * torch.exp2(power.float())[:, None, None]).to(BF16)
     x["k_scales"] = (x["k_scales"] * 2.0 ** 51).clamp(max=2.0 ** 48)
     check(A, x)
+
+
+def token_rows(x, b, i, h, least):
+    """(out, bound) of token i of request b under key head h, in FP64.  Bounds as in scaled_ref, the weights being fp16: u =
+    2^-11 relatively, and `least` of the largest weight times scale that the token sees below that."""
+    cu, kv_len, page, D = x["cu_q"].tolist(), x["kv_len"].tolist(), x["k_cache"].shape[2], x["q"].shape[2]
+    G, dtype = x["q"].shape[1] // x["k_cache"].shape[1], x["q"].dtype
+    n, m = cu[b + 1] - cu[b], kv_len[b]
+    hi = m - n + i + 1
+    pg = x["block_table"][b, :-(-m // page)].long()
+    kc, code = (x[c].view(torch.uint8)[pg, h].view(torch.float8_e4m3fn).float().reshape(-1, D)[:hi].double() for c in ("k_cache", "v_cache"))
+    ks, f = (x[c][pg, h].double().repeat_interleave(page)[:hi] for c in ("k_scales", "v_scales"))
+    q = x["q"][cu[b] + i, h * G:(h + 1) * G].double()
+    k, scale = kc * ks[:, None], D ** -0.5
+    s = q @ k.T * scale
+    d = (D + 8) * 2.0 ** -23 * scale * (q.abs() @ k.abs().T).max(-1).values
+    d = d + 2.0 ** -22 * 1.4427 * s.abs().max(-1).values + 2.0 ** -22 * f.log2().abs().max()
+    w = torch.softmax(s, -1) * f
+    o, mag = w @ code, w @ code.abs()
+    return o, (2.0 ** -11 + 2 * d[:, None] + 2.0 ** -18) * mag + least * w.max(-1, keepdim=True).values * code.abs().sum(0)[None] \
+        + ref.U[dtype] * o.abs() + ref.tiny(dtype)
+
+
+# more than 16 rows a key head: tiles; 12 and 6: the two few-rows kernels
+@pytest.mark.parametrize("far", [20, 24, 28, 30, 33, 36, 44])
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("q_len, D, page", [([70, 33], 64, 32), ([70, 33], 128, 128), ([4, 3], 64, 16), ([2, 1], 128, 64)])
+def test_how_far_small_values_last(A, q_len, D, page, dtype, far):  # noqa: F811
+    """Values' pages 2^far apart, the large ones' codes zeros: small values are all there is.  They are as exact as others down
+    to 2^-21 of the largest weight times scale (few rows: 2^-28), and off by 2^-32 (2^-39) of that one below, whatever the
+    heads' type."""
+    x = inputs((q_len, [700, 290], 6, 2, D, True, 0, dtype, "", page, False), seed=920, spread=0.3)
+    least = 2.0 ** -39 if max(q_len) * 3 <= 16 else 2.0 ** -32
+    for b, n in enumerate([700, 290]):
+        for j in range(-(-n // page)):
+            p = int(x["block_table"][b, j])
+            x["v_scales"][p] *= 8.0 if j % 2 == 0 else 8.0 * 2.0 ** -far
+            if j % 2 == 0:
+                x["v_cache"].view(torch.uint8)[p] = 0
+    x["v_scales"] *= 2.0 ** (far // 2)                       # fp16 outputs hold them
+    x["v_scales"].clamp_(max=2.0 ** 48)
+    out, _ = attend(A, x)
+    for b in range(2):
+        for i in {0, q_len[b] // 2, q_len[b] - 1}:
+            for h in range(2):
+                want, tol = token_rows(x, b, i, h, least)
+                within(out[int(x["cu_q"][b]) + i, 3 * h:3 * h + 3], want.cpu(), tol.cpu(), f"{b} {i} {h}")
