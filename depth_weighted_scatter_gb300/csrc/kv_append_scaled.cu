@@ -180,9 +180,11 @@ struct TurnTable {             // of the pairs, in shared memory
     int32_t axis[128 / 2];
 };
 
-// cos and sin of position * inv_freq, off by 2^-21 at most: the angle, reduced exactly
-// (rotary.cuh), goes to the hardware's functions.  (sincospif's last three bits cost
-// as much as ten heads' rows where a group has few heads.)
+// cos and sin of position * inv_freq, off by 2^-20 at most: the angle, reduced exactly
+// (rotary.cuh), goes to the hardware's functions.  They are off by up to 2^-21.19 in
+// [-pi, pi]; the angle by 2^-23.3 (64 of 2^31 half turns, of its conversion), 2^-23 (its
+// product) and 2^-23.5 (its factor).  (sincospif's last four bits cost as much as ten
+// heads' rows where a group has few heads.)
 __device__ __forceinline__ float2 cos_sin_fast(unsigned long long turns, int32_t pos) {
     const uint32_t top = static_cast<uint32_t>((turns * static_cast<unsigned long long>(static_cast<long long>(pos))) >> 32);
     const float angle = static_cast<float>(static_cast<int32_t>(top)) * 1.4629180792671596e-9f;      // pi 2^-31

@@ -98,3 +98,28 @@ def test_how_far_small_values_last(A, q_len, D, page, dtype, far):  # noqa: F811
             for h in range(2):
                 want, tol = token_rows(x, b, i, h, least)
                 within(out[int(x["cu_q"][b]) + i, 3 * h:3 * h + 3], want.cpu(), tol.cpu(), f"{b} {i} {h}")
+
+
+@pytest.mark.parametrize("T, page", [(60, 16), (40000, 64), (40000, 256)])
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_angles_of_the_append(A, T, page, interleaved):  # noqa: F811
+    """cos and sin are off by 2^-20 at most.  Pairs (1, 0) come out as (cos, sin), rounded to fp16: by 2^-11 of them, which
+    for those below 2^-10 is half of the bound or less.  (The product of position and frequency, exact but for 2^-53 of
+    itself, adds 2^-29 below 2^24 radians.)"""
+    D = 64
+    seqs = 1 if T > 100 else T                               # few tokens a request: a warp a page and head
+    g = torch.Generator().manual_seed(T)
+    pos = torch.randint(-(1 << 24), 1 << 24, (T,), generator=g).to(torch.int32).cuda()
+    f = torch.rand(D // 2, generator=g).cuda()
+    q = torch.zeros(T, 1, D, dtype=F16, device="cuda")
+    first, second = (slice(0, D, 2), slice(1, D, 2)) if interleaved else (slice(0, D // 2), slice(D // 2, D))
+    q[..., first] = 1.0
+    pages = -(-(T // seqs) // page)
+    cache = [torch.zeros(seqs * pages, 1, page, D, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    scales = [torch.ones(seqs * pages, 1, device="cuda") for _ in range(2)]
+    table = torch.arange(seqs * pages, dtype=torch.int32, device="cuda").view(seqs, pages)
+    out = A.kv_append_scaled(q, q, *cache, *scales, table, i32([T // seqs] * seqs), cu_of([T // seqs] * seqs), pos, f, q=q, interleaved=interleaved)
+    cos, sin = ref.cos_sin(pos, f, [D // 2])
+    for got, want in ((out[:, 0, first], cos), (out[:, 0, second], sin)):
+        assert T < 100 or int((want.abs() < 2.0 ** -10).sum()) > 500
+        within(got, want, 2.0 ** -20 + 2.0 ** -11 * want.abs() + 2.0 ** -25 + 2.0 ** -29, "angles")
