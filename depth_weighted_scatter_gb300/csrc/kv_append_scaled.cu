@@ -24,8 +24,12 @@
 // cover what a head's rows wait for (a sum over lanes, a largest over warps) with each
 // other; 64 single tokens: 6.2 us a call, the launch and its call. The rows through
 // registers a head ahead instead of asynchronous copies: 74 and 51 us; sincospif for
-// the angles and factors anew for each head: 112 and 78.
+// the angles and factors anew for each head: 112 and 78.  Pages of 128 and 256, which are
+// read twice: the chunks 86 and 147 us (heads' split pairs, positions of one axis; 43 with
+// pages of 64), the frames 122 and 129 (69).
 //
+#include <algorithm>
+
 #include "rotary.cuh"
 
 namespace bevpool {
@@ -228,6 +232,10 @@ struct RowTurn {
     }
 };
 
+// Shared memory of an SM, and what a CTA takes of it besides the dynamic part (its
+// weights, its pairs, 1 KB of the system's).
+constexpr int kSmShared = 228 * 1024, kFixedShared = 4 * 1024;
+
 // Heads whose rows are on their way: 32 KB a CTA where an SM holds three, 48 KB where
 // it holds two (one head more or less: 63 to 64 us and 47 to 56 of the cases below).
 constexpr int append_ahead(int steps) { return steps == 2 ? 4 : 3; }
@@ -240,8 +248,8 @@ k_append_scaled(ScaledAppendArgs a, int parts, int group_warps) {
     __shared__ __align__(16) RowWeights weights;
     __shared__ TurnTable table;
     __shared__ uint32_t tops[PAGES ? kWarps : 1][3];
-    extern __shared__ __align__(16) uint8_t dynamic[];     // pages: rows on their way; of several batches, their angles
-    float2 *angles = reinterpret_cast<float2 *>(dynamic + AHEAD * STEPS * kThreads * 16);       // [row][pair]
+    extern __shared__ __align__(16) uint8_t dynamic[];     // pages: rows on their way; of several batches, their angles instead
+    float2 *angles = reinterpret_cast<float2 *>(dynamic);  // [row][pair]
     const NormRopeArgs &f = a.g.f;
     const PagedArgs &pg = a.g.pg;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, rg = lane / LPR;
@@ -561,12 +569,14 @@ cudaError_t launch_append_scaled(const ScaledAppendArgs &a) {
             group_warps = pg.page_size >= 64 ? 8 : pg.page_size / 8;       // 64 rows at most
             const int groups = kWarps / group_warps;
             const int64_t full = f.T >> pg.page_shift, places = full + 2 * (static_cast<int64_t>(pg.n_seqs) + 1), pages = full + pg.n_seqs;
-            parts = append_parts(pages, jobs, groups, 152 * (STEPS == 2 ? 3 : 2));
-            grid = places * parts;
-            constexpr int ring = append_ahead(STEPS) * STEPS * kThreads * 16;
+            // a CTA has the rows on their way or its angles in shared memory, never both
+            constexpr int ring = append_ahead(STEPS) * STEPS * kThreads * 16, most = 256 * (LPR * 4) * static_cast<int>(sizeof(float2));
             smem = ring;
-            if (pg.page_size > 64) smem += pg.page_size * (f.rot.rotary_dim / 2) * static_cast<int>(sizeof(float2));
-            const cudaError_t e = allow_smem<&k_append_scaled<decltype(t), LPR, IL, PAGES, STEPS>>(ring + 256 * (LPR * 4) * static_cast<int>(sizeof(float2)));
+            if (pg.page_size > 64) smem = std::max(smem, pg.page_size * (f.rot.rotary_dim / 2) * static_cast<int>(sizeof(float2)));
+            const int held = std::min(STEPS == 2 ? 3 : 2, kSmShared / (smem + kFixedShared));      // CTAs of an SM
+            parts = append_parts(pages, jobs, groups, 152 * held);
+            grid = places * parts;
+            const cudaError_t e = allow_smem<&k_append_scaled<decltype(t), LPR, IL, PAGES, STEPS>>(std::max(ring, most));
             if (e != cudaSuccess) return e;
         } else {
             grid = div_up(static_cast<int64_t>(f.T) * jobs, kWarps);

@@ -5,7 +5,7 @@ import pytest
 import scaled_ref as sref
 import token_ref as ref
 from test_scaled_attention_gpu import A, BF16, F16, NAMES, attend, check, check_rows, inputs  # noqa: F401
-from test_token_ops_gpu import cu_of, freqs, i32, rand, within
+from test_token_ops_gpu import cu_of, freqs, i32, make_pages, positions_of, rand, within
 
 pytestmark = pytest.mark.gpu
 
@@ -123,3 +123,26 @@ def test_angles_of_the_append(A, T, page, interleaved):  # noqa: F811
     for got, want in ((out[:, 0, first], cos), (out[:, 0, second], sin)):
         assert T < 100 or int((want.abs() < 2.0 ** -10).sum()) > 500
         within(got, want, 2.0 ** -20 + 2.0 ** -11 * want.abs() + 2.0 ** -25 + 2.0 ** -29, "angles")
+
+
+@pytest.mark.parametrize("page, D, Hq, Hk", [(128, 64, 8, 8), (256, 64, 3, 2), (128, 128, 32, 8), (256, 128, 5, 1)])
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_long_pages_in_part_and_whole(A, page, D, Hq, Hk, interleaved):  # noqa: F811
+    """Pages of which a call fills a few slots, as many as a group has rows, and all: the first two have their rows on their
+    way in shared memory, the last their angles, in one launch."""
+    q_len, kv_len = [64, page, 2 * page + 3, 65, 1, 7 * page], [64, page, 3 * page + 1, page + 1, 40, 7 * page]
+    T, dtype = sum(q_len), BF16 if D == 128 else F16
+    kc, vc, table = make_pages(1, kv_len, page, Hk, D, dtype, "e4m3")
+    ks, vs = (torch.exp(rand(8 + i, kc.shape[0], Hk)) / 100 for i in range(2))
+    before = [(c.float().cpu().double(), s.cpu().clone()) for c, s in ((kc, ks), (vc, vs))]
+    qkv, pos, f, w = rand(2, T, Hq + 2 * Hk, D, dtype=dtype), positions_of(3, T, 1), freqs(D), 1 + 0.2 * rand(4, D)
+    q, k, v = qkv[:, :Hq], qkv[:, Hq:Hq + Hk], qkv[:, Hq + Hk:]
+    q_out = A.kv_append_scaled(k, v, kc, vc, ks, vs, table, i32(kv_len), cu_of(q_len), pos, f, interleaved=interleaved, q=q, q_weight=w, k_weight=w)
+    cos, sin = ref.cos_sin(pos, f, [D // 2])
+    want, mag = ref.norm_rope(q, w, cos, sin, interleaved, 1e-6)
+    within(q_out, want, ref.U[dtype] * want.abs() + 2.0 ** -18 * mag + ref.tiny(dtype), "q")
+    want_k, mag = ref.norm_rope(k, w, cos, sin, interleaved, 1e-6)
+    runs = sref.page_runs(cu_of(q_len).cpu().numpy(), kv_len, table.cpu().numpy(), page, kc.shape[0])
+    x = v.cpu().double()
+    sref.check_append(runs, want_k, 2.0 ** -18 * mag, *before[0], kc.float().cpu().double(), ks.cpu(), False, "k")
+    sref.check_append(runs, x, torch.zeros_like(x), *before[1], vc.float().cpu().double(), vs.cpu(), True, "v")
