@@ -243,8 +243,10 @@ def plan_pages(q_len, kv_len, first, block_table, free_pages, n_free, *, page_si
     paged_attention take them, each new token's position and slot.  All tensors
     int32 (slots int64); n_tokens is a host bound of the new tokens; drop: oldest
     pages that a request gives back first, negative: it ends.  With missing != 0
-    nothing has changed.  `out`: an earlier plan's tensors to write to, none of
-    which this call reads."""
+    nothing has changed and cu_q is 0 throughout: an append with it puts nothing
+    into the cache, an attention computes no rows, so a program looks at it before
+    it uses them.  `out`: an earlier plan's tensors to write to, none of which this
+    call reads."""
     if stream is not None:
         with _stream_of(stream):
             return PagePlan._make(_ops.plan_pages(q_len, kv_len, first, drop, block_table, free_pages, n_free, page_size, n_tokens, out))

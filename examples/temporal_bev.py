@@ -104,11 +104,17 @@ class PlannedAttention(TemporalAttention):
     def step(self, bevs, drive):
         """A frame of the vehicles that drive (a truth value each; bevs: their cells, one after the other).
         -> [cells of those that drive, heads, head_dim]"""
+        if len(bevs) != sum(map(bool, drive)) * self.cells:
+            raise ValueError(f"{len(bevs)} cells for {sum(map(bool, drive))} vehicles of {self.cells}")
         q, k, v = (bevs @ self.project).view(-1, self.H + 2 * self.Hk, self.D).split([self.H, self.Hk, self.Hk], dim=1)
-        on = torch.tensor(drive, dtype=torch.int32, device="cuda")
+        on = torch.tensor([bool(x) for x in drive], dtype=torch.int32, device="cuda")
         # a vehicle whose cache is full gives its oldest frame's pages back first
         drop = on * (self.state[0] >= self.frames * self.cells).to(torch.int32) * self.pages
         plan = attention.plan_pages(on * self.cells, *self.state, page_size=PAGE, n_tokens=len(bevs), drop=drop)
+        # a plan that does not fit changes nothing and names no tokens: nothing would be attended
+        missing = plan.missing.item()
+        if missing:
+            raise RuntimeError(f"{missing} pages too few for this frame" if missing > 0 else "a vehicle's frames do not fit its pages")
         self.state = [plan.kv_len, plan.first, plan.block_table, plan.free_pages, plan.n_free]
         # token i of a vehicle is cell i % cells of frame i // cells
         at = plan.positions
