@@ -242,8 +242,9 @@ def plan_pages(q_len, kv_len, first, block_table, free_pages, n_free, *, page_si
     request, on the device: cu_q, kv_len and block_table as kv_append and
     paged_attention take them, each new token's position and slot.  All tensors
     int32 (slots int64); n_tokens is a host bound of the new tokens; drop: oldest
-    pages that a request gives back first, negative: it ends.  With missing != 0
-    nothing has changed and cu_q is 0 throughout: an append with it puts nothing
+    pages that a request gives back first, negative: it ends.  Pages that requests
+    share are not for planning: each request would give them back.  With missing !=
+    0 nothing has changed and cu_q is 0 throughout: an append with it puts nothing
     into the cache, an attention computes no rows, so a program looks at it before
     it uses them.  `out`: an earlier plan's tensors to write to, none of which this
     call reads."""

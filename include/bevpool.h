@@ -508,8 +508,10 @@ BEVPOOL_API bevpool_status bevpool_qk_norm_rope_backward(
  *   free_pages       device int32 [n_pool], as its output;  n_free: device int32 [1];
  *   n_seqs           0 .. 16384;  page_size: a power of two in [16, 256];
  *   n_tokens         host bound of the new tokens.
- * Outputs must not overlap inputs or each other.  Page numbers are passed on,
- * not looked at.
+ * Outputs must not overlap inputs or each other.  Page numbers are passed on, not
+ * looked at: a page is named once, by a request's table or on the stack.  (One that
+ * several requests name, as the append and the attention allow of full pages, is
+ * given back by each of them and handed out as often.)
  */
 BEVPOOL_API bevpool_status bevpool_plan_pages(
     const int32_t *q_len, const int32_t *kv_len, const int32_t *first, const int32_t *drop, const int32_t *block_table,
