@@ -146,3 +146,65 @@ def test_long_pages_in_part_and_whole(A, page, D, Hq, Hk, interleaved):  # noqa:
     x = v.cpu().double()
     sref.check_append(runs, want_k, 2.0 ** -18 * mag, *before[0], kc.float().cpu().double(), ks.cpu(), False, "k")
     sref.check_append(runs, x, torch.zeros_like(x), *before[1], vc.float().cpu().double(), vs.cpu(), True, "v")
+
+
+FAR_PAGES, FAR_HEADS, FAR_PAGE, FAR_D = 2200, 16, 256, 128
+FAR = [3, FAR_PAGES - 1, FAR_PAGES - 2, 1, FAR_PAGES - 3]   # pages that the tests use
+
+
+@pytest.fixture(scope="module")
+def far():
+    """Caches of codes whose pages are 2 MB apart, the last ones past 2^32 bytes."""
+    caches = [torch.zeros(FAR_PAGES, FAR_HEADS, 4 * FAR_PAGE, FAR_D, dtype=torch.uint8, device="cuda")[:, :, :FAR_PAGE] for _ in range(2)]
+    assert caches[0].stride(0) * FAR[4] > 2 ** 32
+    return caches
+
+
+def near(seed):
+    """Codes and scales of five pages."""
+    codes = rand(seed, 5, FAR_HEADS, FAR_PAGE, FAR_D, scale=30.0).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+    return codes, torch.exp(0.3 * rand(seed + 1, 5, FAR_HEADS)) / 4000
+
+
+def placed(far, codes, scales):
+    """Those pages in the wide caches, and their scales among all."""
+    for cache, c in zip(far, codes):
+        for i, p in enumerate(FAR):
+            cache[p] = c[i]
+    res = [torch.ones(FAR_PAGES, FAR_HEADS, device="cuda") for _ in range(2)]
+    for all_, s in zip(res, scales):
+        all_[FAR] = s
+    return far, res
+
+
+def table_of(pages):
+    return i32([pages[:3], pages[3:] + [-1]])
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("q_len, G", [([1, 3], 1), ([1, 6], 2), ([1, 40], 1)], ids=["codes", "few", "tiles"])
+def test_attention_over_pages_past_32_bits(A, far, q_len, G, dtype):  # noqa: F811
+    """Each of the three kernels: the bits of the same codes in a small cache."""
+    codes, scales = zip(near(1), near(3))
+    wide, wide_scales = placed(far, codes, scales)
+    q, kv_len = rand(5, sum(q_len), FAR_HEADS * G, FAR_D, dtype=dtype), i32([700, 300])
+    args = dict(max_q_len=max(q_len), max_kv_len=700, return_lse=True)
+    got = A.paged_attention_scaled(q, *wide, *wide_scales, table_of(FAR), kv_len, cu_of(q_len), **args)
+    want = A.paged_attention_scaled(q, *codes, *scales, table_of([0, 1, 2, 3, 4]), kv_len, cu_of(q_len), **args)
+    assert all(torch.equal(a, b) for a, b in zip(got, want)) and got[0].abs().amax() > 0
+
+
+@pytest.mark.parametrize("q_len, kv_len", [([2, 1], [514, 300]), ([200, 20], [700, 290]), ([300, 20], [700, 290])],
+                         ids=["tokens", "pages", "pages read twice"])
+def test_append_to_pages_past_32_bits(A, far, q_len, kv_len):  # noqa: F811
+    """Pages that hold tokens and whose scales grow among them: the codes and scales of the same append to a small cache."""
+    T, f, pos = sum(q_len), freqs(FAR_D), positions_of(8, sum(q_len), 1)
+    k, v = (rand(6 + i, T, FAR_HEADS, FAR_D, dtype=F16) for i in range(2))
+    codes, scales = zip(near(1), near(3))
+    wide, wide_scales = placed(far, codes, scales)
+    before = [s.clone() for s in scales]
+    A.kv_append_scaled(k, v, *wide, *wide_scales, table_of(FAR), i32(kv_len), cu_of(q_len), pos, f)
+    A.kv_append_scaled(k, v, *codes, *scales, table_of([0, 1, 2, 3, 4]), i32(kv_len), cu_of(q_len), pos, f)
+    for a, b, c, d, was in zip(wide, codes, wide_scales, scales, before):
+        assert torch.equal(a[FAR], b) and torch.equal(c[FAR], d)
+        assert (d[4] / was[4]).log2().amax() >= 1           # the last page, past 2^32 bytes, holds tokens and has grown
