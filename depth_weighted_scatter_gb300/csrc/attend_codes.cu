@@ -20,11 +20,11 @@
 //
 // Measured on a GB300, 32 query and 8 key heads of 128, bf16: 64 requests of up to 8192
 // keys, pages of 16: 137 us (5.6 TB/s, 82 % of measured copy; the few-rows kernel 154);
-// two requests of up to 131072 keys, pages of 64: 82 us (5.0 TB/s, 74 %; 94): what is
-// left is mostly a CTA's start (four lookups that wait for each other) and the join;
-// one request of 777 keys, 8 heads of 64: 10.5 to 12 us a call (13.5).  Two CTAs an SM
-// with three tiles a ring instead of three with two: 144 and 91 us; four with tiles of
-// 2 KB: 142 and 85.
+// two requests of up to 131072 keys, pages of 64: 76 us (5.4 TB/s, 80 %; 94): what is
+// left is mostly a CTA's start (four lookups that wait for each other), the shorter
+// request's idle places and the join; one request of 777 keys, 8 heads of 64: 10.5 to 12.5
+// us a call (13.5).  Two CTAs an SM with three tiles a ring instead of three with two:
+// 144 and 91 us where these took 137 and 86; four with tiles of 2 KB: 142 and 85.
 #include "tcgen05.cuh"
 #include "tensor_map.cuh"
 #include "warp_mma.cuh"

@@ -9,21 +9,31 @@ namespace bevpool {
 
 namespace {
 
-// CTAs that a few-rows call's chunks make of its longest requests.  An SM holds
-// two, so a multiple w of 304: each wave costs its start, about 4 us, while w
-// waves leave about 1 / (2 w) of the time t of the read to ragged lengths, so w
-// is near sqrt(t / 8 us); a lone request is not ragged.  Measured with w = 1 /
-// 2 / 4 / 8: one request of 40000 keys (8 key heads of 128, bf16) - / 41 / 49 /
-// 55 us, 64 of up to 8192 - / 248 / 240 / 236 us.  Over codes with page scales an SM
-// holds three; the same rule (bytes are half there): 64 of up to 8192 keys 137 us, 138
-// and 139 with w smaller by 1.4 and 2; two of up to 131072 86 with w = 4, 82 with 2.
-int64_t few_ctas(int64_t keys, int64_t pairs, int32_t n_seqs, int32_t D, bool codes) {
+// Chunks of a few-rows call's requests, from the CTAs that those of its longest ones
+// make.  An SM holds two, so these are a multiple w of 304: each wave costs its start,
+// about 4 us, while w waves leave about 1 / (2 w) of the time t of the read to ragged
+// lengths, so w is near sqrt(t / 8 us); a lone request is not ragged.  Measured with w =
+// 1 / 2 / 4 / 8: one request of 40000 keys (8 key heads of 128, bf16) - / 41 / 49 /
+// 55 us, 64 of up to 8192 - / 248 / 240 / 236 us.
+//
+// Over codes with page scales an SM holds three.  Up to 64 pairs of a request and key
+// head, which have seven chunks each or more, all CTAs are at work at once: ragged
+// lengths then cost less than a second wave's start, and one that is begun for a few
+// CTAs costs most, so the chunks are rounded down.  Measured with w = 1 / 2 / 4, 8 key
+// heads of 128, lengths ragged and equal: 2 requests of 131072 keys 76 / 83 / 86 and 90 /
+// 94 / 101 us (29 chunks each, 464 CTAs, for 28: 114); 4 of 32768 45 / 50 / 50 and 53 /
+// 54 / 59; 8 of 32768 77 / 83 / 77 and 92 / 91 / 97.  Beyond, the rule above: 12 of 32768
+// 120 / 110 / 112 and 129 / 148 / 136, 32 of 16384 161 / 134 / 134 and 175 / 186 / 169,
+// 64 of 8192 153 / 135 / 135 and 212 / 186 / 177.
+int64_t few_chunks(int64_t keys, int64_t pairs, int32_t n_seqs, int32_t D, bool codes) {
     const int64_t wave = 152 * (codes ? kCodesCtas : 2);
-    if (n_seqs == 1) return wave;
-    const double t = static_cast<double>(keys) * static_cast<double>(pairs) * D * 4 / 6.7e6;      // us, 16-bit cache
-    int64_t w = static_cast<int64_t>(std::sqrt(t / 8) + 0.5);
-    if (codes && w > n_seqs) w = n_seqs;                   // few requests leave few ragged ends
-    return wave * (w < 1 ? 1 : w > 6 ? 6 : w);
+    if (codes && pairs <= 64) return wave / pairs;
+    int64_t w = 1;
+    if (n_seqs > 1) {
+        const double t = static_cast<double>(keys) * static_cast<double>(pairs) * D * 4 / 6.7e6;  // us, 16-bit cache
+        w = std::min<int64_t>(std::max<int64_t>(static_cast<int64_t>(std::sqrt(t / 8) + 0.5), 1), 6);
+    }
+    return (wave * w + pairs / 2) / pairs;
 }
 
 constexpr int32_t kSms = 152;
@@ -95,7 +105,7 @@ AttnPlan attention_plan(const AttnSizes &z) {
     const int64_t keys = keys_of(q_len, z.max_kv_len, z.window, pl.align), pairs = static_cast<int64_t>(z.n_seqs) * z.Hk;
     int64_t n = 1;
     if (pl.few) {
-        if (pairs > 0) n = (few_ctas(keys, pairs, z.n_seqs, z.D, pl.codes) + pairs / 2) / pairs;
+        if (pairs > 0) n = few_chunks(keys, pairs, z.n_seqs, z.D, pl.codes);
     } else {
         bool share;
         pl.tiles = static_cast<int32_t>(div_up(pl.rows, kPairRows));
