@@ -164,8 +164,10 @@ __device__ __forceinline__ float largest(float m, const uint64_t *y) {
 // CTAs a page: its heads are shared out so that the waves of CTAs (slots: what the
 // GPU holds at a time) take least, a CTA costing what its heads' rows cost and about
 // kSetUp heads besides (its request, its rows' angles).  Measured with 1 / 2 / 3 / 4 / 5
-// parts, before the rows came by asynchronous copies: 1024 pages of 24 heads 74 / 77 /
-// 74 / 80 / 85 us, 104 of 48 heads 78 / 52 / 65 / 55 / 52.
+// parts, nothing in L2: 1024 pages of 64 slots and 24 heads of 64 76 / 76 / 79 / 83 / 89
+// us, 104 of 48 heads of 128 60 / 48 / 56 / 50 / 48; the same tokens over pages of 128
+// slots 128 / 132 / 152 / 140 / 146 and 232 / 140 / 124 / 95 / 89, of 256 203 / 133 / 181 /
+// 152 / 158 and 443 / 263 / 199 / 148 / 181.  Taken: 1, 2; 1, 5; 2, 4.
 int64_t append_parts(int64_t pages, int jobs, int groups, int64_t slots) {
     constexpr int64_t kSetUp = 4, kMost = 4096;
     int64_t best = 1, least = INT64_MAX;
@@ -587,6 +589,12 @@ cudaError_t launch_append_scaled(const ScaledAppendArgs &a) {
         count_launch();
         return cudaGetLastError();
     };
+    // A warp a page and head or a CTA a page, by the tokens of a request on average (the
+    // host knows no more).  Measured with 1 / 2 / 4 / 6 / 8 tokens for each of 64 requests, 48
+    // heads: 128 elements, pages of 64: 5 / 7 / 12 / 17 / 21 us and 21 to 22; of 16: the same
+    // and 11 to 13; 64 elements, pages of 64: 5 / 7 / 9 / 15 / 17 and 16.  A chunk of 190
+    // tokens beside 63 single ones, which the average hides, takes 42 us for 22 (64 elements:
+    // 23 for 16).
     const auto by_group = [&](auto t, auto lpr, auto il) {
         return f.T <= 4 * static_cast<int64_t>(pg.n_seqs) ? run(t, lpr, il, std::false_type{}) : run(t, lpr, il, std::true_type{});
     };
