@@ -304,8 +304,9 @@ __device__ __forceinline__ void init_bars(TileBars &bars, bool again) {
 // the inverse, 2^(e - 14), times the least factor of a key's score, scale_log2 * 2^-48,
 // is 2^-126 or more, so that the product is never 0 and a masked score never 0 * -inf.
 // (NaN there meant that padded rows were taken again key by key: 2000 tokens of zeros,
-// 8 heads of 128, 11.5 ms for 0.045.)  A row below it gives up bits of fp16 instead: at most 2^-25 *
-// 2^(e - 14) an element, which is 2^-38 of a score under the largest scale.
+// 8 heads of 128, 11.5 ms for 0.045.)  A row below it gives up bits of fp16 instead: at
+// most 2^-25 * 2^(e - 14) an element, which adds up to 2^-38 in a score under the
+// largest scale of a page.
 __device__ __forceinline__ int least_exponent(float scale_log2) {
     const int x = static_cast<int>(__float_as_uint(scale_log2) >> 23) - 127 - 48;          // of the least factor; -126 or more
     return max(-112, -112 - x);

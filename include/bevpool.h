@@ -640,8 +640,8 @@ BEVPOOL_API size_t bevpool_paged_attention_scaled_workspace_size(int32_t n_seqs,
  *   scale               2^-78 or more, scale * 2^48 finite.
  * The weights are rounded to fp16, whatever the heads' type, with their value's scale
  * in them: relatively, so that pages of small values lose no more than others, down to
- * 2^-28 of the largest weight times scale that a token sees (2^-21 where a request and
- * key head has more than 16 query rows), and by 2^-39 (2^-32) of that one below.
+ * 2^-28 of the largest weight times scale that a token sees (2^-21 where max_q_len tokens
+ * are more than 16 query rows a key head), and by 2^-39 (2^-32) of that one below.
  * Other arguments are those of bevpool_paged_attention.
  */
 BEVPOOL_API bevpool_status bevpool_paged_attention_scaled(
